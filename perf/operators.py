@@ -156,7 +156,8 @@ def _held(y, fmt):
     d16 = d.half()
     r = torch.where(d16 == 0, torch.zeros_like(d), 1 / d)
     t = b * r
-    q = torch.copysign(torch.floor(t.abs() + 0.5), t).clamp(-127, 127)
+    w = torch.trunc(t)
+    q = torch.where((t - w).abs() >= 0.5, w + torch.sign(t), w).clamp(-127, 127)
     return (q * d16.float()).reshape(y.shape)
 
 
