@@ -23,6 +23,10 @@ IQ4_E_HIP = -4
 IQ4_E_WORKSPACE = -5
 IQ4_F32 = 0
 IQ4_F16 = 1
+IQ4_BF16 = 2
+IQ4_ROWS_MXFP4 = 0
+IQ4_ROWS_MXFP8 = 1
+IQ4_ROWS_Q8_1 = 2
 IQ4_MOE_ATOMIC_COMBINE = 1
 IQ4_MOE_KEEP_INTERMEDIATE = 2
 # iq4_moe_intermediate_layout indices
@@ -30,6 +34,7 @@ MOE_LAYOUT = {"total": 0, "counts": 1, "offsets": 2, "pairs": 3, "slot_row": 4, 
 IQ4_QMV_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 _c_i64, _c_i32, _c_u32, _c_p, _c_sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_size_t
+_c_f32 = ctypes.c_float
 
 # name -> (restype, argtypes) exactly as declared in include/iq4.h
 SIGNATURES = {
@@ -63,6 +68,19 @@ SIGNATURES = {
                                                   _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
                                                   _c_i64, _c_p, _c_sz, _c_u32, _c_p]),
     "iq4_qgemm": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p]),
+    "iq4_rows_bytes": (ctypes.c_int, [_c_i32, _c_i64, ctypes.POINTER(_c_i64), ctypes.POINTER(_c_i64)]),
+    "iq4_quantize_rows": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_i32, _c_p, _c_i64, _c_p, _c_i64,
+                                         _c_p]),
+    "iq4_dequant_rows": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i32, _c_i64, _c_i64, _c_i32, _c_p, _c_i64,
+                                        _c_p]),
+    "iq4_rmsnorm": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i32, _c_i64, _c_i64, _c_p, _c_f32, _c_p, _c_i64,
+                                   _c_p, _c_i32, _c_i64, _c_i32, _c_p, _c_i64, _c_p, _c_i64, _c_p]),
+    "iq4_mx_packed_bytes": (_c_i64, [_c_i64, _c_i64]),
+    "iq4_mx_pack_weights": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p]),
+    "iq4_mx_gemm": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i32, _c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_i32,
+                                   _c_i64, _c_p]),
+    "iq4_mx_grouped_gemm": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i32, _c_p, _c_i64, _c_p, _c_i64, _c_i64,
+                                           _c_p, _c_p, _c_i32, _c_i64, _c_p, _c_i32, _c_i64, _c_p]),
 }
 
 _lib = None
@@ -218,3 +236,45 @@ def iq4_moe_expert_gemm_shared(x, act_dtype, n_tok, ldx, ids, w, top_k, n_expert
 
 def iq4_qgemm(packed, n, k, x, m, ldx, y, ldy, chunk, stream=None):
     _call("iq4_qgemm", _ptr(packed), n, k, _ptr(x), m, ldx, _ptr(y), ldy, chunk, _stream(stream))
+
+
+def iq4_rows_bytes(fmt, k) -> tuple:
+    """Bytes of one row's codes and of its scales (the least ``ldq`` and ``lds``)."""
+    c, d = _c_i64(0), _c_i64(0)
+    _call("iq4_rows_bytes", fmt, k, ctypes.byref(c), ctypes.byref(d))
+    return c.value, d.value
+
+
+def iq4_quantize_rows(x, x_dtype, m, k, ldx, fmt, codes, ldq, scales, lds, stream=None):
+    _call("iq4_quantize_rows", _ptr(x), x_dtype, m, k, ldx, fmt, _ptr(codes), ldq, _ptr(scales), lds,
+          _stream(stream))
+
+
+def iq4_dequant_rows(codes, ldq, scales, lds, fmt, m, k, out_dtype, out, ldo, stream=None):
+    _call("iq4_dequant_rows", _ptr(codes), ldq, _ptr(scales), lds, fmt, m, k, out_dtype, _ptr(out), ldo,
+          _stream(stream))
+
+
+def iq4_rmsnorm(x, ldx, res, ldr, dtype, m, k, gain, eps, h, ldh, y, y_dtype, ldy, fmt=IQ4_ROWS_Q8_1, codes=None,
+                ldq=0, scales=None, lds=0, stream=None):
+    _call("iq4_rmsnorm", _ptr(x), ldx, _ptr(res), ldr, dtype, m, k, _ptr(gain), eps, _ptr(h), ldh, _ptr(y), y_dtype,
+          ldy, fmt, _ptr(codes), ldq, _ptr(scales), lds, _stream(stream))
+
+
+def iq4_mx_packed_bytes(n, k) -> int:
+    return lib().iq4_mx_packed_bytes(n, k)
+
+
+def iq4_mx_pack_weights(codes, ldq, scales, lds, n, k, packed, stream=None):
+    _call("iq4_mx_pack_weights", _ptr(codes), ldq, _ptr(scales), lds, n, k, _ptr(packed), _stream(stream))
+
+
+def iq4_mx_gemm(packed, n, k, fmt, codes, ldq, scales, lds, m, y, y_dtype, ldy, stream=None):
+    _call("iq4_mx_gemm", _ptr(packed), n, k, fmt, _ptr(codes), ldq, _ptr(scales), lds, m, _ptr(y), y_dtype, ldy,
+          _stream(stream))
+
+
+def iq4_mx_grouped_gemm(packed, n_expert, n, k, fmt, codes, ldq, scales, lds, n_rows, offsets, pairs, top_k, n_pairs,
+                        y, y_dtype, ldy, stream=None):
+    _call("iq4_mx_grouped_gemm", _ptr(packed), n_expert, n, k, fmt, _ptr(codes), ldq, _ptr(scales), lds, n_rows,
+          _ptr(offsets), _ptr(pairs), top_k, n_pairs, _ptr(y), y_dtype, ldy, _stream(stream))

@@ -10,6 +10,8 @@
 #include "qmv.hpp"
 #include "gemm.hpp"
 #include "moe.hpp"
+#include "mx.hpp"
+#include "rows.hpp"
 
 namespace iq4 {
 
@@ -384,6 +386,237 @@ int iq4_xs_qmv_multi(const void* w, int64_t n, int64_t k, const float* x, int64_
     return set_error(IQ4_E_ALIGN, "iq4_xs_qmv_multi: w must be 8-byte, x 16-byte (ldx % 4 == 0) and y 4-byte "
                      "aligned");
   return launch_xs_qmv(w, n, k, x, ldx, T, y, ldy, as_stream(stream));
+}
+
+// ---- rows in 8 or 4 bits, the norm that makes them, products on them ----------------
+
+static int check_rows_format(const char* fn, int32_t fmt, int64_t m, int64_t k) {
+  if (fmt != IQ4_ROWS_MXFP4 && fmt != IQ4_ROWS_MXFP8 && fmt != IQ4_ROWS_Q8_1)
+    return set_error(IQ4_E_ARG, "%s: fmt must be IQ4_ROWS_MXFP4, IQ4_ROWS_MXFP8 or IQ4_ROWS_Q8_1", fn);
+  if (m < 0 || k <= 0) return set_error(IQ4_E_ARG, "%s: m must be >= 0 and k positive", fn);
+  if (k % kQK || k > ((int64_t)1 << 20) || m > ((int64_t)1 << 21) || m * k > ((int64_t)1 << 34))
+    return set_error(IQ4_E_UNSUPPORTED, "%s: k must be a multiple of 32, k <= 2^20, m <= 2^21, m * k <= 2^34 "
+                     "(m=%lld k=%lld)", fn, (long long)m, (long long)k);
+  return IQ4_OK;
+}
+
+// Strides and pointers of rows as the library writes them (codes may be null where the
+// caller allows it: then nothing is checked).
+static int check_rows(const char* fn, int32_t fmt, int64_t k, const void* codes, int64_t ldq, const void* scales,
+                      int64_t lds) {
+  if (ldq < rows_code_bytes(fmt, k) || lds < rows_scale_bytes(fmt, k))
+    return set_error(IQ4_E_ARG, "%s: ldq and lds must hold a row (iq4_rows_bytes: %lld and %lld bytes)", fn,
+                     (long long)rows_code_bytes(fmt, k), (long long)rows_scale_bytes(fmt, k));
+  if (!codes || !scales) return set_error(IQ4_E_ARG, "%s: null pointer", fn);
+  const int qa = fmt == IQ4_ROWS_Q8_1 ? 8 : 16, sa = fmt == IQ4_ROWS_Q8_1 ? 2 : 16;
+  if (!aligned(codes, qa) || ldq % qa || !aligned(scales, sa) || lds % sa)
+    return set_error(IQ4_E_ALIGN, "%s: codes and ldq must be %d-byte, scales and lds %d-byte aligned", fn, qa, sa);
+  return IQ4_OK;
+}
+
+static inline bool is_type(int32_t t) { return t == IQ4_F32 || t == IQ4_F16 || t == IQ4_BF16; }
+
+// A buffer of rows of floats: rows of 16-byte pieces.
+static int check_floats(const char* fn, const char* what, const void* p, int32_t type, int64_t k, int64_t ld) {
+  if (ld < k) return set_error(IQ4_E_ARG, "%s: the row stride of %s must be >= k", fn, what);
+  if (!aligned(p, 16) || ld % (type == IQ4_F32 ? 4 : 8))
+    return set_error(IQ4_E_ALIGN, "%s: rows of %s must be 16-byte aligned", fn, what);
+  return IQ4_OK;
+}
+
+int iq4_rows_bytes(int32_t fmt, int64_t k, int64_t* code_bytes, int64_t* scale_bytes) {
+  clear_error();
+  if (!code_bytes || !scale_bytes) return set_error(IQ4_E_ARG, "iq4_rows_bytes: null pointer");
+  if (int e = check_rows_format("iq4_rows_bytes", fmt, 0, k)) return e;
+  *code_bytes = rows_code_bytes(fmt, k);
+  *scale_bytes = rows_scale_bytes(fmt, k);
+  return IQ4_OK;
+}
+
+int iq4_quantize_rows(const void* x, int32_t x_dtype, int64_t m, int64_t k, int64_t ldx, int32_t fmt, void* codes,
+                      int64_t ldq, void* scales, int64_t lds, void* stream) {
+  const char* fn = "iq4_quantize_rows";
+  clear_error();
+  if (int e = check_rows_format(fn, fmt, m, k)) return e;
+  if (!is_type(x_dtype)) return set_error(IQ4_E_ARG, "%s: x_dtype must be IQ4_F32, IQ4_F16 or IQ4_BF16", fn);
+  if (m == 0) return IQ4_OK;
+  if (!x) return set_error(IQ4_E_ARG, "%s: null pointer", fn);
+  if (int e = check_floats(fn, "x", x, x_dtype, k, ldx)) return e;
+  if (int e = check_rows(fn, fmt, k, codes, ldq, scales, lds)) return e;
+  const RowsOut o{static_cast<uint8_t*>(codes), ldq, static_cast<uint8_t*>(scales), lds};
+  return launch_quantize_rows(x, x_dtype, m, k, ldx, fmt, o, as_stream(stream));
+}
+
+int iq4_dequant_rows(const void* codes, int64_t ldq, const void* scales, int64_t lds, int32_t fmt, int64_t m,
+                     int64_t k, int32_t out_dtype, void* out, int64_t ldo, void* stream) {
+  const char* fn = "iq4_dequant_rows";
+  clear_error();
+  if (int e = check_rows_format(fn, fmt, m, k)) return e;
+  if (!is_type(out_dtype)) return set_error(IQ4_E_ARG, "%s: out_dtype must be IQ4_F32, IQ4_F16 or IQ4_BF16", fn);
+  if (m == 0) return IQ4_OK;
+  if (!out) return set_error(IQ4_E_ARG, "%s: null pointer", fn);
+  if (int e = check_floats(fn, "out", out, out_dtype, k, ldo)) return e;
+  if (int e = check_rows(fn, fmt, k, codes, ldq, scales, lds)) return e;
+  const RowsIn in{static_cast<const uint8_t*>(codes), ldq, static_cast<const uint8_t*>(scales), lds};
+  return launch_dequant_rows(in, fmt, m, k, out_dtype, out, ldo, as_stream(stream));
+}
+
+int iq4_rmsnorm(const void* x, int64_t ldx, const void* res, int64_t ldr, int32_t dtype, int64_t m, int64_t k,
+                const float* gain, float eps, void* h, int64_t ldh, void* y, int32_t y_dtype, int64_t ldy,
+                int32_t fmt, void* codes, int64_t ldq, void* scales, int64_t lds, void* stream) {
+  const char* fn = "iq4_rmsnorm";
+  clear_error();
+  if (int e = check_rows_format(fn, codes ? fmt : IQ4_ROWS_Q8_1, m, k)) return e;
+  if (!is_type(dtype) || (y && !is_type(y_dtype)))
+    return set_error(IQ4_E_ARG, "%s: dtype and y_dtype must be IQ4_F32, IQ4_F16 or IQ4_BF16", fn);
+  if (!(eps >= 0.f) || eps > 3.0e38f) return set_error(IQ4_E_ARG, "%s: eps must be finite and >= 0", fn);
+  if (m == 0) return IQ4_OK;
+  if (!x || (!y && !codes)) return set_error(IQ4_E_ARG, "%s: null pointer (x, or both y and codes)", fn);
+  if (h && !res && h == x) return set_error(IQ4_E_ARG, "%s: h is x, and there is nothing to add", fn);
+  if (int e = check_floats(fn, "x", x, dtype, k, ldx)) return e;
+  if (res)
+    if (int e = check_floats(fn, "res", res, dtype, k, ldr)) return e;
+  if (h)
+    if (int e = check_floats(fn, "h", h, dtype, k, ldh)) return e;
+  if (y)
+    if (int e = check_floats(fn, "y", y, y_dtype, k, ldy)) return e;
+  if (codes)
+    if (int e = check_rows(fn, fmt, k, codes, ldq, scales, lds)) return e;
+  if (gain && !aligned(gain, 16)) return set_error(IQ4_E_ALIGN, "%s: gain must be 16-byte aligned", fn);
+  // the sum may be stored over an addend, row for row; any other overlap would be read after it is written
+  if (h && ((h == x && ldh != ldx) || (h == res && ldh != ldr)))
+    return set_error(IQ4_E_ARG, "%s: h stored over x or res needs the same row stride", fn);
+  NormArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.res = res;
+  a.ldr = ldr;
+  a.gain = gain;
+  a.eps = eps;
+  a.h = h;
+  a.ldh = ldh;
+  a.y = y;
+  a.y_type = y_dtype;
+  a.ldy = ldy;
+  a.fmt = codes ? fmt : -1;
+  a.o = RowsOut{static_cast<uint8_t*>(codes), ldq, static_cast<uint8_t*>(scales), lds};
+  a.m = m;
+  a.k = k;
+  return launch_rmsnorm(a, dtype, as_stream(stream));
+}
+
+static int check_mx_matrix(const char* fn, int64_t n, int64_t k) {
+  if (n <= 0 || k <= 0) return set_error(IQ4_E_ARG, "%s: n and k must be positive", fn);
+  if (k % kQK || k > ((int64_t)1 << 20) || n > ((int64_t)1 << 24))
+    return set_error(IQ4_E_UNSUPPORTED, "%s: k must be a multiple of 32, k <= 2^20, n <= 2^24 (n=%lld k=%lld)", fn,
+                     (long long)n, (long long)k);
+  return IQ4_OK;
+}
+
+int64_t iq4_mx_packed_bytes(int64_t n, int64_t k) {
+  if (n <= 0 || k <= 0 || k % kQK || k > ((int64_t)1 << 20) || n > ((int64_t)1 << 24)) return -1;
+  return mx_packed_bytes(n, k);
+}
+
+int iq4_mx_pack_weights(const void* codes, int64_t ldq, const void* scales, int64_t lds, int64_t n, int64_t k,
+                        void* packed, void* stream) {
+  const char* fn = "iq4_mx_pack_weights";
+  clear_error();
+  if (int e = check_mx_matrix(fn, n, k)) return e;
+  if (ldq < k / 2 || lds < k / kQK) return set_error(IQ4_E_ARG, "%s: ldq must be >= k / 2 and lds >= k / 32", fn);
+  if (!codes || !scales || !packed) return set_error(IQ4_E_ARG, "%s: null pointer", fn);
+  if (!aligned(packed, 256)) return set_error(IQ4_E_ALIGN, "%s: packed must be 256-byte aligned", fn);
+  if (mx_row_tiles(n) * mx_k_quads(k) * 64 >= ((int64_t)1 << 32) - 256)
+    return set_error(IQ4_E_UNSUPPORTED, "%s: n * k too large", fn);
+  const uint8_t* p = static_cast<const uint8_t*>(packed);
+  const uint8_t* c = static_cast<const uint8_t*>(codes);
+  const uint8_t* d = static_cast<const uint8_t*>(scales);
+  const int64_t bytes = mx_packed_bytes(n, k);
+  if ((c < p + bytes && p < c + (n - 1) * ldq + k / 2) || (d < p + bytes && p < d + (n - 1) * lds + k / kQK))
+    return set_error(IQ4_E_ARG, "%s: packed overlaps codes or scales", fn);
+  return launch_mx_pack(c, ldq, d, lds, n, k, static_cast<uint8_t*>(packed), as_stream(stream));
+}
+
+static int check_mx_product(const char* fn, const void* packed, int64_t n, int64_t k, int32_t fmt, const void* codes,
+                            int64_t ldq, const void* scales, int64_t lds, int64_t m, const void* y, int32_t y_dtype,
+                            int64_t ldy) {
+  if (ldy < n) return set_error(IQ4_E_ARG, "%s: ldy must be >= n", fn);
+  if (!packed || !y) return set_error(IQ4_E_ARG, "%s: null pointer", fn);
+  if (int e = check_rows(fn, fmt, k, codes, ldq, scales, lds)) return e;
+  if (!aligned(packed, 256) || !aligned(y, y_dtype == IQ4_F32 ? 4 : 2))
+    return set_error(IQ4_E_ALIGN, "%s: packed must be 256-byte and y element aligned", fn);
+  // the grid: a workgroup at least for each 16 weight rows and 16 output rows
+  if (mx_row_tiles(n) * ((m + 15) / 16 + 1024) >= (int64_t)1 << 22)
+    return set_error(IQ4_E_UNSUPPORTED, "%s: n * m too large (n=%lld m=%lld)", fn, (long long)n, (long long)m);
+  return IQ4_OK;
+}
+
+static int check_mx_args(const char* fn, int64_t n, int64_t k, int32_t fmt, int64_t m, int32_t y_dtype) {
+  if (int e = check_mx_matrix(fn, n, k)) return e;
+  if (fmt != IQ4_ROWS_MXFP4 && fmt != IQ4_ROWS_MXFP8)
+    return set_error(IQ4_E_ARG, "%s: fmt must be IQ4_ROWS_MXFP4 or IQ4_ROWS_MXFP8", fn);
+  if (!is_type(y_dtype)) return set_error(IQ4_E_ARG, "%s: y_dtype must be IQ4_F32, IQ4_F16 or IQ4_BF16", fn);
+  return check_rows_format(fn, fmt, m, k);
+}
+
+int iq4_mx_gemm(const void* packed, int64_t n, int64_t k, int32_t fmt, const void* codes, int64_t ldq,
+                const void* scales, int64_t lds, int64_t m, void* y, int32_t y_dtype, int64_t ldy, void* stream) {
+  const char* fn = "iq4_mx_gemm";
+  clear_error();
+  if (int e = check_mx_args(fn, n, k, fmt, m, y_dtype)) return e;
+  if (m == 0) return IQ4_OK;
+  if (int e = check_mx_product(fn, packed, n, k, fmt, codes, ldq, scales, lds, m, y, y_dtype, ldy)) return e;
+  MxArgs a{};
+  a.W = static_cast<const uint8_t*>(packed);
+  a.n = n;
+  a.k = k;
+  a.codes = static_cast<const uint8_t*>(codes);
+  a.ldq = ldq;
+  a.scales = static_cast<const uint8_t*>(scales);
+  a.lds = lds;
+  a.n_rows = a.m = m;
+  a.y = y;
+  a.y_type = y_dtype;
+  a.ldy = ldy;
+  return launch_mx_gemm(a, fmt, as_stream(stream));
+}
+
+int iq4_mx_grouped_gemm(const void* packed, int32_t n_expert, int64_t n, int64_t k, int32_t fmt, const void* codes,
+                        int64_t ldq, const void* scales, int64_t lds, int64_t n_rows, const int32_t* offsets,
+                        const int32_t* pairs, int32_t top_k, int64_t n_pairs, void* y, int32_t y_dtype, int64_t ldy,
+                        void* stream) {
+  const char* fn = "iq4_mx_grouped_gemm";
+  clear_error();
+  if (int e = check_mx_args(fn, n, k, fmt, n_pairs, y_dtype)) return e;
+  if (n_expert < 1 || n_expert > 1024) return set_error(IQ4_E_ARG, "%s: need 1 <= n_expert <= 1024", fn);
+  if (pairs && top_k < 1) return set_error(IQ4_E_ARG, "%s: top_k must be >= 1", fn);
+  if (n_rows < 0) return set_error(IQ4_E_ARG, "%s: n_rows must be >= 0", fn);
+  if (n_pairs == 0) return IQ4_OK;
+  if (pairs ? n_rows * (int64_t)top_k < n_pairs : n_rows < n_pairs)
+    return set_error(IQ4_E_ARG, "%s: n_rows (times top_k, with pairs) must be >= n_pairs", fn);
+  if (!offsets) return set_error(IQ4_E_ARG, "%s: null pointer", fn);
+  if (!aligned(offsets, 4) || !aligned(pairs, 4))
+    return set_error(IQ4_E_ALIGN, "%s: offsets and pairs must be 4-byte aligned", fn);
+  if (int e = check_mx_product(fn, packed, n, k, fmt, codes, ldq, scales, lds, n_pairs, y, y_dtype, ldy)) return e;
+  MxArgs a{};
+  a.W = static_cast<const uint8_t*>(packed);
+  a.w_stride = mx_packed_bytes(n, k);
+  a.n = n;
+  a.k = k;
+  a.codes = static_cast<const uint8_t*>(codes);
+  a.ldq = ldq;
+  a.scales = static_cast<const uint8_t*>(scales);
+  a.lds = lds;
+  a.n_rows = n_rows;
+  a.m = n_pairs;
+  a.y = y;
+  a.y_type = y_dtype;
+  a.ldy = ldy;
+  a.offsets = offsets;
+  a.n_expert = n_expert;
+  a.pairs = pairs;
+  a.top_k = top_k;
+  return launch_mx_gemm(a, fmt, as_stream(stream));
 }
 
 }  // extern "C"

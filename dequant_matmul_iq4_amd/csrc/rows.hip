@@ -1,0 +1,238 @@
+// rows.hip -- rows of activations in 8 or 4 bits (rows.hpp gives the formats): the
+// quantiser, the decoder, and the RMS norm that quantises its rows as it makes them.
+// All three only move memory: a few operations per element, each element read and
+// written once.  A lane holds eight consecutive elements and four lanes a block of 32.
+#include "common.hpp"
+#include "rows.hpp"
+
+namespace iq4 {
+
+// ---- quantise -------------------------------------------------------------------------
+// Lanes walk the rows' groups of eight, the zero padding of MX rows included; the scale
+// bytes past the padded codes belong to no group and are zeroed by the row's last lane.
+template <int TYPE>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const void* __restrict__ x, int64_t m, int k,
+                                                            int64_t ldx, int fmt, int octs, int scale_bytes,
+                                                            RowsOut o) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t r = i / octs;
+  const int oct = (int)(i - r * octs);
+  const bool live = r < m;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (live && 8 * oct < k) load8<TYPE>(x, r * ldx + 8 * oct, v);
+  store_rows8(o, fmt, r, oct, v, live);
+  if (live && fmt != kRowsQ8_1 && oct == octs - 1)
+    for (int b = octs / 4; b < scale_bytes; ++b) o.scales[r * o.lds + b] = 0;
+}
+
+int launch_quantize_rows(const void* x, int x_type, int64_t m, int64_t k, int64_t ldx, int fmt, RowsOut o,
+                         hipStream_t s) {
+  const int octs = (int)((fmt == kRowsQ8_1 ? k : (k + 127) / 128 * 128) / 8);
+  const int64_t grid = (m * octs + 255) / 256;
+  const int sb = (int)rows_scale_bytes(fmt, k);
+#define IQ4_QUANT(T) \
+  hipLaunchKernelGGL(quantize_rows_kernel<T>, dim3((unsigned)grid), dim3(256), 0, s, x, m, (int)k, ldx, fmt, octs, sb, o)
+  if (x_type == kF32) IQ4_QUANT(kF32);
+  else if (x_type == kF16) IQ4_QUANT(kF16);
+  else IQ4_QUANT(kBF16);
+#undef IQ4_QUANT
+  return check_launch("quantize_rows_kernel");
+}
+
+// ---- decode ---------------------------------------------------------------------------
+// The value code * scale is exact in binary32 (at most four significant bits, or the
+// eight of a Q8_1 code times the eleven of its scale), then rounded once to the output's
+// type.
+template <int FMT>
+__global__ void __launch_bounds__(256) dequant_rows_kernel(RowsIn in, int64_t m, int octs, int out_type,
+                                                           void* __restrict__ out, int64_t ldo) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t r = i / octs;
+  const int oct = (int)(i - r * octs);
+  if (r >= m) return;
+  const uint8_t* codes = in.codes + r * in.ldq;
+  const uint8_t* scales = in.scales + r * in.lds;
+  float v[8];
+  if constexpr (FMT == kRowsQ8_1) {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(codes + 8 * oct);
+    const float d = h2f(*reinterpret_cast<const uint16_t*>(scales + 2 * (oct >> 2)));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)((w[j >> 2] >> (8 * (j & 3))) & 0xFFu) * d;
+  } else {
+    const uint32_t s = scales[oct >> 2];
+    const float d = (s == 255u) ? __uint_as_float(0x7FC00000u) : pow2_biased(s);
+    if constexpr (FMT == kRowsMxfp4) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + 4 * oct);
+#define IQ4_TWO(B)                                                                  \
+  {                                                                                 \
+    const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, B);            \
+    v[2 * B] = p[0] * d;                                                            \
+    v[2 * B + 1] = p[1] * d;                                                        \
+  }
+      IQ4_TWO(0) IQ4_TWO(1) IQ4_TWO(2) IQ4_TWO(3)
+#undef IQ4_TWO
+    } else {
+      const u32x2 w = *reinterpret_cast<const u32x2*>(codes + 8 * oct);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const auto p = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], false);
+        const auto q = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], true);
+        v[4 * j] = p[0] * d;
+        v[4 * j + 1] = p[1] * d;
+        v[4 * j + 2] = q[0] * d;
+        v[4 * j + 3] = q[1] * d;
+      }
+    }
+  }
+  store8(out_type, out, r * ldo + 8 * oct, v);
+}
+
+int launch_dequant_rows(RowsIn in, int fmt, int64_t m, int64_t k, int out_type, void* out, int64_t ldo,
+                        hipStream_t s) {
+  const int octs = (int)(k / 8);
+  const dim3 grid((unsigned)((m * octs + 255) / 256));
+#define IQ4_DEQ(F) hipLaunchKernelGGL(dequant_rows_kernel<F>, grid, dim3(256), 0, s, in, m, octs, out_type, out, ldo)
+  if (fmt == kRowsMxfp4) IQ4_DEQ(kRowsMxfp4);
+  else if (fmt == kRowsMxfp8) IQ4_DEQ(kRowsMxfp8);
+  else IQ4_DEQ(kRowsQ8_1);
+#undef IQ4_DEQ
+  return check_launch("dequant_rows_kernel");
+}
+
+// ---- RMS norm ---------------------------------------------------------------------------
+//   h = x + res, rounded to the rows' type (what is stored is what is normed);
+//   u = f32(1 / sqrt(mean(h^2) + eps));   y = f32(f32(h * u) * gain).
+// The mean is held in 64 bits: its rounding error then stays some 2^-29 of a binary32
+// step, so u, y and with them every rounding decision of the quantised row are a function
+// of the row alone, whatever the order of the sum.  The extra cost (one conversion and one
+// fused multiply-add per element) hides under the row's loads.
+// One workgroup per row; a lane keeps its groups of eight in registers (V of them) between
+// the sum and the second use.
+template <int TYPE>
+__device__ __forceinline__ void norm_load(const NormArgs& a, int64_t r, int oct, float (&v)[8]) {
+  load8<TYPE>(a.x, r * a.ldx + 8 * oct, v);
+  if (a.res) {
+    float t[8];
+    load8<TYPE>(a.res, r * a.ldr + 8 * oct, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // the binary32 sum of two 16-bit floats rounds to them as the exact sum does
+      v[i] = v[i] + t[i];
+      if constexpr (TYPE == kF16) v[i] = (float)(_Float16)v[i];
+      if constexpr (TYPE == kBF16) v[i] = (float)(__bf16)v[i];
+    }
+  }
+}
+
+template <int TYPE>
+__device__ __forceinline__ void norm_store(const NormArgs& a, int64_t r, int oct, float u, float (&v)[8], bool live) {
+  if (live) {
+    float g[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (a.gain) load8<kF32>(a.gain, 8 * oct, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (v[i] * u) * g[i];
+    if (a.y) store8(a.y_type, a.y, r * a.ldy + 8 * oct, v);
+  }
+}
+
+template <int TYPE, int NT, int V>
+__global__ void __launch_bounds__(NT) rmsnorm_kernel(NormArgs a, int octs_k, int octs, int scale_bytes) {
+  __shared__ double part[NT / 64];
+  const int64_t r = blockIdx.x;
+  const int tid = threadIdx.x;
+  float v[V][8];
+  double sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int oct = tid + j * NT;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+    if (oct < octs_k) {
+      norm_load<TYPE>(a, r, oct, v[j]);
+      if (a.h) store8<TYPE>(a.h, r * a.ldh + 8 * oct, v[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = fma((double)v[j][i], (double)v[j][i], sum);
+  }
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+  if constexpr (NT > 64) {
+    if ((tid & 63) == 0) part[tid >> 6] = sum;
+    __syncthreads();
+    sum = part[0];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) sum += part[w];
+  }
+  // a row with an infinity or a NaN is all NaN
+  float u = (float)(1.0 / sqrt(sum / (double)a.k + (double)a.eps));
+  if (!(sum < __builtin_inf())) u = __uint_as_float(0x7FC00000u);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int oct = tid + j * NT;
+    norm_store<TYPE>(a, r, oct, u, v[j], oct < octs_k);
+    if (a.fmt >= 0) store_rows8(a.o, a.fmt, r, oct, v[j], oct < octs);
+  }
+  if (a.fmt >= 0 && a.fmt != kRowsQ8_1)
+    for (int b = octs / 4 + tid; b < scale_bytes; b += NT) a.o.scales[r * a.o.lds + b] = 0;
+}
+
+// Rows too long for registers: the sum in a first pass, which stores h if it is wanted, and
+// the row read again in a second (h if stored: x or res may be the same memory as h).
+template <int TYPE>
+__global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a, int octs_k, int octs, int scale_bytes) {
+  __shared__ double part[16];
+  const int64_t r = blockIdx.x;
+  const int tid = threadIdx.x;
+  double sum = 0.0;
+  for (int oct = tid; oct < octs_k; oct += 1024) {
+    float v[8];
+    norm_load<TYPE>(a, r, oct, v);
+    if (a.h) store8<TYPE>(a.h, r * a.ldh + 8 * oct, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = fma((double)v[i], (double)v[i], sum);
+  }
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+  if ((tid & 63) == 0) part[tid >> 6] = sum;
+  __syncthreads();
+  sum = part[0];
+  for (int w = 1; w < 16; ++w) sum += part[w];
+  float u = (float)(1.0 / sqrt(sum / (double)a.k + (double)a.eps));
+  if (!(sum < __builtin_inf())) u = __uint_as_float(0x7FC00000u);
+  for (int base = 0; base < octs; base += 1024) {
+    const int oct = base + tid;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (oct < octs_k) {
+      if (a.h) load8<TYPE>(a.h, r * a.ldh + 8 * oct, v);
+      else norm_load<TYPE>(a, r, oct, v);
+    }
+    norm_store<TYPE>(a, r, oct, u, v, oct < octs_k);
+    if (a.fmt >= 0) store_rows8(a.o, a.fmt, r, oct, v, oct < octs);
+  }
+  if (a.fmt >= 0 && a.fmt != kRowsQ8_1)
+    for (int b = octs / 4 + tid; b < scale_bytes; b += 1024) a.o.scales[r * a.o.lds + b] = 0;
+}
+
+template <int TYPE>
+static int launch_norm_t(const NormArgs& a, hipStream_t s) {
+  const int octs_k = (int)(a.k / 8);
+  const bool mx = a.fmt == kRowsMxfp4 || a.fmt == kRowsMxfp8;
+  const int octs = mx ? (int)((a.k + 127) / 128 * 16) : octs_k;
+  const int sb = mx ? (int)rows_scale_bytes(a.fmt, a.k) : 0;
+  const dim3 grid((unsigned)a.m);
+#define IQ4_NORM(NT, V) hipLaunchKernelGGL((rmsnorm_kernel<TYPE, NT, V>), grid, dim3(NT), 0, s, a, octs_k, octs, sb)
+  if (octs <= 64) IQ4_NORM(64, 1);
+  else if (octs <= 256) IQ4_NORM(256, 1);
+  else if (octs <= 512) IQ4_NORM(256, 2);
+  else if (octs <= 1024) IQ4_NORM(256, 4);
+  else if (octs <= 2048) IQ4_NORM(1024, 2);
+  else hipLaunchKernelGGL(rmsnorm_long_kernel<TYPE>, grid, dim3(1024), 0, s, a, octs_k, octs, sb);
+#undef IQ4_NORM
+  return check_launch("rmsnorm_kernel");
+}
+
+int launch_rmsnorm(const NormArgs& a, int type, hipStream_t s) {
+  if (type == kF32) return launch_norm_t<kF32>(a, s);
+  if (type == kF16) return launch_norm_t<kF16>(a, s);
+  return launch_norm_t<kBF16>(a, s);
+}
+
+}  // namespace iq4

@@ -397,6 +397,130 @@ int iq4_xs_dequant(const void* sb, int64_t n_superblocks, int32_t out_dtype, voi
 int iq4_xs_qmv_multi(const void* w, int64_t n, int64_t k, const float* x, int64_t ldx, int32_t T,
                      float* y, int64_t ldy, void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Rows of activations in 8 or 4 bits, with a scale per block of 32 consecutive elements.
+ *   IQ4_ROWS_Q8_1   the blocks of iq4_quantize_q8_1: int8 codes, a binary16 scale.
+ *   IQ4_ROWS_MXFP8  OCP microscaling: E4M3 codes (1 byte), a power-of-two scale (1 byte s,
+ *                   2^(s - 127); 255: the block is NaN).
+ *   IQ4_ROWS_MXFP4  the same with E2M1 codes, element 2i in the low and 2i + 1 in the high
+ *                   nibble of byte i.
+ * A row's codes are contiguous, rows are ldq bytes apart; its scales are contiguous in
+ * block order, rows lds bytes apart.  An MX row as the library writes and reads it is
+ * padded with zero codes to a multiple of 128 elements and with zero scale bytes to a
+ * multiple of 16 (iq4_rows_bytes gives the least ldq and lds); Q8_1 rows have no padding.
+ * Alignment: MX rows 16 bytes (pointers and strides); Q8_1 codes 8, scales 2 bytes.
+ *
+ * Quantisation of float32 values x (a 16-bit input is widened, exactly):
+ *   MX    s = max(E - emax, 0), E the biased binary32 exponent of the block's largest
+ *         magnitude, emax = 2 (E2M1) or 8 (E4M3); code = x * 2^(127 - s) rounded to nearest
+ *         even, magnitudes above the largest code (6 or 448) becoming it.
+ *   Q8_1  as iq4_quantize_q8_1.
+ *   A block with an infinity or a NaN: zero codes, scale 255 (MX) or NaN (Q8_1).
+ * The codes are a function of x alone (bit-exact).
+ */
+#define IQ4_BF16 2 /* element type of the calls below (besides IQ4_F32 and IQ4_F16) */
+#define IQ4_ROWS_MXFP4 0
+#define IQ4_ROWS_MXFP8 1
+#define IQ4_ROWS_Q8_1 2
+
+/* Bytes of one row's codes and scales (the least ldq and lds).  Errors: IQ4_E_ARG,
+ * IQ4_E_UNSUPPORTED (k % 32, k > 2^20). */
+int iq4_rows_bytes(int32_t fmt, int64_t k, int64_t* code_bytes, int64_t* scale_bytes);
+
+/*
+ * Quantise rows of floats.
+ *   x       [m][ldx] of x_dtype (IQ4_F32, IQ4_F16, IQ4_BF16), rows 16-byte aligned.
+ *   codes, scales  m rows of `fmt` as above; the padding of each row is written too, what
+ *           lies between the padded row and its stride is left alone.
+ *   m >= 0 (0: no-op), k % 32 == 0.
+ * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED (k % 32, k > 2^20, m > 2^21,
+ * m * k > 2^34).
+ */
+int iq4_quantize_rows(const void* x, int32_t x_dtype, int64_t m, int64_t k, int64_t ldx, int32_t fmt, void* codes,
+                      int64_t ldq, void* scales, int64_t lds, void* stream);
+
+/*
+ * Decode rows: out[r][i] = code * scale, exact in binary32, rounded once (to nearest even)
+ * to out_dtype.  Arguments, limits and errors as iq4_quantize_rows; out [m][ldo], rows
+ * 16-byte aligned.
+ */
+int iq4_dequant_rows(const void* codes, int64_t ldq, const void* scales, int64_t lds, int32_t fmt, int64_t m,
+                     int64_t k, int32_t out_dtype, void* out, int64_t ldo, void* stream);
+
+/*
+ * Residual addition, RMS norm and quantisation of the normed rows in one pass:
+ *   h = x + res, rounded to dtype (h = x without res);
+ *   u = f32(1 / sqrt(mean(h^2) + eps)), the mean in 64 bits;
+ *   y = f32(f32(h * u) * gain).
+ *   x, res  [m][ldx], [m][ldr] of dtype (IQ4_F32, IQ4_F16, IQ4_BF16); res may be NULL.
+ *   gain    [k] float32, 16-byte aligned, or NULL (1).      eps finite, >= 0.
+ *   h       [m][ldh] of dtype, or NULL; may be x or res itself (same stride) when res is
+ *           given.  No other overlap of an output with an input or another output.
+ *   y       [m][ldy] of y_dtype, or NULL.
+ *   codes, scales  y (the float32 values) quantised as by iq4_quantize_rows, or codes NULL
+ *           (fmt, ldq, scales, lds are then ignored).  y or codes must be given.
+ * A row that holds an infinity or a NaN gets all NaN.  A row does not depend on the others,
+ * and every output is a function of the inputs alone, bit for bit.
+ * Errors: as iq4_quantize_rows.
+ */
+int iq4_rmsnorm(const void* x, int64_t ldx, const void* res, int64_t ldr, int32_t dtype, int64_t m, int64_t k,
+                const float* gain, float eps, void* h, int64_t ldh, void* y, int32_t y_dtype, int64_t ldy,
+                int32_t fmt, void* codes, int64_t ldq, void* scales, int64_t lds, void* stream);
+
+/* Size in bytes of the packed form of an n x k MXFP4 matrix, or -1 (n < 1, k < 1, k % 32,
+ * n > 2^24, k > 2^20). */
+int64_t iq4_mx_packed_bytes(int64_t n, int64_t k);
+
+/*
+ * Rearrange an n x k MXFP4 matrix for the products below (one-time, at weight-load time).
+ *   codes   [n][ldq] bytes, ldq >= k / 2: two codes a byte, low nibble first.
+ *   scales  [n][lds] bytes, lds >= k / 32.  Both may have any alignment and no padding
+ *           (a checkpoint's tensors as they are, or rows of iq4_quantize_rows).
+ *   packed  iq4_mx_packed_bytes(n, k) bytes, 256-byte aligned, overlapping neither.
+ * Packed layout, KT = ceil(k / 128), KQ = ceil(k / 512): code tile (rt, kt) at
+ * (rt * KT + kt) * 1024 bytes, 64 entries of 16 bytes, entry 16g + j = block 4kt + g of row
+ * 16rt + j; after all code tiles the scales, at (rt * KQ + kq) * 256 bytes 64 words, byte b
+ * of word 16g + j = the scale of block 16kq + 4b + g of row 16rt + j.  Zero past n and k.
+ * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED.
+ */
+int iq4_mx_pack_weights(const void* codes, int64_t ldq, const void* scales, int64_t lds, int64_t n, int64_t k,
+                        void* packed, void* stream);
+
+/*
+ * Product of microscaled rows with MXFP4 weights on the scaled matrix instructions:
+ *   Y[i][r] = sum_k W[r][k] * X[i][k],  i < m, r < n, fp32 sums, rounded once to y_dtype.
+ *   packed  W (iq4_mx_pack_weights), 256-byte aligned.
+ *   fmt     of X: IQ4_ROWS_MXFP4 or IQ4_ROWS_MXFP8; codes, scales: m rows (above).
+ *   y       [m][ldy] of y_dtype (IQ4_F32, IQ4_F16, IQ4_BF16), ldy >= n, element aligned;
+ *           columns n .. ldy - 1 are left alone.
+ *   m >= 0 (0: no-op), any n >= 1, k % 32 == 0.  No workspace.
+ * Deterministic; for m <= 16 each row is bitwise the m = 1 call's.
+ * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED (k % 32, sizes).
+ */
+int iq4_mx_gemm(const void* packed, int64_t n, int64_t k, int32_t fmt, const void* codes, int64_t ldq,
+                const void* scales, int64_t lds, int64_t m, void* y, int32_t y_dtype, int64_t ldy, void* stream);
+
+/*
+ * The same product with one matrix per expert, output rows sorted by expert:
+ *   Y[i] = W_e X[row(i)],  offsets[e] <= i < offsets[e + 1];  row(i) = pairs[i] / top_k, or
+ *   i if pairs is NULL.
+ * offsets and pairs are iq4_moe_gather's: with pairs, X has a row per token (gate and up
+ * products); without, a row per pair in the experts' order (down products).
+ *   packed  n_expert packed n x k matrices, expert e at e * iq4_mx_packed_bytes(n, k).
+ *   codes, scales  n_rows rows of X.
+ *   offsets [n_expert + 1] int32, ascending from 0, offsets[n_expert] <= n_pairs.
+ *   pairs   [n_pairs] int32 or NULL.   n_pairs >= 0 (0: no-op).   1 <= n_expert <= 1024.
+ *   y       [n_pairs][ldy]; rows from offsets[n_expert] on are left as they were.
+ * offsets and pairs are read on the device and cannot be checked before the call; values
+ * out of range are clamped into it (the result is then unspecified, no memory outside the
+ * buffers is touched).
+ * Errors: as iq4_mx_gemm; IQ4_E_ARG too if X has too few rows for n_pairs.
+ */
+int iq4_mx_grouped_gemm(const void* packed, int32_t n_expert, int64_t n, int64_t k, int32_t fmt, const void* codes,
+                        int64_t ldq, const void* scales, int64_t lds, int64_t n_rows, const int32_t* offsets,
+                        const int32_t* pairs, int32_t top_k, int64_t n_pairs, void* y, int32_t y_dtype, int64_t ldy,
+                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif

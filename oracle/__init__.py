@@ -9,5 +9,7 @@ from .iq4_ref import *  # noqa: F401,F403
 from .iq4_ref import __all__ as _nl_all
 from .iq4xs_ref import *  # noqa: F401,F403
 from .iq4xs_ref import __all__ as _xs_all
+from .rows_ref import *  # noqa: F401,F403
+from .rows_ref import __all__ as _rows_all
 
-__all__ = list(_nl_all) + list(_xs_all)
+__all__ = list(_nl_all) + list(_xs_all) + list(_rows_all)
