@@ -115,17 +115,26 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None  # torch's lookup of a device's current stream as an integer
+
+
 def _stream(stream):
     if stream is None:
+        # torch.cuda.current_stream() builds a Stream object (some 3 us, as long as a small
+        # kernel); the integer alone is a tenth of that
+        global _raw_stream
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 def _call(name, *args):
-    rc = getattr(lib(), name)(*args)
+    rc = getattr(_lib or lib(), name)(*args)
     if rc != IQ4_OK:
         raise IQ4Error(name, rc, lib().iq4_last_error().decode())
     return rc

@@ -8,6 +8,8 @@
 // 16 bytes.  E4M3: elements 16g .. 16g+15 and 64+16g .. 64+16g+15 of row c, 32 bytes.
 // Either way the lane's scale byte is that of the row's block g.  The weights are the first
 // operand, so the lane receives D[4g + i][c]: four consecutive columns of one row of Y.
+#include <type_traits>
+
 #include "common.hpp"
 #include "mx.hpp"
 #include "rows.hpp"
@@ -15,6 +17,7 @@
 namespace iq4 {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // ---- pack -------------------------------------------------------------------------------
 // Code tile (rt, kt) at (rt * KT + kt) * 1024: lane 16g + c has the 16 bytes of row 16 rt + c,
@@ -67,19 +70,73 @@ struct Act {  // one 16-row x 128-element operand of activations
   static constexpr int kTileBytes = FMT == kRowsMxfp4 ? 64 : 128;  // of one row
 };
 
+// An MXFP8 operand is multiplied in two parts, the codes of magnitude 2 and above and the
+// rest (exponent bit 3 of E4M3, bit 6 of the byte, tells which; the other part's codes are
+// zero).  Within an instruction's small groups of products the sum keeps only about 13 bits
+// below the largest product's exponent: over the whole range of E4M3 that costs 1e-5 of the
+// result (measured), while each part's products span few enough bits to add exactly
+// (measured: every sum of 128 equal to the exact one, rounded once).  E2M1 needs no split.
 template <int FMT>
-__device__ __forceinline__ f32x4 mma(u32x4 w, uint32_t sw, int sel, const uint32_t (&x)[Act<FMT>::kWords], uint32_t sx,
-                                     f32x4 acc) {
-  const i32x8 a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-  i32x8 b = {0, 0, 0, 0, 0, 0, 0, 0};
+struct Frag {
+  u32x4 lo[Act<FMT>::kWords / 4], hi[FMT == kRowsMxfp4 ? 1 : 2];
+};
+template <int FMT>
+__device__ __forceinline__ Frag<FMT> split(const u32x4 (&x)[Act<FMT>::kWords / 4]) {
+  Frag<FMT> f;
+  if constexpr (FMT == kRowsMxfp4) {
+    f.lo[0] = x[0];
+  } else {
 #pragma unroll
-  for (int i = 0; i < Act<FMT>::kWords; ++i) b[i] = (int)x[i];
-  constexpr int kB = FMT == kRowsMxfp4 ? 4 : 0;  // E2M1 or E4M3
-  switch (sel) {  // the byte of the weights' scale word
-    case 0: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, kB, 0, (int)sw, 0, (int)sx);
-    case 1: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, kB, 1, (int)sw, 0, (int)sx);
-    case 2: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, kB, 2, (int)sw, 0, (int)sx);
-    default: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, kB, 3, (int)sw, 0, (int)sx);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t t = (x[h][i] >> 6) & 0x01010101u, mask = (t << 8) - t;  // 255 in every byte of the high part
+        f.hi[h][i] = x[h][i] & mask;
+        f.lo[h][i] = x[h][i] & ~mask;
+      }
+  }
+  return f;
+}
+
+// acc += W X^T of one 16 x 16 x 128 step; `sel` is the byte of the weights' scale word.
+template <int FMT, int SEL>
+__device__ __forceinline__ f32x4 mma(u32x4 w, uint32_t sw, const Frag<FMT>& x, uint32_t sx, f32x4 acc) {
+  const i32x8 a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+  if constexpr (FMT == kRowsMxfp4) {
+    const i32x8 b = {(int)x.lo[0][0], (int)x.lo[0][1], (int)x.lo[0][2], (int)x.lo[0][3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 4, SEL, (int)sw, 0, (int)sx);
+  } else {
+    i32x8 l, h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l[i] = (int)x.lo[i >> 2][i & 3], h[i] = (int)x.hi[i >> 2][i & 3];
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, l, acc, 4, 0, SEL, (int)sw, 0, (int)sx);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, h, acc, 4, 0, SEL, (int)sw, 0, (int)sx);
+  }
+}
+template <int FMT>
+__device__ __forceinline__ f32x4 mma(int sel, u32x4 w, uint32_t sw, const Frag<FMT>& x, uint32_t sx, f32x4 acc) {
+  switch (sel) {
+    case 0: return mma<FMT, 0>(w, sw, x, sx, acc);
+    case 1: return mma<FMT, 1>(w, sw, x, sx, acc);
+    case 2: return mma<FMT, 2>(w, sw, x, sx, acc);
+    default: return mma<FMT, 3>(w, sw, x, sx, acc);
+  }
+}
+
+// acc += W X^T of one 32 x 32 x 64 half step: byte J of the weights' scale word, byte 2 H of
+// the rows'.
+template <int FMT, int J, int H>
+__device__ __forceinline__ f32x16 mma32(u32x4 w, uint32_t sw, const Frag<FMT>& x, uint32_t sx, f32x16 acc) {
+  const i32x8 a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+  if constexpr (FMT == kRowsMxfp4) {
+    const i32x8 b = {(int)x.lo[0][0], (int)x.lo[0][1], (int)x.lo[0][2], (int)x.lo[0][3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 4, 4, J, (int)sw, 2 * H, (int)sx);
+  } else {
+    i32x8 l, h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l[i] = (int)x.lo[i >> 2][i & 3], h[i] = (int)x.hi[i >> 2][i & 3];
+    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, l, acc, 4, 0, J, (int)sw, 2 * H, (int)sx);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, h, acc, 4, 0, J, (int)sw, 2 * H, (int)sx);
   }
 }
 
@@ -111,20 +168,37 @@ __device__ __forceinline__ void store_y4(const MxArgs& a, int64_t row, int64_t c
   }
 }
 
-// Tile `t` of the grouped rows in tiles of `bm`: its expert, first row and rows, found by
-// every wave on its own from the offsets (64 experts a step: tiles per expert, a running
-// sum over the lanes, the first lane past t).  Offsets are clamped to [0, m]: whatever they
-// hold, no row outside is touched.  False: there are fewer tiles.
+// Expert e's rows [o0, o1), clamped to [0, m]: whatever the offsets hold, no row outside is
+// touched.
+__device__ __forceinline__ void expert_rows(const MxArgs& a, int e, int64_t& o0, int64_t& o1) {
+  o0 = o1 = 0;
+  if (e < a.n_expert) {
+    o0 = min(max((int64_t)a.offsets[e], (int64_t)0), a.m);
+    o1 = min(max((int64_t)a.offsets[e + 1], o0), a.m);
+  }
+}
+
+// Tiles of `bm` rows over all experts (every wave on its own, 64 experts a step).
+__device__ __forceinline__ int64_t count_tiles(const MxArgs& a, int bm) {
+  int64_t all = 0;
+  for (int e0 = 0; e0 < a.n_expert; e0 += 64) {
+    int64_t o0, o1;
+    expert_rows(a, e0 + (threadIdx.x & 63), o0, o1);
+    int mine = (int)((o1 - o0 + bm - 1) / bm);
+    for (int d = 32; d > 0; d >>= 1) mine += __shfl_xor(mine, d);
+    all += __builtin_amdgcn_readfirstlane(mine);
+  }
+  return all;
+}
+
+// Tile `t` of the grouped rows: its expert, first row and rows (tiles per expert, a running
+// sum over the lanes, the first lane past t).  False: there are fewer tiles.
 __device__ __forceinline__ bool find_tile(const MxArgs& a, int64_t t, int bm, int& e, int64_t& row0, int& rows) {
   const int lane = threadIdx.x & 63;
   int64_t before = 0;
   for (int e0 = 0; e0 < a.n_expert; e0 += 64) {
-    const int el = e0 + lane;
-    int64_t o0 = 0, o1 = 0;
-    if (el < a.n_expert) {
-      o0 = min(max((int64_t)a.offsets[el], (int64_t)0), a.m);
-      o1 = min(max((int64_t)a.offsets[el + 1], o0), a.m);
-    }
+    int64_t o0, o1;
+    expert_rows(a, e0 + lane, o0, o1);
     const int mine = (int)((o1 - o0 + bm - 1) / bm);
     int run = mine;
     for (int d = 1; d < 64; d <<= 1) {
@@ -136,9 +210,9 @@ __device__ __forceinline__ bool find_tile(const MxArgs& a, int64_t t, int bm, in
       const int src = __builtin_ctzll(past);
       const int64_t first = before + __shfl(run, src) - __shfl(mine, src);  // tiles before this expert
       const int64_t b0 = __shfl((int)o0, src), b1 = __shfl((int)o1, src);
-      e = e0 + src;
-      row0 = b0 + (t - first) * bm;
-      rows = (int)min((int64_t)bm, b1 - row0);
+      e = __builtin_amdgcn_readfirstlane(e0 + src);
+      row0 = __builtin_amdgcn_readfirstlane((int)(b0 + (t - first) * bm));
+      rows = __builtin_amdgcn_readfirstlane((int)min((int64_t)bm, b1 - row0));
       return true;
     }
     before += __shfl(run, 63);
@@ -200,14 +274,11 @@ __global__ void __launch_bounds__(64 * NW) mx_rows_kernel(MxArgs a) {
       const u32x4 w = *reinterpret_cast<const u32x4*>(wc + kt * kMxTileBytes);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        uint32_t x[Act<FMT>::kWords];
+        u32x4 x[Act<FMT>::kWords / 4];
 #pragma unroll
-        for (int h = 0; h < Act<FMT>::kWords / 4; ++h) {
-          const u32x4 t = *reinterpret_cast<const u32x4*>(xc[i] + (int64_t)kt * Act<FMT>::kTileBytes + 64 * h);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) x[4 * h + q] = t[q];
-        }
-        acc[i] = mma<FMT>(w, sw, j, x, sx[i][j] >> (8 * g), acc[i]);
+        for (int h = 0; h < Act<FMT>::kWords / 4; ++h)
+          x[h] = *reinterpret_cast<const u32x4*>(xc[i] + (int64_t)kt * Act<FMT>::kTileBytes + 64 * h);
+        acc[i] = mma<FMT>(j, w, sw, split<FMT>(x), sx[i][j] >> (8 * g), acc[i]);
       }
     }
   }
@@ -245,10 +316,368 @@ static int launch_rows(const MxArgs& a, hipStream_t s) {
   return check_launch("mx_rows_kernel");
 }
 
+// ---- many rows ------------------------------------------------------------------------------
+// 32 x 32 x 64 instructions (lane l = 32 h + r: row r, E2M1 elements 32h .. 32h+31 or E4M3
+// elements 16h .. 16h+15 and 32+16h .. 32+16h+15, scale of block h; it receives
+// D[8 (i / 4) + 4 h + i % 4][r]).  WN x WM waves, each FN x FM pieces of 32 x 32.
+//
+// A step is 128 elements of k.  Its operands are copied from memory straight into LDS by
+// global_load_lds, S stages deep: packed weight tiles as they are; rows of X with their
+// 16-byte chunks exchanged inside a row (chunk q of row r at place q ^ f(r)) so that the 16
+// lanes of a read phase fall on different banks.  The scales of four steps (a quad) come the
+// same way into one buffer, which is free again when the quad's second step begins (they are
+// then in registers).  The copies are written as inline assembly so that the
+// compiler, which cannot tell the stages apart, does not wait for all of them before each
+// LDS read; the counts of copies in flight are worked out below.
+//
+// Order in step t (two halves of 64 elements):
+//   read the operands of half 1;  multiply half 0;
+//   wait: half 1's reads done, stage t+1 landed;  barrier: so for every wave;
+//   copy stage t+S (into stage t, which no wave reads any more);
+//   read the operands of half 0 of step t+1;  multiply half 1.
+// A wave's LDS reads so run under its own matrix instructions.
+
+template <int N>
+__device__ __forceinline__ void wait_copies() {  // at most N copies still in flight, and no LDS read
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (0 << 8));
+}
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
+}
+// Lane l's 16 bytes at base + voff to LDS address lds + 16 l.  M0 carries the LDS address; one
+// wait state lies between its write and the copy.
+__device__ __forceinline__ void copy16(const void* base, uint32_t voff, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(base), "{m0}"(lds) : "memory");
+}
+
+// A pointer that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<const uint8_t*>((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) |
+                                          (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32);
+}
+
+// Workgroup b of a grid of >= 8 ceil(G / 8) to tile 0 .. G - 1 (or -1): hardware deals
+// workgroups round-robin to the eight XCDs, so each XCD gets a run of neighbouring tiles,
+// which share operands in its own L2.
+__device__ __forceinline__ int64_t xcd_tile(int64_t b, int64_t G) {
+  const int64_t per = (G + 7) / 8, i = b / 8;
+  if (i >= per) return -1;
+  const int64_t L = (b % 8) * per + i;
+  return L < G ? L : -1;
+}
+
+template <int FMT, int FN, int FM, int WN, int WM, int S>
+struct Tile {
+  static constexpr int kWaves = WN * WM;
+  static constexpr int kBN = 32 * FN * WN, kBM = 32 * FM * WM;
+  static constexpr int kRowB = Act<FMT>::kTileBytes;             // bytes of a row of X per step
+  static constexpr int kChunks = kRowB / 16;                     // 16-byte chunks of them
+  static constexpr int kWBytes = kBN * 64, kXBytes = kBM * kRowB;  // a stage
+  static constexpr int kStage = kWBytes + kXBytes;
+  static constexpr int kCW = kWBytes / 1024 / kWaves, kCX = kXBytes / 1024 / kWaves;  // copies a wave per step
+  static constexpr int kC = kCW + kCX;
+  static constexpr int kWS = kBN * 16, kXS = kBM * 16;           // scales of a quad
+  static constexpr int kScales = kWS + kXS;
+  static constexpr int kCWS = (kWS / 1024 + kWaves - 1) / kWaves, kCXS = (kXS / 1024 + kWaves - 1) / kWaves;
+  static constexpr int kD = S - 1;                               // stages copied ahead
+  static constexpr int kLds = S * kStage + kScales;
+  static_assert(kWBytes % (1024 * kWaves) == 0 && kXBytes % (1024 * kWaves) == 0, "copies split evenly");
+  static_assert(kWS % 1024 == 0 && kXS % 1024 == 0, "whole scale copies");
+  static_assert(kD >= 1 && kD <= 3, "the counts below");
+  static_assert(kLds <= 160 * 1024, "LDS");
+  // Copies younger than stage t+1's when step t (place j in its quad) waits for it: those of
+  // stages t+2 .. t+D, and the next quad's scales if they were issued since (before stage
+  // u+D's copies, after the barrier that begins place u % 4 == 1).
+  static constexpr int in_flight(int j) { return (kD - 1) * kC + (j >= 1 && j < kD ? kCWS + kCXS : 0); }
+};
+
+// `rows` x `cols` values in LDS (rows of PITCH, at most 32 x COLS) to Y from (row0, col0) on,
+// by one wave: eight columns a lane.
+template <int COLS, int PITCH>
+__device__ __forceinline__ void store_rows_piece(const MxArgs& a, const float* part, int64_t row0, int rows, int64_t col0,
+                                                 int cols) {
+  constexpr int kLanes = COLS / 8, kStep = 64 / kLanes;  // lanes a row, rows a step
+  const int lane = threadIdx.x & 63, c = 8 * (lane % kLanes);
+#pragma unroll 1
+  for (int r = lane / kLanes; r < rows; r += kStep) {
+    if (c >= cols) continue;
+    float v[8];
+    const f32x4 p = *reinterpret_cast<const f32x4*>(part + r * PITCH + c), q = *reinterpret_cast<const f32x4*>(part + r * PITCH + c + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = p[i], v[4 + i] = q[i];
+    const int64_t at = (row0 + r) * a.ldy + col0 + c;
+    if (a.vec_y && c + 8 <= cols) {
+      store8(a.y_type, a.y, at, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (c + i >= cols) break;
+        if (a.y_type == kF32) static_cast<float*>(a.y)[at + i] = v[i];
+        else static_cast<uint16_t*>(a.y)[at + i] = (uint16_t)(a.y_type == kF16 ? pack2<kF16>(v[i], v[i]) : pack2<kBF16>(v[i], v[i]));
+      }
+    }
+  }
+}
+
+// waves a SIMD: registers are given out so that as many workgroups share a CU as LDS allows (two at most)
+template <int FMT, int FN, int FM, int WN, int WM, int S, bool GROUPED>
+__global__ void __launch_bounds__(64 * WN * WM)
+__attribute__((amdgpu_waves_per_eu(Tile<FMT, FN, FM, WN, WM, S>::kWaves / 4 * (Tile<FMT, FN, FM, WN, WM, S>::kLds <= 80 * 1024 ? 2 : 1))))
+mx_tile_kernel(MxArgs a) {
+  using T = Tile<FMT, FN, FM, WN, WM, S>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
+  const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave % WN, wm = wave / WN;
+
+  // ---- which tile ---------------------------------------------------------------------
+  const int64_t nt_n = (a.n + T::kBN - 1) / T::kBN;
+  int64_t nt, row0;
+  int rows;
+  const uint8_t* W = a.W;
+  if constexpr (GROUPED) {
+    const int64_t L = xcd_tile(blockIdx.x, count_tiles(a, T::kBM) * nt_n);
+    if (L < 0) return;
+    int e;
+    if (!find_tile(a, L / nt_n, T::kBM, e, row0, rows)) return;
+    nt = L % nt_n;
+    W += e * a.w_stride;
+  } else {
+    const int64_t mt_n = (a.m + T::kBM - 1) / T::kBM;
+    const int64_t L = xcd_tile(blockIdx.x, mt_n * nt_n);
+    if (L < 0) return;
+    // bands of eight row tiles, walked row tile first: the 32 CUs of an XCD hold about
+    // 8 x 4 tiles and read 12 operand panels for them
+    const int64_t band = L / (8 * nt_n), in = L - band * 8 * nt_n;
+    const int64_t high = min((int64_t)8, mt_n - 8 * band);
+    row0 = (8 * band + in % high) * T::kBM;
+    nt = in / high;
+    rows = (int)min((int64_t)T::kBM, a.m - row0);
+  }
+  const int kt_n = mx_k_tiles(a.k), kq_n = mx_k_quads(a.k);
+  const int64_t rt_n = mx_row_tiles(a.n), rt0 = nt * (T::kBN / 16);
+  const uint32_t lds0 = lds_offset(lds);
+
+  // ---- what this lane copies ------------------------------------------------------------
+  // W: tiles wave * kCW ..; those past n repeat the last one (read in bounds, not stored)
+  const uint8_t* wt[T::kCW];
+#pragma unroll
+  for (int i = 0; i < T::kCW; ++i) wt[i] = scalar(W + min(rt0 + wave * T::kCW + i, rt_n - 1) * kt_n * kMxTileBytes);
+  // X: kilobytes wave * kCX ..; rows past the last repeat it
+  uint32_t xo[T::kCX];
+#pragma unroll
+  for (int i = 0; i < T::kCX; ++i) {
+    const int at = (wave * T::kCX + i) * 64 + lane, row = at / T::kChunks, place = at % T::kChunks;
+    const int chunk = place ^ (FMT == kRowsMxfp4 ? (row >> 2) & 3 : (row >> 1) & 7);
+    int64_t src = min(row, rows - 1);
+    if constexpr (GROUPED) src = act_row(a, row0 + src);
+    xo[i] = (uint32_t)(src * a.ldq) + 16 * chunk;
+  }
+  // scales: every wave issues the same number of copies, some of them twice (the same bytes
+  // to the same place)
+  uint32_t wso[T::kCWS], xso[T::kCXS];
+  int wsl[T::kCWS], xsl[T::kCXS];
+#pragma unroll
+  for (int i = 0; i < T::kCWS; ++i) {
+    const int kb = (wave * T::kCWS + i) % (T::kWS / 1024);
+    wsl[i] = kb * 1024;
+    // four row tiles a kilobyte, relative to the workgroup's first
+    const int64_t rt = min(rt0 + 4 * kb + (lane >> 4), rt_n - 1) - rt0;
+    wso[i] = (uint32_t)(rt * kq_n * kMxScaleBytes) + 16 * (lane & 15);
+  }
+#pragma unroll
+  for (int i = 0; i < T::kCXS; ++i) {
+    const int kb = (wave * T::kCXS + i) % (T::kXS / 1024);
+    xsl[i] = T::kWS + kb * 1024;
+    int64_t src = min(kb * 64 + lane, rows - 1);
+    if constexpr (GROUPED) src = act_row(a, row0 + src);
+    xso[i] = (uint32_t)(src * a.lds);
+  }
+  const uint8_t* xbase = scalar(a.codes + (GROUPED ? 0 : row0 * a.ldq));
+  const uint8_t* xsbase = scalar(a.scales + (GROUPED ? 0 : row0 * a.lds));
+  const uint8_t* wsbase = scalar(W + mx_code_plane(a.n, a.k) + rt0 * kq_n * kMxScaleBytes);
+
+  // (steps and quads past the last copy it again: the counts hold to the end)
+  auto copy_part = [&](int t, int i0, int i1) {  // copies i0 .. i1 - 1 of this wave's kC
+    const uint32_t st = lds0 + (uint32_t)(t % S) * T::kStage;
+    const int k = min(t, kt_n - 1);
+#pragma unroll
+    for (int i = 0; i < T::kC; ++i) {
+      if (i < i0 || i >= i1) continue;
+      if (i < T::kCW) copy16(wt[i] + (int64_t)k * kMxTileBytes, 16 * lane, st + (wave * T::kCW + i) * 1024);
+      else copy16(xbase + (int64_t)k * T::kRowB, xo[i - T::kCW], st + T::kWBytes + (wave * T::kCX + i - T::kCW) * 1024);
+    }
+  };
+  auto copy_stage = [&](int t) { copy_part(t, 0, T::kC); };
+  auto copy_scales = [&](int q) {
+    const uint32_t st = lds0 + S * T::kStage;
+    const int k = min(q, kq_n - 1);
+#pragma unroll
+    for (int i = 0; i < T::kCWS; ++i) copy16(wsbase + (int64_t)k * kMxScaleBytes, wso[i], st + wsl[i]);
+#pragma unroll
+    for (int i = 0; i < T::kCXS; ++i) copy16(xsbase + (int64_t)k * 16, xso[i], st + xsl[i]);
+  };
+
+  // ---- operands from LDS --------------------------------------------------------------------
+  struct Ops {
+    u32x4 w[FN], x[FM][Act<FMT>::kWords / 4];
+  };
+  // where this lane reads: weights 32 (FN wn + i) + r, rows 32 (FM wm + i) + r
+  const int wrow = 32 * FN * wn + r, xrow = 32 * FM * wm + r;
+  auto read_half = [&](int t, int s, Ops& o) {
+    const uint8_t* st = lds + (t % S) * T::kStage;
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+      o.w[i] = *reinterpret_cast<const u32x4*>(st + (wrow / 16 + 2 * i) * 1024 + (16 * (2 * s + h) + (r & 15)) * 16);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int c = 0; c < Act<FMT>::kWords / 4; ++c) {
+        const int chunk = FMT == kRowsMxfp4 ? 2 * s + h : 4 * s + 2 * c + h;
+        const int place = chunk ^ (FMT == kRowsMxfp4 ? (r >> 2) & 3 : (r >> 1) & 7);
+        o.x[i][c] = *reinterpret_cast<const u32x4*>(st + T::kWBytes + (xrow + 32 * i) * T::kRowB + place * 16);
+      }
+  };
+  struct Scales {
+    uint32_t w[FN][2];
+    u32x4 x[FM];  // of step j in word j, this lane's blocks h and 2 + h in bytes 0 and 2
+  };
+  auto read_scales = [&](Scales& o) {
+    const uint8_t* st = lds + S * T::kStage;
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        o.w[i][s] = *reinterpret_cast<const uint32_t*>(st + (wrow / 16 + 2 * i) * 256 + (16 * (2 * s + h) + (r & 15)) * 4);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) o.x[i] = *reinterpret_cast<const u32x4*>(st + T::kWS + (xrow + 32 * i) * 16) >> (8 * h);
+  };
+
+  f32x16 acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+  // one half step; `before(m)` runs before the products of row piece m
+  auto multiply = [&](auto jj, auto ss, const Ops& o, const Scales& sc, auto before) {
+    constexpr int j = decltype(jj)::value, s = decltype(ss)::value;
+#pragma unroll
+    for (int m = 0; m < FM; ++m) {
+      before(m);
+      const Frag<FMT> x = split<FMT>(o.x[m]);
+#pragma unroll
+      for (int n = 0; n < FN; ++n) acc[n][m] = mma32<FMT, j, s>(o.w[n], sc.w[n][s], x, sc.x[m][j], acc[n][m]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // the operands are in registers here: keeps the reads where they are issued
+  auto arrived = [&](Ops& o) {
+#pragma unroll
+    for (int i = 0; i < FN; ++i) asm volatile("" : "+v"(o.w[i]));
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int c = 0; c < Act<FMT>::kWords / 4; ++c) asm volatile("" : "+v"(o.x[i][c]));
+  };
+
+  // ---- main loop ------------------------------------------------------------------------------
+  copy_scales(0);
+#pragma unroll
+  for (int t = 0; t < T::kD; ++t) copy_stage(t);
+  wait_copies<(T::kD - 1) * T::kC>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  copy_stage(T::kD);
+  Ops o0, o1;
+  Scales sc, next;
+  read_scales(sc);
+  read_half(0, 0, o0);
+  auto step = [&](auto jj, int t) {
+    constexpr int j = decltype(jj)::value;
+    read_half(t, 1, o1);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(jj, std::integral_constant<int, 0>{}, o0, sc, [](int) {});
+    asm volatile("" ::: "memory");
+    wait_copies<T::in_flight(j)>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read_half(t + 1, 0, o0);
+    if constexpr (j == 3) read_scales(next);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(jj, std::integral_constant<int, 1>{}, o1, sc, [&](int m) {
+      if (j == 0 && m == 0) copy_scales(t / 4 + 1);  // every wave has read this quad's
+      copy_part(t + 1 + T::kD, m * T::kC / FM, (m + 1) * T::kC / FM);
+    });
+    arrived(o0);
+    if constexpr (j == 3) sc = next;
+  };
+  for (int t = 0;; t += 4) {
+    step(std::integral_constant<int, 0>{}, t);
+    if (t + 1 >= kt_n) break;
+    step(std::integral_constant<int, 1>{}, t + 1);
+    if (t + 2 >= kt_n) break;
+    step(std::integral_constant<int, 2>{}, t + 2);
+    if (t + 3 >= kt_n) break;
+    step(std::integral_constant<int, 3>{}, t + 3);
+    if (t + 4 >= kt_n) break;
+  }
+  // ---- store ------------------------------------------------------------------------------------
+  // Through LDS, a row piece at a time and each wave in a part of its own, so that the rows are
+  // written in runs of 64 FN or 128 FN bytes (a lane holds four columns of 32 different rows).
+  wait_copies<0>();
+  __builtin_amdgcn_s_barrier();  // no copy lands in LDS any more, and no wave reads the stages
+  asm volatile("" ::: "memory");
+  constexpr int kCols = 32 * FN, kPitch = kCols + 4;
+  static_assert(T::kWaves * 32 * kPitch * 4 <= T::kLds, "the parts fit");
+  float* part = reinterpret_cast<float*>(lds) + wave * 32 * kPitch;
+  const int64_t col0 = nt * T::kBN + kCols * wn;
+  const int cols = (int)min((int64_t)kCols, a.n - col0);
+#pragma unroll
+  for (int m = 0; m < FM; ++m) {
+    const int first = 32 * (FM * wm + m);
+    if (first >= rows || cols <= 0) break;
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(part + r * kPitch + 32 * n + 8 * q + 4 * h) =
+            f32x4{acc[n][m][4 * q], acc[n][m][4 * q + 1], acc[n][m][4 * q + 2], acc[n][m][4 * q + 3]};
+    store_rows_piece<kCols, kPitch>(a, part, row0 + first, min(32, rows - first), col0, cols);
+  }
+}
+
+template <int FMT, int FN, int FM, int WN, int WM, int S>
+static int launch_tiles(const MxArgs& a, hipStream_t s) {
+  using T = Tile<FMT, FN, FM, WN, WM, S>;
+  const int64_t nt = (a.n + T::kBN - 1) / T::kBN;
+  const bool grouped = a.offsets != nullptr;
+  int64_t tiles = (a.m + T::kBM - 1) / T::kBM;
+  if (grouped) tiles = a.m / T::kBM + a.n_expert < a.m ? a.m / T::kBM + a.n_expert : a.m;
+  const dim3 grid((unsigned)((nt * tiles + 7) / 8 * 8));
+  if (grouped) hipLaunchKernelGGL((mx_tile_kernel<FMT, FN, FM, WN, WM, S, true>), grid, dim3(64 * T::kWaves), 0, s, a);
+  else hipLaunchKernelGGL((mx_tile_kernel<FMT, FN, FM, WN, WM, S, false>), grid, dim3(64 * T::kWaves), 0, s, a);
+  return check_launch("mx_tile_kernel");
+}
+
+// Which kernel: see the comments at each.
+template <int FMT>
+static int launch_fmt(const MxArgs& a, hipStream_t s) {
+  const int64_t tiles = ((a.n + 255) / 256) * ((a.m + 127) / 128);
+  // the tile kernel's row offsets have 32 bits
+  const int64_t span = (a.offsets ? a.n_rows : 256) * (a.ldq > a.lds ? a.ldq : a.lds);
+  if (a.m <= 16) return launch_rows<FMT, 1, 8>(a, s);
+  if (a.m <= 32 || span >= ((int64_t)1 << 32)) return launch_rows<FMT, 4, 4>(a, s);
+  if (tiles >= 256) return launch_tiles<FMT, 4, 2, 2, 2, FMT == kRowsMxfp4 ? 3 : 2>(a, s);
+  return launch_tiles<FMT, 1, 1, 2, 2, 4>(a, s);
+}
+
 int launch_mx_gemm(MxArgs a, int fmt, hipStream_t s) {
-  a.vec_y = a.ldy % 4 == 0 && aligned(a.y, a.y_type == kF32 ? 16 : 8);
-  if (fmt == kRowsMxfp4) return a.m <= 16 ? launch_rows<kRowsMxfp4, 1, 8>(a, s) : launch_rows<kRowsMxfp4, 4, 4>(a, s);
-  return a.m <= 16 ? launch_rows<kRowsMxfp8, 1, 8>(a, s) : launch_rows<kRowsMxfp8, 4, 4>(a, s);
+  a.vec_y = a.ldy % (a.y_type == kF32 ? 4 : 8) == 0 && aligned(a.y, 16);
+  return fmt == kRowsMxfp4 ? launch_fmt<kRowsMxfp4>(a, s) : launch_fmt<kRowsMxfp8>(a, s);
 }
 
 }  // namespace iq4

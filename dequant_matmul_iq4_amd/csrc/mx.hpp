@@ -36,7 +36,7 @@ struct MxArgs {
   void* y;
   int y_type;
   int64_t ldy;
-  int vec_y;                  // y and ldy allow stores of four consecutive columns
+  int vec_y;                  // y and ldy allow 16-byte stores
   // grouped: expert e's output rows are offsets[e] .. offsets[e + 1]
   const int32_t* offsets;
   int n_expert;

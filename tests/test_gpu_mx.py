@@ -155,6 +155,25 @@ def test_nan_scales_and_codes(fmt, m):
     assert np.isnan(y[:, 7]).all() and np.isnan(y[m - 2]).all() and np.isfinite(y[0, :7]).all()
 
 
+def test_whole_range_of_8_bit_codes():
+    """Every E4M3 code next to the largest ones: the largest product of a row is some 2^21
+    times its smallest, and the small ones must not be lost."""
+    note("mx gemm: E4M3 codes of all magnitudes")
+    n, m, k = 64, 200, 128
+    rng = np.random.default_rng(9)
+    cw, _ = exact_weights(3, n, k)
+    sw, sx = np.full((n, 4), 127, np.uint8), np.full((m, 4), 127, np.uint8)
+    c = rng.integers(0, 256, (m, k)).astype(np.uint8)
+    c[rng.random((m, k)) < 0.2] = 0x7E
+    c[:, 1::8] = rng.integers(1, 0x48, (m, k // 8))
+    c[(c & 0x7F) == 0x7F] = 0x80
+    w = packed(cw, sw, n, k)
+    for rows in (m, 7):
+        r, tol = bound(value("mxfp4", cw, sw), value("mxfp8", c[:rows], sx[:rows]), k, "f32")
+        y = product(w, (c[:rows], sx[:rows]), "mxfp8", n, k, rows, "f32")
+        assert np.all(np.abs(y - r) <= tol), float(np.max(np.abs(y - r) / tol))
+
+
 def test_far_scales():
     note("mx gemm: scales far apart, results that overflow or vanish")
     n, k, m = 32, 128, 4
