@@ -168,152 +168,247 @@ __device__ __forceinline__ void store_y4(const MxArgs& a, int64_t row, int64_t c
   }
 }
 
+// ---- rows by expert -------------------------------------------------------------------------
 // Expert e's rows [o0, o1), clamped to [0, m]: whatever the offsets hold, no row outside is
 // touched.
-__device__ __forceinline__ void expert_rows(const MxArgs& a, int e, int64_t& o0, int64_t& o1) {
-  o0 = o1 = 0;
-  if (e < a.n_expert) {
-    o0 = min(max((int64_t)a.offsets[e], (int64_t)0), a.m);
-    o1 = min(max((int64_t)a.offsets[e + 1], o0), a.m);
-  }
+__device__ __forceinline__ void expert_rows(const MxArgs& a, int e, int& o0, int& o1) {
+  const int m = (int)a.m, el = min(e, a.n_expert - 1);
+  o0 = min(max(a.offsets[el], 0), m);
+  o1 = min(max(a.offsets[el + 1], o0), m);
+  if (e >= a.n_expert) o1 = o0;
 }
 
-// Tiles of `bm` rows over all experts (every wave on its own, 64 experts a step).
-__device__ __forceinline__ int64_t count_tiles(const MxArgs& a, int bm) {
-  int64_t all = 0;
-  for (int e0 = 0; e0 < a.n_expert; e0 += 64) {
-    int64_t o0, o1;
-    expert_rows(a, e0 + (threadIdx.x & 63), o0, o1);
-    int mine = (int)((o1 - o0 + bm - 1) / bm);
-    for (int d = 32; d > 0; d >>= 1) mine += __shfl_xor(mine, d);
-    all += __builtin_amdgcn_readfirstlane(mine);
-  }
-  return all;
+// Sums of a value over lanes 0 .. own (one wave, without LDS: row shifts and broadcasts).
+__device__ __forceinline__ int scan64(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);  // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);  // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);  // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1, 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2, 3
+  return v;
 }
 
-// Tile `t` of the grouped rows: its expert, first row and rows (tiles per expert, a running
-// sum over the lanes, the first lane past t).  False: there are fewer tiles.
-__device__ __forceinline__ bool find_tile(const MxArgs& a, int64_t t, int bm, int& e, int64_t& row0, int& rows) {
-  const int lane = threadIdx.x & 63;
-  int64_t before = 0;
-  for (int e0 = 0; e0 < a.n_expert; e0 += 64) {
-    int64_t o0, o1;
-    expert_rows(a, e0 + lane, o0, o1);
-    const int mine = (int)((o1 - o0 + bm - 1) / bm);
-    int run = mine;
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(run, d);
-      if (lane >= d) run += up;
-    }
-    const uint64_t past = __ballot(before + run > t);
+// The tiles of `bm` rows that the experts' rows make, found by every wave on its own from the
+// offsets: lanes hold the experts 64 c + lane, four c at a time (all loads at once).
+constexpr int kGroupExperts = 256;
+struct ExpertTiles {
+  int row[4], rows[4], upto[4];  // first row, rows, tiles of the group's experts up to this one
+  int total;                     // tiles of the group
+};
+__device__ __forceinline__ ExpertTiles group_tiles(const MxArgs& a, int e0, int bm) {
+  ExpertTiles g;
+  int o0[4], o1[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) expert_rows(a, e0 + 64 * c + (threadIdx.x & 63), o0[c], o1[c]);
+  g.total = 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    g.row[c] = o0[c];
+    g.rows[c] = o1[c] - o0[c];
+    g.upto[c] = g.total + scan64((g.rows[c] + bm - 1) / bm);
+    g.total = __builtin_amdgcn_readlane(g.upto[c], 63);
+  }
+  return g;
+}
+// Tile `t` of the group: its expert, first row and rows.  False: t >= g.total.
+__device__ __forceinline__ bool group_find(ExpertTiles g, int e0, int t, int bm, int& e, int64_t& row0, int& rows) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint64_t past = __ballot(g.upto[c] > t);
     if (past) {
-      const int src = __builtin_ctzll(past);
-      const int64_t first = before + __shfl(run, src) - __shfl(mine, src);  // tiles before this expert
-      const int64_t b0 = __shfl((int)o0, src), b1 = __shfl((int)o1, src);
-      e = __builtin_amdgcn_readfirstlane(e0 + src);
-      row0 = __builtin_amdgcn_readfirstlane((int)(b0 + (t - first) * bm));
-      rows = __builtin_amdgcn_readfirstlane((int)min((int64_t)bm, b1 - row0));
+      const int l = __builtin_ctzll(past);
+      const int mine = __builtin_amdgcn_readlane(g.rows[c], l);
+      const int at = (t - (__builtin_amdgcn_readlane(g.upto[c], l) - (mine + bm - 1) / bm)) * bm;  // rows before it
+      e = e0 + 64 * c + l;
+      row0 = __builtin_amdgcn_readlane(g.row[c], l) + at;
+      rows = min(bm, mine - at);
       return true;
     }
-    before += __shfl(run, 63);
   }
   return false;
 }
 
-// Activation row of output row i (grouped), inside the buffer whatever `pairs` holds.
-__device__ __forceinline__ int64_t act_row(const MxArgs& a, int64_t i) {
-  const int64_t r = a.pairs ? a.pairs[i] / a.top_k : i;
-  return min(max(r, (int64_t)0), a.n_rows - 1);
+// Activation row of a pair (or of output row p, without pairs), inside the buffer whatever
+// `pairs` holds.
+__device__ __forceinline__ int64_t act_row(const MxArgs& a, int p) {
+  return min(max(a.pairs ? p / a.top_k : p, 0), (int)a.n_rows - 1);
 }
 
 // ---- few rows -----------------------------------------------------------------------------
-// One workgroup: 16 weight rows, MT x 16 rows of Y, all of k.  Its waves take turns at the
-// quads of four tiles along k (every operand straight from memory into registers) and their
-// sums are added through LDS in the waves' order.
-template <int FMT, int MT, int NW, bool GROUPED>
+// A workgroup of NW waves: NW / KS neighbouring row tiles of W against MT x 16 rows of Y, each
+// tile's k split over KS waves (wave s takes the quads s, s + KS, ...), whose sums are added
+// through LDS in the waves' order.  Every operand goes from memory straight into registers, the
+// rows one quad (four tiles along k) ahead of their products, the weights kAhead quads.
+//
+// Rows by expert: workgroup column i stands for output row i; it works if row i begins a tile
+// of its expert (MT x 16 rows from the expert's first on), so a wave finds its expert with one
+// comparison per expert and no sum over them.
+template <int FMT, int MT, int KS, int NW, bool GROUPED>
 __global__ void __launch_bounds__(64 * NW) mx_rows_kernel(MxArgs a) {
-  __shared__ f32x4 part[NW > 1 ? NW * MT * 64 : 1];
+  __shared__ f32x4 part[KS > 1 ? NW * MT * 64 : 1];
+  constexpr int kTiles = NW / KS, kWords = Act<FMT>::kWords / 4, kAhead = 2;
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t nt = mx_row_tiles(a.n);
-  const int64_t rt = blockIdx.x % nt, mt = blockIdx.x / nt;
+  const int slice = wave % KS;
+  const int64_t rt_n = mx_row_tiles(a.n), cols = (rt_n + kTiles - 1) / kTiles;
+  const int64_t col = blockIdx.x % cols, at = blockIdx.x / cols;
+  const int64_t rt_raw = col * kTiles + wave / KS;
+  const int64_t rt = min(rt_raw, rt_n - 1);  // past the last tile: the last again, not stored
   const uint8_t* W = a.W;
-  int64_t row0 = mt * (16 * MT);
+  int64_t row0 = at * (16 * MT);
   int rows = 16 * MT;
   if constexpr (GROUPED) {
-    int e;
-    if (!find_tile(a, mt, 16 * MT, e, row0, rows)) return;
+    const int i = (int)at;
+    int o0 = 0, o1 = 0, e = -1;
+    for (int e0 = 0; e0 < a.n_expert; e0 += kGroupExperts) {
+      int b0[4], b1[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) expert_rows(a, e0 + 64 * q + lane, b0[q], b1[q]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint64_t in = __ballot(b0[q] <= i && i < b1[q]);
+        if (in && e < 0) {
+          const int l = __builtin_ctzll(in);
+          e = e0 + 64 * q + l;
+          o0 = __builtin_amdgcn_readlane(b0[q], l);
+          o1 = __builtin_amdgcn_readlane(b1[q], l);
+        }
+      }
+    }
+    if (e < 0 || (i - o0) % (16 * MT)) return;
     W += e * a.w_stride;
+    row0 = i;
+    rows = min(rows, o1 - i);
   } else {
     rows = (int)min((int64_t)rows, a.m - row0);
   }
   const int kt_n = mx_k_tiles(a.k), kq_n = mx_k_quads(a.k);
   const uint8_t* wc = W + rt * kt_n * kMxTileBytes + lane * 16;
-  const uint8_t* wsc = W + mx_code_plane(a.n, a.k) + rt * kq_n * kMxScaleBytes + lane * 4;
+  const uint8_t* ws = W + mx_code_plane(a.n, a.k) + rt * kq_n * kMxScaleBytes + lane * 4;
+  struct WQuad {
+    u32x4 w[4];
+    uint32_t s;
+  };
+  struct XQuad {
+    u32x4 x[MT][4][kWords], s[MT];
+  };
+  // this wave's quad number u is slice + u KS (tiles past the last repeat it and are not multiplied)
+  const int u_n = (kq_n - slice + KS - 1) / KS;
+  auto load_w = [&](int u, WQuad& o) {
+    if (u >= u_n) return;
+    const int q = slice + u * KS;
+    o.s = *reinterpret_cast<const uint32_t*>(ws + (int64_t)q * kMxScaleBytes);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o.w[j] = *reinterpret_cast<const u32x4*>(wc + (int64_t)min(4 * q + j, kt_n - 1) * kMxTileBytes);
+  };
   const uint8_t* xc[MT];
   const uint8_t* xs[MT];
+  auto load_x = [&](int u, XQuad& o) {
+    if (u >= u_n) return;
+    const int q = slice + u * KS;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      o.s[i] = *reinterpret_cast<const u32x4*>(xs[i] + q * 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int h = 0; h < kWords; ++h)
+          o.x[i][j][h] = *reinterpret_cast<const u32x4*>(xc[i] + (int64_t)min(4 * q + j, kt_n - 1) * Act<FMT>::kTileBytes + 64 * h);
+    }
+  };
+  WQuad w[kAhead];
+  XQuad x[2];
+  // the pair ids first, then the first weights, then (the ids have arrived) the rows
+  int64_t xr[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    int64_t r = row0 + min(16 * i + c, rows - 1);  // rows past the last repeat it and are not stored
-    if constexpr (GROUPED) r = act_row(a, r);
+    xr[i] = row0 + min(16 * i + c, rows - 1);  // rows past the last repeat it and are not stored
+    if constexpr (GROUPED) {
+      if (a.pairs) xr[i] = a.pairs[xr[i]];
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) load_w(u, w[u]);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    int64_t r = xr[i];
+    if constexpr (GROUPED) r = act_row(a, (int)r);
     xc[i] = a.codes + r * a.ldq + 16 * g;
     xs[i] = a.scales + r * a.lds;
   }
+  load_x(0, x[0]);
   f32x4 acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int kq = wave; kq < kq_n; kq += NW) {
-    const uint32_t sw = *reinterpret_cast<const uint32_t*>(wsc + kq * kMxScaleBytes);
-    u32x4 sx[MT];
+  for (int u0 = 0; u0 < u_n; u0 += kAhead) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) sx[i] = *reinterpret_cast<const u32x4*>(xs[i] + kq * 16);
+    for (int v = 0; v < kAhead; ++v) {
+      const int u = u0 + v;
+      if (u >= u_n) break;
+      load_x(u + 1, x[(v + 1) & 1]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int kt = 4 * kq + j;
-      if (kt >= kt_n) break;
-      const u32x4 w = *reinterpret_cast<const u32x4*>(wc + kt * kMxTileBytes);
+      for (int j = 0; j < 4; ++j) {
+        if (4 * (slice + u * KS) + j >= kt_n) break;
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        u32x4 x[Act<FMT>::kWords / 4];
-#pragma unroll
-        for (int h = 0; h < Act<FMT>::kWords / 4; ++h)
-          x[h] = *reinterpret_cast<const u32x4*>(xc[i] + (int64_t)kt * Act<FMT>::kTileBytes + 64 * h);
-        acc[i] = mma<FMT>(j, w, sw, split<FMT>(x), sx[i][j] >> (8 * g), acc[i]);
+        for (int i = 0; i < MT; ++i)
+          acc[i] = mma<FMT>(j, w[v].w[j], w[v].s, split<FMT>(x[v & 1].x[i][j]), x[v & 1].s[i][j] >> (8 * g), acc[i]);
       }
+      load_w(u + kAhead, w[v]);
     }
   }
-  if constexpr (NW > 1) {
+  const bool mine = rt_raw < rt_n;
+  if constexpr (KS > 1) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) part[(wave * MT + i) * 64 + lane] = acc[i];
     __syncthreads();
-    // wave w adds up and stores the pieces w, w + NW, ...
-    for (int i = wave; i < MT; i += NW) {
-      f32x4 s = part[i * 64 + lane];
-      for (int w = 1; w < NW; ++w) {
-        const f32x4 p = part[(w * MT + i) * 64 + lane];
+    // wave s of a tile adds up and stores the pieces s, s + KS, ...
+    const int w0 = wave - slice;
+    for (int i = slice; i < MT; i += KS) {
+      f32x4 s = part[(w0 * MT + i) * 64 + lane];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s[q] = s[q] + p[q];
+      for (int w = 1; w < KS; ++w) {
+        const f32x4 v = part[((w0 + w) * MT + i) * 64 + lane];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] = s[k] + v[k];
       }
-      if (16 * i + c < rows) store_y4(a, row0 + 16 * i + c, rt * 16 + 4 * g, s);
+      if (mine && 16 * i + c < rows) store_y4(a, row0 + 16 * i + c, rt * 16 + 4 * g, s);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      if (16 * i + c < rows) store_y4(a, row0 + 16 * i + c, rt * 16 + 4 * g, acc[i]);
+      if (mine && 16 * i + c < rows) store_y4(a, row0 + 16 * i + c, rt * 16 + 4 * g, acc[i]);
   }
 }
 
-template <int FMT, int MT, int NW>
-static int launch_rows(const MxArgs& a, hipStream_t s) {
-  const int64_t nt = mx_row_tiles(a.n);
+template <int FMT, int MT, int KS, int NW>
+static int launch_rows_ks(const MxArgs& a, hipStream_t s) {
+  const int64_t cols = (mx_row_tiles(a.n) + NW / KS - 1) / (NW / KS);
   const bool grouped = a.offsets != nullptr;
-  // grouped: every expert's last tile may be partial
-  int64_t tiles = (a.m + 16 * MT - 1) / (16 * MT);
-  if (grouped) tiles = a.m / (16 * MT) + a.n_expert < a.m ? a.m / (16 * MT) + a.n_expert : a.m;
-  const dim3 grid((unsigned)(nt * tiles));
-  if (grouped) hipLaunchKernelGGL((mx_rows_kernel<FMT, MT, NW, true>), grid, dim3(64 * NW), 0, s, a);
-  else hipLaunchKernelGGL((mx_rows_kernel<FMT, MT, NW, false>), grid, dim3(64 * NW), 0, s, a);
+  const dim3 grid((unsigned)(cols * (grouped ? a.m : (a.m + 16 * MT - 1) / (16 * MT))));
+  if (grouped) hipLaunchKernelGGL((mx_rows_kernel<FMT, MT, KS, NW, true>), grid, dim3(64 * NW), 0, s, a);
+  else hipLaunchKernelGGL((mx_rows_kernel<FMT, MT, KS, NW, false>), grid, dim3(64 * NW), 0, s, a);
   return check_launch("mx_rows_kernel");
+}
+
+// Waves over k: as many as bring the device to 2,048 waves (eight a CU), and no more than
+// there are quads.  Depends on n and k alone for one matrix (MT = 1: every row of a call of up
+// to 16 is computed as a single row is).
+template <int FMT, int MT>
+static int launch_rows(const MxArgs& a, hipStream_t s) {
+  const int64_t waves = mx_row_tiles(a.n) * (a.offsets ? (a.m < a.n_expert ? a.m : a.n_expert) : 1);
+  const int kq_n = mx_k_quads(a.k);
+  int ks = 1;
+  while (ks < 8 && ks < kq_n && waves * ks < 2048) ks *= 2;
+  switch (ks) {
+    case 1: return launch_rows_ks<FMT, MT, 1, 4>(a, s);
+    case 2: return launch_rows_ks<FMT, MT, 2, 4>(a, s);
+    case 4: return launch_rows_ks<FMT, MT, 4, 4>(a, s);
+    default: return launch_rows_ks<FMT, MT, 8, 8>(a, s);
+  }
 }
 
 // ---- many rows ------------------------------------------------------------------------------
@@ -438,10 +533,19 @@ mx_tile_kernel(MxArgs a) {
   int rows;
   const uint8_t* W = a.W;
   if constexpr (GROUPED) {
-    const int64_t L = xcd_tile(blockIdx.x, count_tiles(a, T::kBM) * nt_n);
+    ExpertTiles g = group_tiles(a, 0, T::kBM);
+    int total = g.total;
+    for (int e0 = kGroupExperts; e0 < a.n_expert; e0 += kGroupExperts) total += group_tiles(a, e0, T::kBM).total;
+    const int64_t L = xcd_tile(blockIdx.x, total * nt_n);
     if (L < 0) return;
-    int e;
-    if (!find_tile(a, L / nt_n, T::kBM, e, row0, rows)) return;
+    int e, t = (int)(L / nt_n), e0 = 0;
+    while (t >= g.total) {
+      t -= g.total;
+      e0 += kGroupExperts;
+      if (e0 >= a.n_expert) return;
+      g = group_tiles(a, e0, T::kBM);
+    }
+    if (!group_find(g, e0, t, T::kBM, e, row0, rows)) return;
     nt = L % nt_n;
     W += e * a.w_stride;
   } else {
@@ -472,7 +576,7 @@ mx_tile_kernel(MxArgs a) {
     const int at = (wave * T::kCX + i) * 64 + lane, row = at / T::kChunks, place = at % T::kChunks;
     const int chunk = place ^ (FMT == kRowsMxfp4 ? (row >> 2) & 3 : (row >> 1) & 7);
     int64_t src = min(row, rows - 1);
-    if constexpr (GROUPED) src = act_row(a, row0 + src);
+    if constexpr (GROUPED) src = act_row(a, a.pairs ? a.pairs[row0 + src] : (int)(row0 + src));
     xo[i] = (uint32_t)(src * a.ldq) + 16 * chunk;
   }
   // scales: every wave issues the same number of copies, some of them twice (the same bytes
@@ -492,7 +596,7 @@ mx_tile_kernel(MxArgs a) {
     const int kb = (wave * T::kCXS + i) % (T::kXS / 1024);
     xsl[i] = T::kWS + kb * 1024;
     int64_t src = min(kb * 64 + lane, rows - 1);
-    if constexpr (GROUPED) src = act_row(a, row0 + src);
+    if constexpr (GROUPED) src = act_row(a, a.pairs ? a.pairs[row0 + src] : (int)(row0 + src));
     xso[i] = (uint32_t)(src * a.lds);
   }
   const uint8_t* xbase = scalar(a.codes + (GROUPED ? 0 : row0 * a.ldq));
@@ -669,8 +773,10 @@ static int launch_fmt(const MxArgs& a, hipStream_t s) {
   const int64_t tiles = ((a.n + 255) / 256) * ((a.m + 127) / 128);
   // the tile kernel's row offsets have 32 bits
   const int64_t span = (a.offsets ? a.n_rows : 256) * (a.ldq > a.lds ? a.ldq : a.lds);
-  if (a.m <= 16) return launch_rows<FMT, 1, 8>(a, s);
-  if (a.m <= 32 || span >= ((int64_t)1 << 32)) return launch_rows<FMT, 4, 4>(a, s);
+  const bool wide = span >= ((int64_t)1 << 32);
+  if (a.offsets ? a.m <= 4 * a.n_expert : a.m <= 16) return launch_rows<FMT, 1>(a, s);
+  if (wide) return launch_rows<FMT, 2>(a, s);
+  if (!a.offsets && a.m <= 32) return launch_rows<FMT, 2>(a, s);
   if (tiles >= 256) return launch_tiles<FMT, 4, 2, 2, 2, FMT == kRowsMxfp4 ? 3 : 2>(a, s);
   return launch_tiles<FMT, 1, 1, 2, 2, 4>(a, s);
 }
