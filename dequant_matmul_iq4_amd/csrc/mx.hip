@@ -231,7 +231,7 @@ __device__ __forceinline__ bool group_find(ExpertTiles g, int e0, int t, int bm,
 
 // Activation row of a pair (or of output row p, without pairs), inside the buffer whatever
 // `pairs` holds.
-__device__ __forceinline__ int64_t act_row(const MxArgs& a, int p) {
+__device__ __forceinline__ int act_row(const MxArgs& a, int p) {
   return min(max(a.pairs ? p / a.top_k : p, 0), (int)a.n_rows - 1);
 }
 
@@ -456,11 +456,57 @@ __device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
 // Workgroup b of a grid of >= 8 ceil(G / 8) to tile 0 .. G - 1 (or -1): hardware deals
 // workgroups round-robin to the eight XCDs, so each XCD gets a run of neighbouring tiles,
 // which share operands in its own L2.
-__device__ __forceinline__ int64_t xcd_tile(int64_t b, int64_t G) {
-  const int64_t per = (G + 7) / 8, i = b / 8;
+__device__ __forceinline__ int xcd_tile(uint32_t b, uint32_t G) {
+  const uint32_t per = (G + 7) / 8, i = b / 8;
   if (i >= per) return -1;
-  const int64_t L = (b % 8) * per + i;
-  return L < G ? L : -1;
+  const uint32_t L = (b % 8) * per + i;
+  return L < G ? (int)L : -1;
+}
+
+// Which tile of bn x bm outputs this workgroup makes: its place along n, its first row, its
+// rows, its matrix.  False: none.  (All counts fit 32 bits: a grid has fewer workgroups.)
+template <bool GROUPED>
+__device__ __forceinline__ bool place_tile(const MxArgs& a, int bn, int bm, int& nt, int64_t& row0, int& rows,
+                                           const uint8_t*& W) {
+  const uint32_t nt_n = ((uint32_t)a.n + bn - 1) / bn;
+  if constexpr (GROUPED) {
+    ExpertTiles g = group_tiles(a, 0, bm);
+    int total = g.total;
+    for (int e0 = kGroupExperts; e0 < a.n_expert; e0 += kGroupExperts) total += group_tiles(a, e0, bm).total;
+    const int L = xcd_tile(blockIdx.x, (uint32_t)total * nt_n);
+    if (L < 0) return false;
+    int e, t = (int)((uint32_t)L / nt_n), e0 = 0;
+    nt = L - t * (int)nt_n;
+    while (t >= g.total) {
+      t -= g.total;
+      e0 += kGroupExperts;
+      if (e0 >= a.n_expert) return false;
+      g = group_tiles(a, e0, bm);
+    }
+    if (!group_find(g, e0, t, bm, e, row0, rows)) return false;
+    W += e * a.w_stride;
+  } else {
+    const uint32_t mt_n = ((uint32_t)a.m + bm - 1) / bm;
+    const int L = xcd_tile(blockIdx.x, mt_n * nt_n);
+    if (L < 0) return false;
+    // bands of eight row tiles, walked row tile first: the 32 CUs of an XCD hold about
+    // 8 x 4 tiles and read 12 operand panels for them
+    const uint32_t band = (uint32_t)L / (8 * nt_n), in = (uint32_t)L - band * 8 * nt_n;
+    const uint32_t high = min(8u, mt_n - 8 * band);
+    nt = (int)(high == 8 ? in / 8 : in / high);
+    const uint32_t mt = 8 * band + in - (uint32_t)nt * high;
+    row0 = (int64_t)mt * bm;
+    rows = (int)min((int64_t)bm, a.m - row0);
+  }
+  return true;
+}
+
+static unsigned tile_grid(const MxArgs& a, int bn, int bm) {
+  const int64_t nt = (a.n + bn - 1) / bn;
+  int64_t tiles = (a.m + bm - 1) / bm;
+  // by expert: each expert's last tile may be partial
+  if (a.offsets) tiles = a.m / bm + a.n_expert < a.m ? a.m / bm + a.n_expert : a.m;
+  return (unsigned)((nt * tiles + 7) / 8 * 8);
 }
 
 template <int FMT, int FN, int FM, int WN, int WM, int S>
@@ -490,29 +536,58 @@ struct Tile {
 
 // `rows` x `cols` values in LDS (rows of PITCH, at most 32 x COLS) to Y from (row0, col0) on,
 // by one wave: eight columns a lane.
-template <int COLS, int PITCH>
+template <int TYPE, int COLS, int PITCH>
 __device__ __forceinline__ void store_rows_piece(const MxArgs& a, const float* part, int64_t row0, int rows, int64_t col0,
                                                  int cols) {
   constexpr int kLanes = COLS / 8, kStep = 64 / kLanes;  // lanes a row, rows a step
-  const int lane = threadIdx.x & 63, c = 8 * (lane % kLanes);
-#pragma unroll 1
-  for (int r = lane / kLanes; r < rows; r += kStep) {
-    if (c >= cols) continue;
-    float v[8];
-    const f32x4 p = *reinterpret_cast<const f32x4*>(part + r * PITCH + c), q = *reinterpret_cast<const f32x4*>(part + r * PITCH + c + 4);
+  const int lane = threadIdx.x & 63, c = 8 * (lane % kLanes), r0 = lane / kLanes;
+  const float* from = part + r0 * PITCH + c;
+  const int64_t at = (row0 + r0) * a.ldy + col0 + c;
+  if (a.vec_y && cols == COLS) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = p[i], v[4 + i] = q[i];
-    const int64_t at = (row0 + r) * a.ldy + col0 + c;
-    if (a.vec_y && c + 8 <= cols) {
-      store8(a.y_type, a.y, at, v);
-    } else {
+    for (int r = 0; r < 32; r += kStep) {
+      float v[8];
+      const f32x4 p = *reinterpret_cast<const f32x4*>(from + r * PITCH), q = *reinterpret_cast<const f32x4*>(from + r * PITCH + 4);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (c + i >= cols) break;
-        if (a.y_type == kF32) static_cast<float*>(a.y)[at + i] = v[i];
-        else static_cast<uint16_t*>(a.y)[at + i] = (uint16_t)(a.y_type == kF16 ? pack2<kF16>(v[i], v[i]) : pack2<kBF16>(v[i], v[i]));
-      }
+      for (int i = 0; i < 4; ++i) v[i] = p[i], v[4 + i] = q[i];
+      if (r0 + r < rows) store8<TYPE>(a.y, at + r * a.ldy, v);
     }
+    return;
+  }
+#pragma unroll 1
+  for (int r = 0; r0 + r < rows; r += kStep)
+#pragma unroll 1
+    for (int i = 0; i < 8 && c + i < cols; ++i) {
+      const float v = from[r * PITCH + i];
+      if constexpr (TYPE == kF32) static_cast<float*>(a.y)[at + r * a.ldy + i] = v;
+      else static_cast<uint16_t*>(a.y)[at + r * a.ldy + i] = (uint16_t)pack2<TYPE>(v, v);
+    }
+}
+
+// A wave's pieces to Y through LDS (`part`, its own), 32 rows at a time, so that the rows are
+// written in runs of 64 FN or 128 FN bytes (a lane holds four columns of 32 different rows;
+// stored from the registers, 32 bytes a row and store, the long prompt took 450 us for 432).
+// `first`: the wave's first row in the tile, `col0` its first column.
+template <int FN, int FM>
+__device__ __forceinline__ void store_tile(const MxArgs& a, float* part, const f32x16 (&acc)[FN][FM], int64_t row0, int first,
+                                           int rows, int64_t col0) {
+  constexpr int kCols = 32 * FN, kPitch = kCols + 4;
+  const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+  const int cols = (int)min((int64_t)kCols, a.n - col0);
+#pragma unroll
+  for (int m = 0; m < FM; ++m) {
+    if (first + 32 * m >= rows || cols <= 0) break;
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(part + r * kPitch + 32 * n + 8 * q + 4 * h) =
+            f32x4{acc[n][m][4 * q], acc[n][m][4 * q + 1], acc[n][m][4 * q + 2], acc[n][m][4 * q + 3]};
+    const int64_t to = row0 + first + 32 * m;
+    const int left = min(32, rows - first - 32 * m);
+    if (a.y_type == kF32) store_rows_piece<kF32, kCols, kPitch>(a, part, to, left, col0, cols);
+    else if (a.y_type == kF16) store_rows_piece<kF16, kCols, kPitch>(a, part, to, left, col0, cols);
+    else store_rows_piece<kBF16, kCols, kPitch>(a, part, to, left, col0, cols);
   }
 }
 
@@ -527,57 +602,28 @@ mx_tile_kernel(MxArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave % WN, wm = wave / WN;
 
-  // ---- which tile ---------------------------------------------------------------------
-  const int64_t nt_n = (a.n + T::kBN - 1) / T::kBN;
-  int64_t nt, row0;
-  int rows;
+  int nt, rows;
+  int64_t row0;
   const uint8_t* W = a.W;
-  if constexpr (GROUPED) {
-    ExpertTiles g = group_tiles(a, 0, T::kBM);
-    int total = g.total;
-    for (int e0 = kGroupExperts; e0 < a.n_expert; e0 += kGroupExperts) total += group_tiles(a, e0, T::kBM).total;
-    const int64_t L = xcd_tile(blockIdx.x, total * nt_n);
-    if (L < 0) return;
-    int e, t = (int)(L / nt_n), e0 = 0;
-    while (t >= g.total) {
-      t -= g.total;
-      e0 += kGroupExperts;
-      if (e0 >= a.n_expert) return;
-      g = group_tiles(a, e0, T::kBM);
-    }
-    if (!group_find(g, e0, t, T::kBM, e, row0, rows)) return;
-    nt = L % nt_n;
-    W += e * a.w_stride;
-  } else {
-    const int64_t mt_n = (a.m + T::kBM - 1) / T::kBM;
-    const int64_t L = xcd_tile(blockIdx.x, mt_n * nt_n);
-    if (L < 0) return;
-    // bands of eight row tiles, walked row tile first: the 32 CUs of an XCD hold about
-    // 8 x 4 tiles and read 12 operand panels for them
-    const int64_t band = L / (8 * nt_n), in = L - band * 8 * nt_n;
-    const int64_t high = min((int64_t)8, mt_n - 8 * band);
-    row0 = (8 * band + in % high) * T::kBM;
-    nt = in / high;
-    rows = (int)min((int64_t)T::kBM, a.m - row0);
-  }
+  if (!place_tile<GROUPED>(a, T::kBN, T::kBM, nt, row0, rows, W)) return;
   const int kt_n = mx_k_tiles(a.k), kq_n = mx_k_quads(a.k);
-  const int64_t rt_n = mx_row_tiles(a.n), rt0 = nt * (T::kBN / 16);
+  const int rt_n = (int)mx_row_tiles(a.n), rt0 = nt * (T::kBN / 16);
   const uint32_t lds0 = lds_offset(lds);
 
   // ---- what this lane copies ------------------------------------------------------------
   // W: tiles wave * kCW ..; those past n repeat the last one (read in bounds, not stored)
   const uint8_t* wt[T::kCW];
 #pragma unroll
-  for (int i = 0; i < T::kCW; ++i) wt[i] = scalar(W + min(rt0 + wave * T::kCW + i, rt_n - 1) * kt_n * kMxTileBytes);
+  for (int i = 0; i < T::kCW; ++i) wt[i] = scalar(W + (int64_t)min(rt0 + wave * T::kCW + i, rt_n - 1) * (kt_n * (int64_t)kMxTileBytes));
   // X: kilobytes wave * kCX ..; rows past the last repeat it
   uint32_t xo[T::kCX];
 #pragma unroll
   for (int i = 0; i < T::kCX; ++i) {
     const int at = (wave * T::kCX + i) * 64 + lane, row = at / T::kChunks, place = at % T::kChunks;
     const int chunk = place ^ (FMT == kRowsMxfp4 ? (row >> 2) & 3 : (row >> 1) & 7);
-    int64_t src = min(row, rows - 1);
-    if constexpr (GROUPED) src = act_row(a, a.pairs ? a.pairs[row0 + src] : (int)(row0 + src));
-    xo[i] = (uint32_t)(src * a.ldq) + 16 * chunk;
+    uint32_t src = min(row, rows - 1);
+    if constexpr (GROUPED) src = (uint32_t)act_row(a, a.pairs ? a.pairs[row0 + src] : (int)(row0 + src));
+    xo[i] = src * (uint32_t)a.ldq + 16 * chunk;
   }
   // scales: every wave issues the same number of copies, some of them twice (the same bytes
   // to the same place)
@@ -588,20 +634,20 @@ mx_tile_kernel(MxArgs a) {
     const int kb = (wave * T::kCWS + i) % (T::kWS / 1024);
     wsl[i] = kb * 1024;
     // four row tiles a kilobyte, relative to the workgroup's first
-    const int64_t rt = min(rt0 + 4 * kb + (lane >> 4), rt_n - 1) - rt0;
-    wso[i] = (uint32_t)(rt * kq_n * kMxScaleBytes) + 16 * (lane & 15);
+    const int rt = min(rt0 + 4 * kb + (lane >> 4), rt_n - 1) - rt0;
+    wso[i] = (uint32_t)(rt * kq_n) * kMxScaleBytes + 16 * (lane & 15);
   }
 #pragma unroll
   for (int i = 0; i < T::kCXS; ++i) {
     const int kb = (wave * T::kCXS + i) % (T::kXS / 1024);
     xsl[i] = T::kWS + kb * 1024;
-    int64_t src = min(kb * 64 + lane, rows - 1);
-    if constexpr (GROUPED) src = act_row(a, a.pairs ? a.pairs[row0 + src] : (int)(row0 + src));
-    xso[i] = (uint32_t)(src * a.lds);
+    uint32_t src = min(kb * 64 + lane, rows - 1);
+    if constexpr (GROUPED) src = (uint32_t)act_row(a, a.pairs ? a.pairs[row0 + src] : (int)(row0 + src));
+    xso[i] = src * (uint32_t)a.lds;
   }
   const uint8_t* xbase = scalar(a.codes + (GROUPED ? 0 : row0 * a.ldq));
   const uint8_t* xsbase = scalar(a.scales + (GROUPED ? 0 : row0 * a.lds));
-  const uint8_t* wsbase = scalar(W + mx_code_plane(a.n, a.k) + rt0 * kq_n * kMxScaleBytes);
+  const uint8_t* wsbase = scalar(W + mx_code_plane(a.n, a.k) + (int64_t)rt0 * (kq_n * kMxScaleBytes));
 
   // (steps and quads past the last copy it again: the counts hold to the end)
   auto copy_part = [&](int t, int i0, int i1) {  // copies i0 .. i1 - 1 of this wave's kC
@@ -730,39 +776,19 @@ mx_tile_kernel(MxArgs a) {
     if (t + 4 >= kt_n) break;
   }
   // ---- store ------------------------------------------------------------------------------------
-  // Through LDS, a row piece at a time and each wave in a part of its own, so that the rows are
-  // written in runs of 64 FN or 128 FN bytes (a lane holds four columns of 32 different rows).
   wait_copies<0>();
   __builtin_amdgcn_s_barrier();  // no copy lands in LDS any more, and no wave reads the stages
   asm volatile("" ::: "memory");
-  constexpr int kCols = 32 * FN, kPitch = kCols + 4;
-  static_assert(T::kWaves * 32 * kPitch * 4 <= T::kLds, "the parts fit");
-  float* part = reinterpret_cast<float*>(lds) + wave * 32 * kPitch;
-  const int64_t col0 = nt * T::kBN + kCols * wn;
-  const int cols = (int)min((int64_t)kCols, a.n - col0);
-#pragma unroll
-  for (int m = 0; m < FM; ++m) {
-    const int first = 32 * (FM * wm + m);
-    if (first >= rows || cols <= 0) break;
-#pragma unroll
-    for (int n = 0; n < FN; ++n)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4*>(part + r * kPitch + 32 * n + 8 * q + 4 * h) =
-            f32x4{acc[n][m][4 * q], acc[n][m][4 * q + 1], acc[n][m][4 * q + 2], acc[n][m][4 * q + 3]};
-    store_rows_piece<kCols, kPitch>(a, part, row0 + first, min(32, rows - first), col0, cols);
-  }
+  constexpr int kPart = 32 * (32 * FN + 4);
+  static_assert(T::kWaves * kPart * 4 <= T::kLds, "the parts fit");
+  store_tile<FN, FM>(a, reinterpret_cast<float*>(lds) + wave * kPart, acc, row0, 32 * FM * wm, rows, (int64_t)nt * T::kBN + 32 * FN * wn);
 }
 
 template <int FMT, int FN, int FM, int WN, int WM, int S>
 static int launch_tiles(const MxArgs& a, hipStream_t s) {
   using T = Tile<FMT, FN, FM, WN, WM, S>;
-  const int64_t nt = (a.n + T::kBN - 1) / T::kBN;
-  const bool grouped = a.offsets != nullptr;
-  int64_t tiles = (a.m + T::kBM - 1) / T::kBM;
-  if (grouped) tiles = a.m / T::kBM + a.n_expert < a.m ? a.m / T::kBM + a.n_expert : a.m;
-  const dim3 grid((unsigned)((nt * tiles + 7) / 8 * 8));
-  if (grouped) hipLaunchKernelGGL((mx_tile_kernel<FMT, FN, FM, WN, WM, S, true>), grid, dim3(64 * T::kWaves), 0, s, a);
+  const dim3 grid(tile_grid(a, T::kBN, T::kBM));
+  if (a.offsets) hipLaunchKernelGGL((mx_tile_kernel<FMT, FN, FM, WN, WM, S, true>), grid, dim3(64 * T::kWaves), 0, s, a);
   else hipLaunchKernelGGL((mx_tile_kernel<FMT, FN, FM, WN, WM, S, false>), grid, dim3(64 * T::kWaves), 0, s, a);
   return check_launch("mx_tile_kernel");
 }
