@@ -232,7 +232,10 @@ __device__ __forceinline__ bool group_find(ExpertTiles g, int e0, int t, int bm,
 // Activation row of a pair (or of output row p, without pairs), inside the buffer whatever
 // `pairs` holds.
 __device__ __forceinline__ int act_row(const MxArgs& a, int p) {
-  return min(max(a.pairs ? p / a.top_k : p, 0), (int)a.n_rows - 1);
+  // p / top_k: p is below 2^21, so (p + 1/2) / top_k is further from a whole number (1 / (2 top_k))
+  // than the product's error (2^-23 of it)
+  const int r = a.pairs ? (int)(((float)p + 0.5f) * a.inv_top) : p;
+  return min(max(r, 0), (int)a.n_rows - 1);
 }
 
 // ---- few rows -----------------------------------------------------------------------------
@@ -615,20 +618,28 @@ mx_tile_kernel(MxArgs a) {
   const uint8_t* wt[T::kCW];
 #pragma unroll
   for (int i = 0; i < T::kCW; ++i) wt[i] = scalar(W + (int64_t)min(rt0 + wave * T::kCW + i, rt_n - 1) * (kt_n * (int64_t)kMxTileBytes));
-  // X: kilobytes wave * kCX ..; rows past the last repeat it
-  uint32_t xo[T::kCX];
+  // X: kilobytes wave * kCX ..; rows past the last repeat it.  (By expert: the pair ids are
+  // loaded here, and used after W's first copies have been issued.)
+  uint32_t xo[T::kCX], xso[T::kCXS];
+  int xsl[T::kCXS];
+  auto row_of = [&](int row) -> uint32_t {
+    const uint32_t src = min(row, rows - 1);
+    if constexpr (GROUPED) return a.pairs ? (uint32_t)a.pairs[row0 + src] : (uint32_t)row0 + src;
+    return src;
+  };
 #pragma unroll
-  for (int i = 0; i < T::kCX; ++i) {
-    const int at = (wave * T::kCX + i) * 64 + lane, row = at / T::kChunks, place = at % T::kChunks;
-    const int chunk = place ^ (FMT == kRowsMxfp4 ? (row >> 2) & 3 : (row >> 1) & 7);
-    uint32_t src = min(row, rows - 1);
-    if constexpr (GROUPED) src = (uint32_t)act_row(a, a.pairs ? a.pairs[row0 + src] : (int)(row0 + src));
-    xo[i] = src * (uint32_t)a.ldq + 16 * chunk;
+  for (int i = 0; i < T::kCX; ++i) xo[i] = row_of(((wave * T::kCX + i) * 64 + lane) / T::kChunks);
+#pragma unroll
+  for (int i = 0; i < T::kCXS; ++i) {
+    const int kb = (wave * T::kCXS + i) % (T::kXS / 1024);
+    xsl[i] = T::kWS + kb * 1024;
+    xso[i] = row_of(kb * 64 + lane);
   }
+  __builtin_amdgcn_sched_barrier(0);
   // scales: every wave issues the same number of copies, some of them twice (the same bytes
   // to the same place)
-  uint32_t wso[T::kCWS], xso[T::kCXS];
-  int wsl[T::kCWS], xsl[T::kCXS];
+  uint32_t wso[T::kCWS];
+  int wsl[T::kCWS];
 #pragma unroll
   for (int i = 0; i < T::kCWS; ++i) {
     const int kb = (wave * T::kCWS + i) % (T::kWS / 1024);
@@ -636,14 +647,6 @@ mx_tile_kernel(MxArgs a) {
     // four row tiles a kilobyte, relative to the workgroup's first
     const int rt = min(rt0 + 4 * kb + (lane >> 4), rt_n - 1) - rt0;
     wso[i] = (uint32_t)(rt * kq_n) * kMxScaleBytes + 16 * (lane & 15);
-  }
-#pragma unroll
-  for (int i = 0; i < T::kCXS; ++i) {
-    const int kb = (wave * T::kCXS + i) % (T::kXS / 1024);
-    xsl[i] = T::kWS + kb * 1024;
-    uint32_t src = min(kb * 64 + lane, rows - 1);
-    if constexpr (GROUPED) src = (uint32_t)act_row(a, a.pairs ? a.pairs[row0 + src] : (int)(row0 + src));
-    xso[i] = src * (uint32_t)a.lds;
   }
   const uint8_t* xbase = scalar(a.codes + (GROUPED ? 0 : row0 * a.ldq));
   const uint8_t* xsbase = scalar(a.scales + (GROUPED ? 0 : row0 * a.lds));
@@ -660,14 +663,13 @@ mx_tile_kernel(MxArgs a) {
       else copy16(xbase + (int64_t)k * T::kRowB, xo[i - T::kCW], st + T::kWBytes + (wave * T::kCX + i - T::kCW) * 1024);
     }
   };
-  auto copy_stage = [&](int t) { copy_part(t, 0, T::kC); };
-  auto copy_scales = [&](int q) {
-    const uint32_t st = lds0 + S * T::kStage;
-    const int k = min(q, kq_n - 1);
+  auto copy_wscales = [&](int q) {
 #pragma unroll
-    for (int i = 0; i < T::kCWS; ++i) copy16(wsbase + (int64_t)k * kMxScaleBytes, wso[i], st + wsl[i]);
+    for (int i = 0; i < T::kCWS; ++i) copy16(wsbase + (int64_t)min(q, kq_n - 1) * kMxScaleBytes, wso[i], lds0 + S * T::kStage + wsl[i]);
+  };
+  auto copy_xscales = [&](int q) {
 #pragma unroll
-    for (int i = 0; i < T::kCXS; ++i) copy16(xsbase + (int64_t)k * 16, xso[i], st + xsl[i]);
+    for (int i = 0; i < T::kCXS; ++i) copy16(xsbase + (int64_t)min(q, kq_n - 1) * 16, xso[i], lds0 + S * T::kStage + xsl[i]);
   };
 
   // ---- operands from LDS --------------------------------------------------------------------
@@ -735,13 +737,29 @@ mx_tile_kernel(MxArgs a) {
   };
 
   // ---- main loop ------------------------------------------------------------------------------
-  copy_scales(0);
+  copy_wscales(0);
 #pragma unroll
-  for (int t = 0; t < T::kD; ++t) copy_stage(t);
-  wait_copies<(T::kD - 1) * T::kC>();
+  for (int t = 0; t < T::kD; ++t) copy_part(t, 0, T::kCW);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < T::kCX; ++i) {
+    const int at = (wave * T::kCX + i) * 64 + lane, row = at / T::kChunks, place = at % T::kChunks;
+    const int chunk = place ^ (FMT == kRowsMxfp4 ? (row >> 2) & 3 : (row >> 1) & 7);
+    if constexpr (GROUPED) xo[i] = act_row(a, (int)xo[i]);
+    xo[i] = xo[i] * (uint32_t)a.ldq + 16 * chunk;
+  }
+#pragma unroll
+  for (int i = 0; i < T::kCXS; ++i) {
+    if constexpr (GROUPED) xso[i] = act_row(a, (int)xso[i]);
+    xso[i] *= (uint32_t)a.lds;
+  }
+  copy_xscales(0);
+#pragma unroll
+  for (int t = 0; t < T::kD; ++t) copy_part(t, T::kCW, T::kC);
+  wait_copies<(T::kD - 1) * T::kCX>();  // younger than stage 0 and the scales
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  copy_stage(T::kD);
+  copy_part(T::kD, 0, T::kC);
   Ops o0, o1;
   Scales sc, next;
   read_scales(sc);
@@ -759,7 +777,10 @@ mx_tile_kernel(MxArgs a) {
     if constexpr (j == 3) read_scales(next);
     __builtin_amdgcn_sched_barrier(0);
     multiply(jj, std::integral_constant<int, 1>{}, o1, sc, [&](int m) {
-      if (j == 0 && m == 0) copy_scales(t / 4 + 1);  // every wave has read this quad's
+      if (j == 0 && m == 0) {  // every wave has read this quad's
+        copy_wscales(t / 4 + 1);
+        copy_xscales(t / 4 + 1);
+      }
       copy_part(t + 1 + T::kD, m * T::kC / FM, (m + 1) * T::kC / FM);
     });
     arrived(o0);
@@ -808,6 +829,7 @@ static int launch_fmt(const MxArgs& a, hipStream_t s) {
 }
 
 int launch_mx_gemm(MxArgs a, int fmt, hipStream_t s) {
+  a.inv_top = a.pairs ? 1.0f / (float)a.top_k : 0.0f;
   a.vec_y = a.ldy % (a.y_type == kF32 ? 4 : 8) == 0 && aligned(a.y, 16);
   return fmt == kRowsMxfp4 ? launch_fmt<kRowsMxfp4>(a, s) : launch_fmt<kRowsMxfp8>(a, s);
 }

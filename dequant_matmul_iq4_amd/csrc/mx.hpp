@@ -42,6 +42,7 @@ struct MxArgs {
   int n_expert;
   const int32_t* pairs;       // activation row of output row i: pairs[i] / top_k (null: i)
   int top_k;
+  float inv_top;              // 1 / top_k (set by the launcher)
 };
 
 int launch_mx_gemm(MxArgs a, int fmt, hipStream_t s);
