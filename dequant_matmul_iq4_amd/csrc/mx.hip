@@ -387,30 +387,28 @@ __global__ void __launch_bounds__(64 * NW) mx_rows_kernel(MxArgs a) {
   }
 }
 
-template <int FMT, int MT, int KS, int NW>
+template <int FMT, int MT, int KS, int NW, bool GROUPED>
 static int launch_rows_ks(const MxArgs& a, hipStream_t s) {
   const int64_t cols = (mx_row_tiles(a.n) + NW / KS - 1) / (NW / KS);
-  const bool grouped = a.offsets != nullptr;
-  const dim3 grid((unsigned)(cols * (grouped ? a.m : (a.m + 16 * MT - 1) / (16 * MT))));
-  if (grouped) hipLaunchKernelGGL((mx_rows_kernel<FMT, MT, KS, NW, true>), grid, dim3(64 * NW), 0, s, a);
-  else hipLaunchKernelGGL((mx_rows_kernel<FMT, MT, KS, NW, false>), grid, dim3(64 * NW), 0, s, a);
+  const dim3 grid((unsigned)(cols * (GROUPED ? a.m : (a.m + 16 * MT - 1) / (16 * MT))));
+  hipLaunchKernelGGL((mx_rows_kernel<FMT, MT, KS, NW, GROUPED>), grid, dim3(64 * NW), 0, s, a);
   return check_launch("mx_rows_kernel");
 }
 
 // Waves over k: as many as bring the device to 2,048 waves (eight a CU), and no more than
 // there are quads.  Depends on n and k alone for one matrix (MT = 1: every row of a call of up
 // to 16 is computed as a single row is).
-template <int FMT, int MT>
+template <int FMT, int MT, bool GROUPED>
 static int launch_rows(const MxArgs& a, hipStream_t s) {
-  const int64_t waves = mx_row_tiles(a.n) * (a.offsets ? (a.m < a.n_expert ? a.m : a.n_expert) : 1);
+  const int64_t waves = mx_row_tiles(a.n) * (GROUPED ? (a.m < a.n_expert ? a.m : a.n_expert) : 1);
   const int kq_n = mx_k_quads(a.k);
   int ks = 1;
   while (ks < 8 && ks < kq_n && waves * ks < 2048) ks *= 2;
   switch (ks) {
-    case 1: return launch_rows_ks<FMT, MT, 1, 4>(a, s);
-    case 2: return launch_rows_ks<FMT, MT, 2, 4>(a, s);
-    case 4: return launch_rows_ks<FMT, MT, 4, 4>(a, s);
-    default: return launch_rows_ks<FMT, MT, 8, 8>(a, s);
+    case 1: return launch_rows_ks<FMT, MT, 1, 4, GROUPED>(a, s);
+    case 2: return launch_rows_ks<FMT, MT, 2, 4, GROUPED>(a, s);
+    case 4: return launch_rows_ks<FMT, MT, 4, 4, GROUPED>(a, s);
+    default: return launch_rows_ks<FMT, MT, 8, 8, GROUPED>(a, s);
   }
 }
 
@@ -535,6 +533,39 @@ struct Tile {
   // stages t+2 .. t+D, and the next quad's scales if they were issued since (before stage
   // u+D's copies, after the barrier that begins place u % 4 == 1).
   static constexpr int in_flight(int j) { return (kD - 1) * kC + (j >= 1 && j < kD ? kCWS + kCXS : 0); }
+  // Copies that may still be in flight when step 0 begins.  The first stages are copied W of all
+  // of them, then X of all of them (X's addresses are known later): younger than stage 0's X is
+  // X of the others, but with three stages ahead step 0's own wait counts whole stages behind
+  // stage 1, so stage 1's X has to be there by now.
+  static constexpr int kFirst = kD == 3 ? kCX : (kD - 1) * kCX;
+
+  // The counts, checked against the order in which a wave issues its copies: whatever step t
+  // waits for must be older than the copies it lets fly.
+  static constexpr bool counts_hold() {
+    int op[512] = {}, n = 0;  // what each copy brings: a stage, or 1000 + a quad's scales
+    int done = 0;             // copies before this one are known to have landed (they land in order)
+    auto put = [&](int count, int what) {
+      for (int i = 0; i < count; ++i) op[n++] = what;
+    };
+    auto landed = [&](int flying, int stage, int quad) {  // all stages and quads up to these
+      if (n - flying > done) done = n - flying;
+      for (int i = done; i < n; ++i)
+        if (op[i] >= 1000 ? op[i] <= 1000 + quad : op[i] <= stage) return false;
+      return true;
+    };
+    put(kCWS, 1000);
+    for (int t = 0; t < kD; ++t) put(kCW, t);
+    put(kCXS, 1000);
+    for (int t = 0; t < kD; ++t) put(kCX, t);
+    if (!landed(kFirst, 0, 0)) return false;
+    put(kC, kD);
+    for (int t = 0; t < 16; ++t) {
+      if (!landed(in_flight(t % 4), t + 1, (t + 1) / 4)) return false;
+      if (t % 4 == 0) put(kCWS + kCXS, 1000 + t / 4 + 1);
+      put(kC, t + 1 + kD);
+    }
+    return true;
+  }
 };
 
 // Eight values past the L2 (nothing here reads Y again): the long prompt's 374 MB of results
@@ -770,7 +801,8 @@ mx_tile_kernel(MxArgs a) {
   copy_xscales(0);
 #pragma unroll
   for (int t = 0; t < T::kD; ++t) copy_part(t, T::kCW, T::kC);
-  wait_copies<(T::kD - 1) * T::kCX>();  // younger than stage 0 and the scales
+  static_assert(T::counts_hold(), "the copies in flight");
+  wait_copies<T::kFirst>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   copy_part(T::kD, 0, T::kC);
@@ -829,33 +861,58 @@ mx_tile_kernel(MxArgs a) {
   store_tile<FN, FM>(a, reinterpret_cast<float*>(lds) + wave * kPart, acc, row0, 32 * FM * wm, rows, (int64_t)nt * T::kBN + 32 * FN * wn);
 }
 
-template <int FMT, int FN, int FM, int WN, int WM, int S>
+template <int FMT, int FN, int FM, int WN, int WM, int S, bool GROUPED>
 static int launch_tiles(const MxArgs& a, hipStream_t s) {
   using T = Tile<FMT, FN, FM, WN, WM, S>;
-  const dim3 grid(tile_grid(a, T::kBN, T::kBM));
-  if (a.offsets) hipLaunchKernelGGL((mx_tile_kernel<FMT, FN, FM, WN, WM, S, true>), grid, dim3(64 * T::kWaves), 0, s, a);
-  else hipLaunchKernelGGL((mx_tile_kernel<FMT, FN, FM, WN, WM, S, false>), grid, dim3(64 * T::kWaves), 0, s, a);
+  hipLaunchKernelGGL((mx_tile_kernel<FMT, FN, FM, WN, WM, S, GROUPED>), dim3(tile_grid(a, T::kBN, T::kBM)), dim3(64 * T::kWaves), 0, s, a);
   return check_launch("mx_tile_kernel");
 }
 
-// Which kernel: see the comments at each.
+// Which kernel, by the workgroups each tile gives (times in us on an MI355X, MXFP4 unless
+// MXFP8 is named).  The larger tile reads less per product; below some 160-220 workgroups of it
+// the 256 CUs are not filled and the next smaller one is faster:
+//   256 x 128 from 224: 14336 x 4096, m = 512 (224): 22.0, 128 x 128 23.3; 5000 x 2592,
+//     m = 1024 (160): 20.9 for 17.9.  MXFP8, same m: 50.2 for 52.8; m = 333 (168): 47.3, 128 x 64 43.7.
+//   128 x 128 from 160, MXFP4 only: 4096 x 4096, m = 1024 (256): 14.9, 128 x 64 17.4; m = 512
+//     (128): 12.8 for 10.7.  MXFP8, m = 1024: 35.2 for 32.9.
+//   128 x 64 from 160, else 64 x 64: 4096 x 4096, m = 333 (192): 9.9 for 11.2; m = 256 (128): 9.8 for 8.9.
+//   Up to 32 rows straight from memory unless 64 x 64 fills the CUs: 4096 x 4096, m = 32
+//     (64): 5.2 for 6.2; 14336 x 4096 (224): 14.6 for 8.9.
 template <int FMT>
-static int launch_fmt(const MxArgs& a, hipStream_t s) {
-  const int64_t tiles = ((a.n + 255) / 256) * ((a.m + 127) / 128);
+static int launch_dense(const MxArgs& a, hipStream_t s) {
+  constexpr bool k4 = FMT == kRowsMxfp4;
+  auto count = [&](int bn, int bm) { return ((a.n + bn - 1) / bn) * ((a.m + bm - 1) / bm); };
+  if (a.m <= 16) return launch_rows<FMT, 1, false>(a, s);
   // the tile kernel's row offsets have 32 bits
-  const int64_t span = (a.offsets ? a.n_rows : 256) * (a.ldq > a.lds ? a.ldq : a.lds);
-  const bool wide = span >= ((int64_t)1 << 32);
-  if (a.offsets ? a.m <= 4 * a.n_expert : a.m <= 16) return launch_rows<FMT, 1>(a, s);
-  if (wide) return launch_rows<FMT, 2>(a, s);
-  if (!a.offsets && a.m <= 32) return launch_rows<FMT, 2>(a, s);
-  if (tiles >= 256) return launch_tiles<FMT, 4, 2, 2, 2, FMT == kRowsMxfp4 ? 3 : 2>(a, s);
-  return launch_tiles<FMT, 1, 1, 2, 2, 4>(a, s);
+  if (256 * (a.ldq > a.lds ? a.ldq : a.lds) >= ((int64_t)1 << 32)) return launch_rows<FMT, 2, false>(a, s);
+  if (a.m <= 32 && count(64, 64) < 160) return launch_rows<FMT, 2, false>(a, s);
+  if (count(256, 128) >= 224) return launch_tiles<FMT, 4, 2, 2, 2, k4 ? 3 : 2, false>(a, s);
+  if constexpr (k4)
+    if (count(128, 128) >= 160) return launch_tiles<FMT, 2, 2, 2, 2, 4, false>(a, s);
+  if (count(128, 64) >= 160) return launch_tiles<FMT, 2, 1, 2, 2, 4, false>(a, s);
+  return launch_tiles<FMT, 1, 1, 2, 2, 4, false>(a, s);
+}
+
+// By expert: how the rows fall is not known here, only their average r.  Straight from memory
+// up to r = 2 (128 experts of 1536 x 2048: r = 1 17.7 us, 128 x 64 tiles 19.6; r = 4 42.8 for
+// 37.4), 256 x 128 tiles from r = 32 (MXFP8 64) if there are enough of them (r = 64: 60.7, 128 x 64
+// 65.4; r = 16: 52.3 for 49.8; 16 experts, r = 128, some 144 tiles: 13.7 for 13.3).
+template <int FMT>
+static int launch_grouped(const MxArgs& a, hipStream_t s) {
+  constexpr bool k4 = FMT == kRowsMxfp4;
+  const int64_t experts = a.m < a.n_expert ? a.m : a.n_expert;
+  const bool wide = a.n_rows * (a.ldq > a.lds ? a.ldq : a.lds) >= ((int64_t)1 << 32);  // 32-bit row offsets
+  if (wide || a.m <= 2 * a.n_expert) return launch_rows<FMT, 1, true>(a, s);
+  if (a.m >= (k4 ? 32 : 64) * (int64_t)a.n_expert && ((a.n + 255) / 256) * (a.m / 128 + experts / 2) >= 192)
+    return launch_tiles<FMT, 4, 2, 2, 2, k4 ? 3 : 2, true>(a, s);
+  return launch_tiles<FMT, 2, 1, 2, 2, 4, true>(a, s);
 }
 
 int launch_mx_gemm(MxArgs a, int fmt, hipStream_t s) {
   a.inv_top = a.pairs ? 1.0f / (float)a.top_k : 0.0f;
   a.vec_y = a.ldy % (a.y_type == kF32 ? 4 : 8) == 0 && aligned(a.y, 16);
-  return fmt == kRowsMxfp4 ? launch_fmt<kRowsMxfp4>(a, s) : launch_fmt<kRowsMxfp8>(a, s);
+  if (a.offsets) return fmt == kRowsMxfp4 ? launch_grouped<kRowsMxfp4>(a, s) : launch_grouped<kRowsMxfp8>(a, s);
+  return fmt == kRowsMxfp4 ? launch_dense<kRowsMxfp4>(a, s) : launch_dense<kRowsMxfp8>(a, s);
 }
 
 }  // namespace iq4

@@ -86,6 +86,61 @@ def test_exact_sums(fmt, m, n, k):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("k", [32, 160, 416, 512])
+@pytest.mark.parametrize("m,n", [(325, 4099), (641, 4100), (1003, 7201), (40, 10300)])
+def test_exact_sums_of_larger_tiles(fmt, m, n, k):
+    """Sizes that fill the device with 128 x 64, 128 x 128, 256 x 128 and 64 x 64 tiles, one to four
+    128-element steps, the last row and column tiles partial."""
+    note(f"mx gemm exact, large: {m} x {n} x {k} {fmt}")
+    cw, sw = exact_weights(m + n, n, k)
+    x = exact_rows(m + k, fmt, m, k)
+    r = oracle.mx_product(value("mxfp4", cw, sw), value(fmt, *x))
+    w = packed(cw, sw, n, k)
+    assert np.array_equal(product(w, x, fmt, n, k, m, "f32"), r)
+    assert np.array_equal(product(w, x, fmt, n, k, m, "bf16", ldy=n + 5), rounder("bf16")(r))
+    if n % 4 == 0:
+        assert np.array_equal(product(w, x, fmt, n, k, m, "f16", ldy=n + 4), rounder("f16")(r))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_large_tiles_over_many_steps(fmt):
+    note(f"mx gemm: 900 x 6144 x 2336 {fmt} (19 steps)")
+    m, n, k = 900, 6144, 2336
+    cw, sw = real_weights(n, n, k)
+    x = real_rows(m, fmt, m, k)
+    dw, dx = value("mxfp4", cw, sw), value(fmt, *x)
+    r, tol = bound(dw, dx, k, "f32")
+    y = product(packed(cw, sw, n, k), x, fmt, n, k, m, "f32")
+    assert np.all(np.abs(y - r) <= tol), float(np.max(np.abs(y - r) / tol))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_rows_more_than_32_bits_apart(fmt):
+    note(f"mx gemm: rows of X some 17 and 67 MB apart, {fmt}")
+    n, k = 96, 160
+    cw, sw = exact_weights(1, n, k)
+    w = packed(cw, sw, n, k)
+    for m, ldq in ((40, (1 << 24) + 64), (70, 1 << 26)):
+        x = exact_rows(3, fmt, m, k)
+        r = oracle.mx_product(value("mxfp4", cw, sw), value(fmt, *x))
+        c, s = iq4.iq4_rows_bytes(FMT[fmt], k)
+        q = torch.empty(m * ldq, dtype=torch.uint8, device="cuda")
+        rows = q.view(m, ldq)
+        rows[:, :c] = 0
+        rows[:, : x[0].shape[1]] = dev(x[0])
+        d = torch.zeros(m, s, dtype=torch.uint8, device="cuda")
+        d[:, : k // 32] = dev(x[1])
+        y = torch.full((m, n), -7.0, device="cuda")
+        iq4.iq4_mx_gemm(w, n, k, FMT[fmt], q, ldq, d, s, m, y, iq4.IQ4_F32, n)
+        assert np.array_equal(host(y), r)
+        y.fill_(-7.0)
+        off = dev(np.array([0, m], np.int32))
+        iq4.iq4_mx_grouped_gemm(w, 1, n, k, FMT[fmt], q, ldq, d, s, m, off, None, 0, m, y, iq4.IQ4_F32, n)
+        assert np.array_equal(host(y), r)
+        del q, rows
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (4, 2560, 6144), (16, 1024, 14336), (20, 1000, 2592), (200, 333, 2048), (700, 1300, 2592)])
 def test_real_values(fmt, m, n, k):
     note(f"mx gemm: {m} x {n} x {k} {fmt}")
@@ -237,6 +292,8 @@ COUNTS = {
     "single": [41],
     "many": [i % 3 for i in range(150)],
     "long": [260, 0, 515, 31],
+    "crowd": [i % 5 for i in range(300)],
+    "crowded": [i % 8 for i in range(301)],
 }
 
 
@@ -269,6 +326,40 @@ def test_grouped(fmt, name, n, k):
     r = np.stack([dense[expert[i]] @ dx[pairs[i] // top] for i in range(total)])
     y = grouped(w, e, n, k, fmt, x, off, pairs, top, total, ldy=n + 3)
     assert np.array_equal(y, r)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("k", [160, 512])
+def test_grouped_large_tiles(fmt, k):
+    note(f"mx grouped: 256 x 128 tiles, k = {k} {fmt}")
+    counts, n = [130, 0, 1, 300, 64, 65, 128, 33], 7201
+    e, total = len(counts), sum(counts)
+    w, dense = bank(300, e, n, k)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    expert = np.repeat(np.arange(e), counts)
+    top = 2
+    tokens = (total + 1) // 2 + 2
+    pairs = np.concatenate([np.random.default_rng(8).permutation(total), [0, 0, 0]])  # three pairs more than rows
+    x = exact_rows(9, fmt, tokens, k)
+    dx = value(fmt, *x)
+    r = np.concatenate([dx[pairs[off[i]:off[i + 1]] // top] @ dense[i].T for i in range(e)])
+    assert np.array_equal(expert, np.sort(expert)) and r.shape == (total, n)
+    for out, ldy in (("f32", n), ("f16", n + 7)):
+        y = grouped(w, e, n, k, fmt, x, off, pairs, top, total + 3, out, ldy)
+        assert np.array_equal(y[:total], rounder(out)(r)) and np.all(y[total:] == -7.0)
+
+
+def test_grouped_offsets_and_pairs_out_of_range():
+    """Device values that break the rules are clamped: the result means nothing, and no byte
+    outside it is written."""
+    note("mx grouped: offsets and pairs out of range")
+    e, n, k, cap = 5, 40, 160, 60
+    w, _ = bank(100, e, n, k)
+    x = exact_rows(5, "mxfp4", 30, k)
+    for off in ([-5, 10, 7, 90, 20, 1 << 30], [0, 60, 60, 60, 60, 60], [1 << 30] * 6, [60, 50, 40, 30, 20, 10]):
+        for pairs in (None, [-(1 << 31), (1 << 31) - 1, 59, -1] * 15):
+            rows = exact_rows(5, "mxfp4", 60, k) if pairs is None else x
+            grouped(w, e, n, k, "mxfp4", rows, off, pairs, 2, cap)  # checks the sentinels around y
 
 
 def test_grouped_no_rows_at_all():
