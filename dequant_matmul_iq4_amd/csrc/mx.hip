@@ -90,9 +90,11 @@ __device__ __forceinline__ Frag<FMT> split(const u32x4 (&x)[Act<FMT>::kWords / 4
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t t = (x[h][i] >> 6) & 0x01010101u, mask = (t << 8) - t;  // 255 in every byte of the high part
+        // bit 6 of every byte spread over the byte: the permute's selectors 8 .. 11 give the signs
+        // of the second operand's and the first operand's 16-bit halves
+        const uint32_t mask = __builtin_amdgcn_perm(x[h][i] << 9, x[h][i] << 1, 0x090B080Au);
         f.hi[h][i] = x[h][i] & mask;
-        f.lo[h][i] = x[h][i] & ~mask;
+        f.lo[h][i] = x[h][i] ^ f.hi[h][i];
       }
   }
   return f;
@@ -807,10 +809,10 @@ mx_tile_kernel(MxArgs a) {
   asm volatile("" ::: "memory");
   copy_part(T::kD, 0, T::kC);
   Ops o0, o1;
-  // MXFP8: a half is read right before it is multiplied.  Its products take four times as long
-  // as its reads, the CU's other workgroup fills the gap, and the registers for a half ahead
-  // are not there.
-  constexpr bool kAhead = FMT == kRowsMxfp4;
+  // Large MXFP8 pieces: a half is read right before it is multiplied.  Their products take four
+  // times as long as their reads, the CU's other workgroup fills the gap, and the registers
+  // for a half ahead are not there.
+  constexpr bool kAhead = FMT == kRowsMxfp4 || FN * FM <= 2;
   Scales sc;
   read_scales(sc);
   if constexpr (kAhead) read_half(0, 0, o0);
