@@ -7,21 +7,30 @@
 
 namespace iq4 {
 
+// Float rows larger than this are read and written past the L2: they would only push each other
+// out of it and of the memory-side cache behind it (norm of 13056 x 4096 bf16 with its decode
+// 125 -> 118 us reading so, 112 -> 109 writing so; 3256 x 14336 f16 rows 72 -> 66 and 65 -> 63).
+// Smaller ones were often just written, or are read next, and are still there (norm of 3256 x 2048:
+// 22.4 us, 24.9 reading past it).
+constexpr int64_t kStreamBytes = 64 << 20;
+static inline bool streams(int type, int64_t m, int64_t k) { return m * k * (type == kF32 ? 4 : 2) > kStreamBytes; }
+
 // ---- quantise -------------------------------------------------------------------------
-// Lanes walk the rows' groups of eight, the zero padding of MX rows included; the scale
-// bytes past the padded codes belong to no group and are zeroed by the row's last lane.
-template <int TYPE>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const void* __restrict__ x, int64_t m, int k,
-                                                            int64_t ldx, int fmt, int octs, int scale_bytes,
+// Lanes walk the rows' groups of eight, the zero padding of MX rows included (fewer than 2^32
+// groups); the scale bytes past the padded codes belong to no group and are zeroed by the
+// row's last lane.
+template <int TYPE, bool STREAM>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const void* __restrict__ x, uint32_t m, int k,
+                                                            int64_t ldx, int fmt, uint32_t octs, int scale_bytes,
                                                             RowsOut o) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t r = i / octs;
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  const uint32_t r = i / octs;
   const int oct = (int)(i - r * octs);
   const bool live = r < m;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (live && 8 * oct < k) load8<TYPE>(x, r * ldx + 8 * oct, v);
+  if (live && 8 * oct < k) load8<TYPE, STREAM>(x, r * ldx + 8 * oct, v);
   store_rows8(o, fmt, r, oct, v, live);
-  if (live && fmt != kRowsQ8_1 && oct == octs - 1)
+  if (live && fmt != kRowsQ8_1 && oct == (int)octs - 1)
     for (int b = octs / 4; b < scale_bytes; ++b) o.scales[r * o.lds + b] = 0;
 }
 
@@ -30,11 +39,13 @@ int launch_quantize_rows(const void* x, int x_type, int64_t m, int64_t k, int64_
   const int octs = (int)((fmt == kRowsQ8_1 ? k : (k + 127) / 128 * 128) / 8);
   const int64_t grid = (m * octs + 255) / 256;
   const int sb = (int)rows_scale_bytes(fmt, k);
-#define IQ4_QUANT(T) \
-  hipLaunchKernelGGL(quantize_rows_kernel<T>, dim3((unsigned)grid), dim3(256), 0, s, x, m, (int)k, ldx, fmt, octs, sb, o)
-  if (x_type == kF32) IQ4_QUANT(kF32);
-  else if (x_type == kF16) IQ4_QUANT(kF16);
-  else IQ4_QUANT(kBF16);
+  const bool st = streams(x_type, m, k);
+#define IQ4_QUANT(T, S)                                                                                             \
+  hipLaunchKernelGGL((quantize_rows_kernel<T, S>), dim3((unsigned)grid), dim3(256), 0, s, x, (uint32_t)m, (int)k, ldx, \
+                     fmt, (uint32_t)octs, sb, o)
+  if (x_type == kF32) { if (st) IQ4_QUANT(kF32, true); else IQ4_QUANT(kF32, false); }
+  else if (x_type == kF16) { if (st) IQ4_QUANT(kF16, true); else IQ4_QUANT(kF16, false); }
+  else { if (st) IQ4_QUANT(kBF16, true); else IQ4_QUANT(kBF16, false); }
 #undef IQ4_QUANT
   return check_launch("quantize_rows_kernel");
 }
@@ -42,41 +53,37 @@ int launch_quantize_rows(const void* x, int x_type, int64_t m, int64_t k, int64_
 // ---- decode ---------------------------------------------------------------------------
 // The value code * scale is exact in binary32 (at most four significant bits, or the
 // eight of a Q8_1 code times the eleven of its scale), then rounded once to the output's
-// type.
-template <int FMT>
-__global__ void __launch_bounds__(256) dequant_rows_kernel(RowsIn in, int64_t m, int octs, int out_type,
-                                                           void* __restrict__ out, int64_t ldo) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t r = i / octs;
-  const int oct = (int)(i - r * octs);
-  if (r >= m) return;
-  const uint8_t* codes = in.codes + r * in.ldq;
-  const uint8_t* scales = in.scales + r * in.lds;
-  float v[8];
+// type.  A lane stores 16 bytes (four binary32 values, eight of 16 bits), so that a wave
+// writes a kilobyte in one piece.
+template <int FMT, int PER>
+__device__ __forceinline__ void decode(const uint8_t* codes, const uint8_t* scales, int at, float (&v)[PER]) {
   if constexpr (FMT == kRowsQ8_1) {
-    const u32x2 w = *reinterpret_cast<const u32x2*>(codes + 8 * oct);
-    const float d = h2f(*reinterpret_cast<const uint16_t*>(scales + 2 * (oct >> 2)));
+    const float d = h2f(*reinterpret_cast<const uint16_t*>(scales + 2 * (at >> 5)));
+    uint32_t w[PER / 4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)((w[j >> 2] >> (8 * (j & 3))) & 0xFFu) * d;
+    for (int j = 0; j < PER / 4; ++j) w[j] = *reinterpret_cast<const uint32_t*>(codes + at + 4 * j);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) v[j] = (float)(int8_t)((w[j >> 2] >> (8 * (j & 3))) & 0xFFu) * d;
   } else {
-    const uint32_t s = scales[oct >> 2];
+    const uint32_t s = scales[at >> 5];
     const float d = (s == 255u) ? __uint_as_float(0x7FC00000u) : pow2_biased(s);
     if constexpr (FMT == kRowsMxfp4) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + 4 * oct);
-#define IQ4_TWO(B)                                                                  \
-  {                                                                                 \
-    const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, B);            \
-    v[2 * B] = p[0] * d;                                                            \
-    v[2 * B + 1] = p[1] * d;                                                        \
+      uint32_t w;
+      if constexpr (PER == 8) w = *reinterpret_cast<const uint32_t*>(codes + at / 2);
+      else w = *reinterpret_cast<const uint16_t*>(codes + at / 2);
+#define IQ4_TWO(B)                                                       \
+  if constexpr (2 * B < PER) {                                           \
+    const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, B); \
+    v[2 * B] = p[0] * d;                                                 \
+    v[2 * B + 1] = p[1] * d;                                             \
   }
       IQ4_TWO(0) IQ4_TWO(1) IQ4_TWO(2) IQ4_TWO(3)
 #undef IQ4_TWO
     } else {
-      const u32x2 w = *reinterpret_cast<const u32x2*>(codes + 8 * oct);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const auto p = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], false);
-        const auto q = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], true);
+      for (int j = 0; j < PER / 4; ++j) {
+        const int w = *reinterpret_cast<const int*>(codes + at + 4 * j);
+        const auto p = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), q = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
         v[4 * j] = p[0] * d;
         v[4 * j + 1] = p[1] * d;
         v[4 * j + 2] = q[0] * d;
@@ -84,19 +91,53 @@ __global__ void __launch_bounds__(256) dequant_rows_kernel(RowsIn in, int64_t m,
       }
     }
   }
-  store8(out_type, out, r * ldo + 8 * oct, v);
+}
+
+template <int FMT, int TYPE, bool STREAM>
+__global__ void __launch_bounds__(256) dequant_rows_kernel(RowsIn in, uint32_t m, uint32_t pieces,
+                                                           void* __restrict__ out, int64_t ldo) {
+  constexpr int kPer = TYPE == kF32 ? 4 : 8;
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  const uint32_t r = i / pieces;
+  const int at = kPer * (int)(i - r * pieces);
+  if (r >= m) return;
+  float v[kPer];
+  decode<FMT, kPer>(in.codes + r * in.ldq, in.scales + r * in.lds, at, v);
+  if constexpr (TYPE == kF32) {
+    f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(out) + r * ldo + at);
+    const f32x4 w = {v[0], v[1], v[2], v[3]};
+    if constexpr (STREAM) __builtin_nontemporal_store(w, o);
+    else *o = w;
+  } else {
+    u32x4* o = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + r * ldo + at);
+    const u32x4 w = {pack2<TYPE>(v[0], v[1]), pack2<TYPE>(v[2], v[3]), pack2<TYPE>(v[4], v[5]), pack2<TYPE>(v[6], v[7])};
+    if constexpr (STREAM) __builtin_nontemporal_store(w, o);
+    else *o = w;
+  }
+}
+
+template <int FMT>
+static int launch_dequant_fmt(RowsIn in, int64_t m, int64_t k, int out_type, void* out, int64_t ldo, hipStream_t s) {
+  const uint32_t pieces = (uint32_t)(k / (out_type == kF32 ? 4 : 8));
+  const dim3 grid((unsigned)((m * pieces + 255) / 256));
+  const bool st = streams(out_type, m, k);
+#define IQ4_DEQ(T)                                                                                                       \
+  {                                                                                                                      \
+    if (st) hipLaunchKernelGGL((dequant_rows_kernel<FMT, T, true>), grid, dim3(256), 0, s, in, (uint32_t)m, pieces, out, ldo); \
+    else hipLaunchKernelGGL((dequant_rows_kernel<FMT, T, false>), grid, dim3(256), 0, s, in, (uint32_t)m, pieces, out, ldo);   \
+  }
+  if (out_type == kF32) IQ4_DEQ(kF32)
+  else if (out_type == kF16) IQ4_DEQ(kF16)
+  else IQ4_DEQ(kBF16)
+#undef IQ4_DEQ
+  return check_launch("dequant_rows_kernel");
 }
 
 int launch_dequant_rows(RowsIn in, int fmt, int64_t m, int64_t k, int out_type, void* out, int64_t ldo,
                         hipStream_t s) {
-  const int octs = (int)(k / 8);
-  const dim3 grid((unsigned)((m * octs + 255) / 256));
-#define IQ4_DEQ(F) hipLaunchKernelGGL(dequant_rows_kernel<F>, grid, dim3(256), 0, s, in, m, octs, out_type, out, ldo)
-  if (fmt == kRowsMxfp4) IQ4_DEQ(kRowsMxfp4);
-  else if (fmt == kRowsMxfp8) IQ4_DEQ(kRowsMxfp8);
-  else IQ4_DEQ(kRowsQ8_1);
-#undef IQ4_DEQ
-  return check_launch("dequant_rows_kernel");
+  if (fmt == kRowsMxfp4) return launch_dequant_fmt<kRowsMxfp4>(in, m, k, out_type, out, ldo, s);
+  if (fmt == kRowsMxfp8) return launch_dequant_fmt<kRowsMxfp8>(in, m, k, out_type, out, ldo, s);
+  return launch_dequant_fmt<kRowsQ8_1>(in, m, k, out_type, out, ldo, s);
 }
 
 // ---- RMS norm ---------------------------------------------------------------------------
@@ -108,12 +149,12 @@ int launch_dequant_rows(RowsIn in, int fmt, int64_t m, int64_t k, int out_type, 
 // fused multiply-add per element) hides under the row's loads.
 // One workgroup per row; a lane keeps its groups of eight in registers (V of them) between
 // the sum and the second use.
-template <int TYPE>
+template <int TYPE, bool STREAM>
 __device__ __forceinline__ void norm_load(const NormArgs& a, int64_t r, int oct, float (&v)[8]) {
-  load8<TYPE>(a.x, r * a.ldx + 8 * oct, v);
+  load8<TYPE, STREAM>(a.x, r * a.ldx + 8 * oct, v);
   if (a.res) {
     float t[8];
-    load8<TYPE>(a.res, r * a.ldr + 8 * oct, t);
+    load8<TYPE, STREAM>(a.res, r * a.ldr + 8 * oct, t);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // the binary32 sum of two 16-bit floats rounds to them as the exact sum does
@@ -135,7 +176,7 @@ __device__ __forceinline__ void norm_store(const NormArgs& a, int64_t r, int oct
   }
 }
 
-template <int TYPE, int NT, int V>
+template <int TYPE, int NT, int V, bool STREAM>
 __global__ void __launch_bounds__(NT) rmsnorm_kernel(NormArgs a, int octs_k, int octs, int scale_bytes) {
   __shared__ double part[NT / 64];
   const int64_t r = blockIdx.x;
@@ -148,7 +189,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_kernel(NormArgs a, int octs_k, int
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
     if (oct < octs_k) {
-      norm_load<TYPE>(a, r, oct, v[j]);
+      norm_load<TYPE, STREAM>(a, r, oct, v[j]);
       if (a.h) store8<TYPE>(a.h, r * a.ldh + 8 * oct, v[j]);
     }
 #pragma unroll
@@ -185,7 +226,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a, int octs
   double sum = 0.0;
   for (int oct = tid; oct < octs_k; oct += 1024) {
     float v[8];
-    norm_load<TYPE>(a, r, oct, v);
+    norm_load<TYPE, false>(a, r, oct, v);
     if (a.h) store8<TYPE>(a.h, r * a.ldh + 8 * oct, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum = fma((double)v[i], (double)v[i], sum);
@@ -202,7 +243,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a, int octs
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (oct < octs_k) {
       if (a.h) load8<TYPE>(a.h, r * a.ldh + 8 * oct, v);
-      else norm_load<TYPE>(a, r, oct, v);
+      else norm_load<TYPE, false>(a, r, oct, v);
     }
     norm_store<TYPE>(a, r, oct, u, v, oct < octs_k);
     if (a.fmt >= 0) store_rows8(a.o, a.fmt, r, oct, v, oct < octs);
@@ -218,12 +259,19 @@ static int launch_norm_t(const NormArgs& a, hipStream_t s) {
   const int octs = mx ? (int)((a.k + 127) / 128 * 16) : octs_k;
   const int sb = mx ? (int)rows_scale_bytes(a.fmt, a.k) : 0;
   const dim3 grid((unsigned)a.m);
-#define IQ4_NORM(NT, V) hipLaunchKernelGGL((rmsnorm_kernel<TYPE, NT, V>), grid, dim3(NT), 0, s, a, octs_k, octs, sb)
-  if (octs <= 64) IQ4_NORM(64, 1);
-  else if (octs <= 256) IQ4_NORM(256, 1);
-  else if (octs <= 512) IQ4_NORM(256, 2);
-  else if (octs <= 1024) IQ4_NORM(256, 4);
-  else if (octs <= 2048) IQ4_NORM(1024, 2);
+  const bool st = streams(TYPE, a.m, a.k);
+#define IQ4_NORM(NT, V)                                                                                              \
+  {                                                                                                                  \
+    if (st) hipLaunchKernelGGL((rmsnorm_kernel<TYPE, NT, V, true>), grid, dim3(NT), 0, s, a, octs_k, octs, sb);       \
+    else hipLaunchKernelGGL((rmsnorm_kernel<TYPE, NT, V, false>), grid, dim3(NT), 0, s, a, octs_k, octs, sb);         \
+  }
+  // a lane per group of eight as far as a workgroup goes (one row of 4096: 5.4 us with its decode
+  // for 6.1 with two groups a lane)
+  if (octs <= 64) IQ4_NORM(64, 1)
+  else if (octs <= 256) IQ4_NORM(256, 1)
+  else if (octs <= 512) IQ4_NORM(512, 1)
+  else if (octs <= 1024) IQ4_NORM(1024, 1)
+  else if (octs <= 2048) IQ4_NORM(1024, 2)
   else hipLaunchKernelGGL(rmsnorm_long_kernel<TYPE>, grid, dim3(1024), 0, s, a, octs_k, octs, sb);
 #undef IQ4_NORM
   return check_launch("rmsnorm_kernel");

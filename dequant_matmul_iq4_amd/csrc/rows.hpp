@@ -63,15 +63,22 @@ int launch_rmsnorm(const NormArgs& a, int type, hipStream_t s);
 #ifdef __HIPCC__
 // ---- eight consecutive elements -------------------------------------------------------
 
-template <int TYPE>
+// STREAM: past the L2 (a non-temporal load).
+template <bool STREAM, typename V>
+__device__ __forceinline__ V load_vec(const void* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(static_cast<const V*>(p));
+  return *static_cast<const V*>(p);
+}
+
+template <int TYPE, bool STREAM = false>
 __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
   if constexpr (TYPE == kF32) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at);
-    const f32x4 b = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at + 4);
+    const f32x4 a = load_vec<STREAM, f32x4>(static_cast<const float*>(p) + at);
+    const f32x4 b = load_vec<STREAM, f32x4>(static_cast<const float*>(p) + at + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
   } else {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at);
+    const u32x4 w = load_vec<STREAM, u32x4>(static_cast<const uint16_t*>(p) + at);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (TYPE == kF16) {
