@@ -545,9 +545,6 @@ static int check_mx_product(const char* fn, const void* packed, int64_t n, int64
   if (int e = check_rows(fn, fmt, k, codes, ldq, scales, lds)) return e;
   if (!aligned(packed, 256) || !aligned(y, y_dtype == IQ4_F32 ? 4 : 2))
     return set_error(IQ4_E_ALIGN, "%s: packed must be 256-byte and y element aligned", fn);
-  // the grid: a workgroup at least for each 16 weight rows and 16 output rows
-  if (mx_row_tiles(n) * ((m + 15) / 16 + 1024) >= (int64_t)1 << 22)
-    return set_error(IQ4_E_UNSUPPORTED, "%s: n * m too large (n=%lld m=%lld)", fn, (long long)n, (long long)m);
   return IQ4_OK;
 }
 
@@ -590,10 +587,12 @@ int iq4_mx_grouped_gemm(const void* packed, int32_t n_expert, int64_t n, int64_t
   if (int e = check_mx_args(fn, n, k, fmt, n_pairs, y_dtype)) return e;
   if (n_expert < 1 || n_expert > 1024) return set_error(IQ4_E_ARG, "%s: need 1 <= n_expert <= 1024", fn);
   if (pairs && top_k < 1) return set_error(IQ4_E_ARG, "%s: top_k must be >= 1", fn);
-  if (n_rows < 0) return set_error(IQ4_E_ARG, "%s: n_rows must be >= 0", fn);
+  if (n_rows < 0 || n_rows > (int64_t)1 << 30) return set_error(IQ4_E_ARG, "%s: n_rows must be 0 .. 2^30", fn);
   if (n_pairs == 0) return IQ4_OK;
   if (pairs ? n_rows * (int64_t)top_k < n_pairs : n_rows < n_pairs)
     return set_error(IQ4_E_ARG, "%s: n_rows (times top_k, with pairs) must be >= n_pairs", fn);
+  if (pairs && n_rows * (int64_t)top_k > (int64_t)1 << 22)
+    return set_error(IQ4_E_UNSUPPORTED, "%s: n_rows * top_k must be at most 2^22 with pairs", fn);
   if (!offsets) return set_error(IQ4_E_ARG, "%s: null pointer", fn);
   if (!aligned(offsets, 4) || !aligned(pairs, 4))
     return set_error(IQ4_E_ALIGN, "%s: offsets and pairs must be 4-byte aligned", fn);

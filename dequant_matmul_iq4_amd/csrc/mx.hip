@@ -64,6 +64,12 @@ int launch_mx_pack(const uint8_t* codes, int64_t ldq, const uint8_t* scales, int
 
 // ---- shared pieces ------------------------------------------------------------------------
 
+// A launch has fewer than 2^32 threads.
+static int check_grid(int64_t groups, int threads) {
+  if (groups * threads >= (int64_t)1 << 32) return set_error(-3, "iq4_mx product: too many workgroups (n * m too large)");
+  return 0;
+}
+
 template <int FMT>
 struct Act {  // one 16-row x 128-element operand of activations
   static constexpr int kWords = FMT == kRowsMxfp4 ? 4 : 8;
@@ -234,7 +240,7 @@ __device__ __forceinline__ bool group_find(ExpertTiles g, int e0, int t, int bm,
 // Activation row of a pair (or of output row p, without pairs), inside the buffer whatever
 // `pairs` holds.
 __device__ __forceinline__ int act_row(const MxArgs& a, int p) {
-  // p / top_k: p is below 2^21, so (p + 1/2) / top_k is further from a whole number (1 / (2 top_k))
+  // p / top_k: p is below 2^22, so (p + 1/2) / top_k is further from a whole number (1 / (2 top_k))
   // than the product's error (2^-23 of it)
   const int r = a.pairs ? (int)(((float)p + 0.5f) * a.inv_top) : p;
   return min(max(r, 0), (int)a.n_rows - 1);
@@ -392,8 +398,9 @@ __global__ void __launch_bounds__(64 * NW) mx_rows_kernel(MxArgs a) {
 template <int FMT, int MT, int KS, int NW, bool GROUPED>
 static int launch_rows_ks(const MxArgs& a, hipStream_t s) {
   const int64_t cols = (mx_row_tiles(a.n) + NW / KS - 1) / (NW / KS);
-  const dim3 grid((unsigned)(cols * (GROUPED ? a.m : (a.m + 16 * MT - 1) / (16 * MT))));
-  hipLaunchKernelGGL((mx_rows_kernel<FMT, MT, KS, NW, GROUPED>), grid, dim3(64 * NW), 0, s, a);
+  const int64_t groups = cols * (GROUPED ? a.m : (a.m + 16 * MT - 1) / (16 * MT));
+  if (int e = check_grid(groups, 64 * NW)) return e;
+  hipLaunchKernelGGL((mx_rows_kernel<FMT, MT, KS, NW, GROUPED>), dim3((unsigned)groups), dim3(64 * NW), 0, s, a);
   return check_launch("mx_rows_kernel");
 }
 
@@ -504,12 +511,12 @@ __device__ __forceinline__ bool place_tile(const MxArgs& a, int bn, int bm, int&
   return true;
 }
 
-static unsigned tile_grid(const MxArgs& a, int bn, int bm) {
+static int64_t tile_grid(const MxArgs& a, int bn, int bm) {
   const int64_t nt = (a.n + bn - 1) / bn;
   int64_t tiles = (a.m + bm - 1) / bm;
   // by expert: each expert's last tile may be partial
   if (a.offsets) tiles = a.m / bm + a.n_expert < a.m ? a.m / bm + a.n_expert : a.m;
-  return (unsigned)((nt * tiles + 7) / 8 * 8);
+  return (nt * tiles + 7) / 8 * 8;
 }
 
 template <int FMT, int FN, int FM, int WN, int WM, int S>
@@ -866,7 +873,9 @@ mx_tile_kernel(MxArgs a) {
 template <int FMT, int FN, int FM, int WN, int WM, int S, bool GROUPED>
 static int launch_tiles(const MxArgs& a, hipStream_t s) {
   using T = Tile<FMT, FN, FM, WN, WM, S>;
-  hipLaunchKernelGGL((mx_tile_kernel<FMT, FN, FM, WN, WM, S, GROUPED>), dim3(tile_grid(a, T::kBN, T::kBM)), dim3(64 * T::kWaves), 0, s, a);
+  const int64_t groups = tile_grid(a, T::kBN, T::kBM);
+  if (int e = check_grid(groups, 64 * T::kWaves)) return e;
+  hipLaunchKernelGGL((mx_tile_kernel<FMT, FN, FM, WN, WM, S, GROUPED>), dim3((unsigned)groups), dim3(64 * T::kWaves), 0, s, a);
   return check_launch("mx_tile_kernel");
 }
 

@@ -459,8 +459,9 @@ int iq4_dequant_rows(const void* codes, int64_t ldq, const void* scales, int64_t
  *   y       [m][ldy] of y_dtype, or NULL.
  *   codes, scales  y (the float32 values) quantised as by iq4_quantize_rows, or codes NULL
  *           (fmt, ldq, scales, lds are then ignored).  y or codes must be given.
- * A row that holds an infinity or a NaN gets all NaN.  A row does not depend on the others,
- * and every output is a function of the inputs alone, bit for bit.
+ * A row that holds an infinity or a NaN gets all NaN (h keeps its values), and so does a zero
+ * row with eps = 0.  A row does not depend on the others, and every output is a function of
+ * the inputs alone, bit for bit.
  * Errors: as iq4_quantize_rows.
  */
 int iq4_rmsnorm(const void* x, int64_t ldx, const void* res, int64_t ldr, int32_t dtype, int64_t m, int64_t k,
@@ -494,8 +495,9 @@ int iq4_mx_pack_weights(const void* codes, int64_t ldq, const void* scales, int6
  *   y       [m][ldy] of y_dtype (IQ4_F32, IQ4_F16, IQ4_BF16), ldy >= n, element aligned;
  *           columns n .. ldy - 1 are left alone.
  *   m >= 0 (0: no-op), any n >= 1, k % 32 == 0.  No workspace.
- * Deterministic; for m <= 16 each row is bitwise the m = 1 call's.
- * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED (k % 32, sizes).
+ * Deterministic; for m <= 16 each row is bitwise the m = 1 call's.  Every product is exact,
+ * MXFP8 ones too (the instruction alone loses some: the kernels multiply in two parts).
+ * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED (k % 32, sizes; a grid of 2^32 threads).
  */
 int iq4_mx_gemm(const void* packed, int64_t n, int64_t k, int32_t fmt, const void* codes, int64_t ldq,
                 const void* scales, int64_t lds, int64_t m, void* y, int32_t y_dtype, int64_t ldy, void* stream);
@@ -507,7 +509,7 @@ int iq4_mx_gemm(const void* packed, int64_t n, int64_t k, int32_t fmt, const voi
  * offsets and pairs are iq4_moe_gather's: with pairs, X has a row per token (gate and up
  * products); without, a row per pair in the experts' order (down products).
  *   packed  n_expert packed n x k matrices, expert e at e * iq4_mx_packed_bytes(n, k).
- *   codes, scales  n_rows rows of X.
+ *   codes, scales  n_rows rows of X (n_rows <= 2^30; with pairs n_rows * top_k <= 2^22).
  *   offsets [n_expert + 1] int32, ascending from 0, offsets[n_expert] <= n_pairs.
  *   pairs   [n_pairs] int32 or NULL.   n_pairs >= 0 (0: no-op).   1 <= n_expert <= 1024.
  *   y       [n_pairs][ldy]; rows from offsets[n_expert] on are left as they were.

@@ -106,10 +106,11 @@ def test_mx_gemm_refusals():
         assert f(yt=1, y=FAKE + 1) == AL and f(ldq=72) == AL and f(lds=20) == AL and f(ldq=48) == A
         assert f(fmt=MX8) == A  # ldq of MXFP4 rows
     assert gemm(m=0, q=None, y=None) == iq4.IQ4_OK
-    assert gemm(n=1 << 24, m=1 << 10, ldy=1 << 24) == U
+    assert gemm(n=1 << 24, m=1 << 21, ldy=1 << 24) == U and "workgroups" in iq4.iq4_last_error()
     assert grouped(m=0, off=None, y=None) == iq4.IQ4_OK
     assert grouped(e=0) == A and grouped(e=1025) == A and grouped(top=0) == A and grouped(off=None) == A
     assert grouped(off=FAKE + 2) == AL and grouped(pairs=FAKE + 1) == AL
+    assert grouped(rows=(1 << 21) + 1) == U and grouped(rows=(1 << 30) + 1, pairs=None) == A
     assert grouped(rows=7) == A and grouped(rows=8, pairs=None, m=9) == A and grouped(rows=-1) == A
 
 

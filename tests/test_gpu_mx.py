@@ -102,6 +102,16 @@ def test_exact_sums_of_larger_tiles(fmt, m, n, k):
         assert np.array_equal(product(w, x, fmt, n, k, m, "f16", ldy=n + 4), rounder("f16")(r))
 
 
+@pytest.mark.parametrize("m", [1, 20, 70])
+def test_very_wide_matrix(m):
+    note(f"mx gemm: 200003 weight rows, {m} rows")
+    n, k = 200003, 96
+    cw, sw = exact_weights(4, n, k)
+    x = exact_rows(5, "mxfp4", m, k)
+    y = product(packed(cw, sw, n, k), x, "mxfp4", n, k, m, "f32", extra=1)
+    assert np.array_equal(y, oracle.mx_product(value("mxfp4", cw, sw), value("mxfp4", *x)))
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 def test_large_tiles_over_many_steps(fmt):
     note(f"mx gemm: 900 x 6144 x 2336 {fmt} (19 steps)")
