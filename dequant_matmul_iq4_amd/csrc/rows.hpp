@@ -126,6 +126,12 @@ __device__ __forceinline__ float pow2_biased(uint32_t e) {
   return __uint_as_float(e ? e << 23 : 0x00400000u);
 }
 
+// Another lane's value inside a row of 16 lanes, by a DPP control (without LDS).
+template <int CTRL>
+__device__ __forceinline__ int lane_move(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+}
+
 // ---- one block of 32 by four neighbouring lanes, eight elements each ---------------------
 // All four lanes of a block call this together (the maxima cross lanes); `live` lanes
 // write.  `oct` is the index of the eight elements in the row, `r` the row.
@@ -134,8 +140,8 @@ __device__ __forceinline__ void store_rows8(const RowsOut& o, int fmt, int64_t r
   uint32_t top = 0;  // the largest magnitude by its bits: a NaN is above infinity, and that above all else
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-  top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+  top = max(top, (uint32_t)lane_move<0xB1>((int)top));  // lane ^ 1
+  top = max(top, (uint32_t)lane_move<0x4E>((int)top));  // lane ^ 2
   const bool bad = top >= 0x7F800000u;
   uint8_t* codes = o.codes + r * o.ldq;
   uint8_t* scales = o.scales + r * o.lds;
