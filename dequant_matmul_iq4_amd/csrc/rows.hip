@@ -18,9 +18,9 @@ static inline bool streams(int type, int64_t m, int64_t k) { return m * k * (typ
 // ---- quantise -------------------------------------------------------------------------
 // Lanes walk the rows' groups of eight, the zero padding of MX rows included (fewer than 2^32
 // groups); the scale bytes past the padded codes belong to no group and are zeroed by the
-// row's last lane.  Four lanes agree on a block's scale by two lane exchanges, so nothing goes
-// through LDS and every wave reads and writes one run of memory.  Bound by memory: 3256 x 14336
-// f16 to MXFP8 27.6 us, 5.1 TB/s; 4 x 4096 2.6 us, of which an empty launch is 1.7.
+// row's last lane.  Four lanes agree on a block's scale inside the wave, and every wave reads and
+// writes one run of memory.  Bound by memory: 3256 x 14336 f16 to MXFP8 27.1 us, 5.2 TB/s;
+// 4 x 4096 2.5 us, of which an empty launch is 1.7.
 template <int TYPE, bool STREAM>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const void* __restrict__ x, uint32_t m, int k,
                                                             int64_t ldx, int fmt, uint32_t octs, int scale_bytes,
@@ -56,7 +56,7 @@ int launch_quantize_rows(const void* x, int x_type, int64_t m, int64_t k, int64_
 // The value code * scale is exact in binary32 (at most four significant bits, or the
 // eight of a Q8_1 code times the eleven of its scale), then rounded once to the output's
 // type.  A lane stores 16 bytes (four binary32 values, eight of 16 bits), so that a wave
-// writes a kilobyte in one piece.  Bound by the writes: 3256 x 14336 MXFP8 to f32 33.4 us, 7.0 TB/s
+// writes a kilobyte in one piece.  Bound by the writes: 3256 x 14336 MXFP8 to f32 33.5 us, 7.0 TB/s
 // (the last of them still on their way through the memory-side cache); 13056 x 4096 MXFP4 34.7.
 template <int FMT, int PER>
 __device__ __forceinline__ void decode(const uint8_t* codes, const uint8_t* scales, int at, float (&v)[PER]) {
@@ -150,8 +150,8 @@ int launch_dequant_rows(RowsIn in, int fmt, int64_t m, int64_t k, int out_type, 
 // step, so u, y and with them every rounding decision of the quantised row are a function
 // of the row alone, whatever the order of the sum.  The extra cost (one conversion and one
 // fused multiply-add per element) hides under the row's loads.
-// Bound by memory: 13056 x 4096 bf16 with a residual to MXFP4 63 us, 349 MB, 5.5 TB/s; for one
-// row of 4096 by latency: 3.3 us, of which an empty launch is 1.7.
+// Bound by memory: 13056 x 4096 bf16 with a residual to MXFP4 60 us, 349 MB, 5.8 TB/s; for one
+// row of 4096 by latency: 3.0 us, of which an empty launch is 1.7.
 // One workgroup per row; a lane keeps its groups of eight in registers (V of them) between
 // the sum and the second use.
 template <int TYPE, bool STREAM>
