@@ -304,6 +304,7 @@ COUNTS = {
     "long": [260, 0, 515, 31],
     "crowd": [i % 5 for i in range(300)],
     "crowded": [i % 8 for i in range(301)],
+    "most": [(i * 7) % 4 for i in range(1024)],
 }
 
 

@@ -266,3 +266,61 @@ def test_rows_do_not_depend_on_each_other():
         h1, y1, q1, d1 = norm(x[r:r + 1], res[r:r + 1], "bf16", gain, 1e-6, y_t="bf16", fmt="mxfp4")
         assert bits_equal(h1, h[r:r + 1]) and bits_equal(y1, y[r:r + 1])
         assert bits_equal(host(q1), host(q[r:r + 1])) and bits_equal(host(d1), host(d[r:r + 1]))
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_large_calls_equal_small_ones(t, fmt):
+    """Rows of more than 64 MB are read and written past the L2; their values are those of small calls."""
+    m, k = (4100, 4128) if t == "f32" else (8200, 4128)
+    note(f"rows: {m} x {k} {t} {fmt} at once and in parts")
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = (torch.randn(m, k, device="cuda", generator=g) * 3).to(TYPES[t][1])
+    res = torch.randn(m, k, device="cuda", generator=g).to(TYPES[t][1])
+    gain = torch.rand(k, device="cuda", generator=g) + 0.5
+
+    def run(a, b):
+        """h, y, codes, scales of the norm; codes, scales of x; x decoded, twice; of rows a .. b - 1."""
+        xs, rs, n = x[a:b], res[a:b].clone(), b - a
+        y = torch.empty(n, k, dtype=TYPES[t][1], device="cuda")
+        q, d, ldq, lds = row_buffers(fmt, n, k)
+        iq4.iq4_rmsnorm(xs, k, rs, k, TYPES[t][0], n, k, gain, 1e-6, rs, k, y, TYPES[t][0], k, FMT[fmt], q, ldq, d, lds)
+        q2, d2, _, _ = row_buffers(fmt, n, k)
+        iq4.iq4_quantize_rows(xs, TYPES[t][0], n, k, k, FMT[fmt], q2, ldq, d2, lds)
+        back = torch.empty(n, k, dtype=TYPES[t][1], device="cuda")
+        iq4.iq4_dequant_rows(q2, ldq, d2, lds, FMT[fmt], n, k, TYPES[t][0], back, k)
+        return rs, y, q, d, q2, d2, back
+
+    whole = run(0, m)
+    for a, b in ((0, 700), (m // 2, m // 2 + 333), (m - 512, m)):
+        for w, p in zip(whole, run(a, b)):
+            assert torch.equal(w[a:b].contiguous().view(torch.uint8), p.contiguous().view(torch.uint8))
+
+
+def test_rows_more_than_32_bits_apart():
+    note("rows and norm: two rows 4.3 GB apart")
+    k, far = 512, (1 << 30) + 64
+    x, res, gain = inputs(51, 2, k, "f32")
+    b = torch.zeros(far + k, device="cuda")
+    b[:k], b[far:] = torch.from_numpy(x[0]).cuda(), torch.from_numpy(x[1]).cuda()
+    q, d, ldq, lds = row_buffers("mxfp8", 2, k)
+    iq4.iq4_quantize_rows(b, iq4.IQ4_F32, 2, k, far, FMT["mxfp8"], q, ldq, d, lds)
+    want = oracle.quantize_rows(x, "mxfp8")
+    same_rows("mxfp8", k, q, d, want)
+    o = torch.full((far + k,), -7.0, device="cuda")
+    iq4.iq4_dequant_rows(q, ldq, d, lds, FMT["mxfp8"], 2, k, iq4.IQ4_F32, o, far)
+    got = np.stack([host(o[:k]), host(o[far:])])
+    assert np.array_equal(got.astype(np.float64), value("mxfp8", *want)) and bool((o[k:far] == -7.0).all())
+    # the norm with x and its sum there, and codes as far apart
+    fq = (1 << 32) + 128
+    q = torch.full((fq + 512,), 0xEE, dtype=torch.uint8, device="cuda")
+    d = torch.full((2, lds), 0xEE, dtype=torch.uint8, device="cuda")
+    rd = torch.from_numpy(res).cuda()
+    iq4.iq4_rmsnorm(b, far, rd, k, iq4.IQ4_F32, 2, k, torch.from_numpy(gain).cuda(), 1e-6, b, far, o, iq4.IQ4_F32, far,
+                    FMT["mxfp8"], q, fq, d, lds)
+    hr, yr = norm_oracle(x, res, "f32", gain, 1e-6)
+    assert np.array_equal(np.stack([host(b[:k]), host(b[far:])]).astype(np.float64), hr)
+    assert np.array_equal(np.stack([host(o[:k]), host(o[far:])]).astype(np.float64), yr.astype(np.float64))
+    two = torch.stack([q[:512], q[fq:]])
+    same_rows("mxfp8", k, two, d, oracle.quantize_rows(yr, "mxfp8"))
+    assert bool((q[512:fq] == 0xEE).all())
