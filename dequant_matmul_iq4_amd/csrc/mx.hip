@@ -593,58 +593,45 @@ struct Tile {
   }
 };
 
-// Eight values past the L2 (nothing here reads Y again): the long prompt's 374 MB of results
-// took 428 us with ordinary stores and 412 with these.
-template <int TYPE>
-__device__ __forceinline__ void stream8(void* p, int64_t at, const float (&v)[8]) {
-  if constexpr (TYPE == kF32) {
-    f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(p) + at);
-    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, o);
-    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, o + 1);
-  } else {
-    __builtin_nontemporal_store(u32x4{pack2<TYPE>(v[0], v[1]), pack2<TYPE>(v[2], v[3]), pack2<TYPE>(v[4], v[5]), pack2<TYPE>(v[6], v[7])},
-                                reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + at));
-  }
-}
-
-// `rows` x `cols` values in LDS (rows of PITCH, at most 32 x COLS) to Y from (row0, col0) on,
-// by one wave: eight columns a lane.
-template <int TYPE, int COLS, int PITCH>
-__device__ __forceinline__ void store_rows_piece(const MxArgs& a, const float* part, int64_t row0, int rows, int64_t col0,
+// `rows` x `cols` values of Y's type in LDS (rows of PITCH, at most 32 x COLS) to Y from (row0,
+// col0) on, by one wave: eight columns a lane, past the L2 (nothing here reads Y again: the long
+// prompt's 374 MB of results took 428 us with ordinary stores and 412 with these).
+template <typename E, int COLS, int PITCH>
+__device__ __forceinline__ void store_rows_piece(const MxArgs& a, const E* part, int64_t row0, int rows, int64_t col0,
                                                  int cols) {
   constexpr int kLanes = COLS / 8, kStep = 64 / kLanes;  // lanes a row, rows a step
   const int lane = threadIdx.x & 63, c = 8 * (lane % kLanes), r0 = lane / kLanes;
-  const float* from = part + r0 * PITCH + c;
-  const int64_t at = (row0 + r0) * a.ldy + col0 + c;
+  const E* from = part + r0 * PITCH + c;
+  E* to = static_cast<E*>(a.y) + (row0 + r0) * a.ldy + col0 + c;
   if (a.vec_y && cols == COLS) {
 #pragma unroll
     for (int r = 0; r < 32; r += kStep) {
-      float v[8];
-      const f32x4 p = *reinterpret_cast<const f32x4*>(from + r * PITCH), q = *reinterpret_cast<const f32x4*>(from + r * PITCH + 4);
+      u32x4 v[sizeof(E) / 2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = p[i], v[4 + i] = q[i];
-      if (r0 + r < rows) stream8<TYPE>(a.y, at + r * a.ldy, v);
+      for (int i = 0; i < (int)sizeof(E) / 2; ++i) v[i] = reinterpret_cast<const u32x4*>(from + r * PITCH)[i];
+      if (r0 + r < rows) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(E) / 2; ++i) __builtin_nontemporal_store(v[i], reinterpret_cast<u32x4*>(to + r * a.ldy) + i);
+      }
     }
     return;
   }
 #pragma unroll 1
   for (int r = 0; r0 + r < rows; r += kStep)
 #pragma unroll 1
-    for (int i = 0; i < 8 && c + i < cols; ++i) {
-      const float v = from[r * PITCH + i];
-      if constexpr (TYPE == kF32) static_cast<float*>(a.y)[at + r * a.ldy + i] = v;
-      else static_cast<uint16_t*>(a.y)[at + r * a.ldy + i] = (uint16_t)pack2<TYPE>(v, v);
-    }
+    for (int i = 0; i < 8 && c + i < cols; ++i) to[r * a.ldy + i] = from[r * PITCH + i];
 }
 
-// A wave's pieces to Y through LDS (`part`, its own), 32 rows at a time, so that the rows are
-// written in runs of 64 FN or 128 FN bytes (a lane holds four columns of 32 different rows;
-// stored from the registers, 32 bytes a row and store, the long prompt took 450 us for 432).
+// A wave's pieces to Y through LDS (`part`, its own, in Y's type), 32 rows at a time, so that the
+// rows are written in runs of 64 FN or 128 FN bytes (a lane holds four columns of 32 different
+// rows; stored from the registers, 32 bytes a row and store, the long prompt took 450 us for 432).
 // `first`: the wave's first row in the tile, `col0` its first column.
-template <int FN, int FM>
-__device__ __forceinline__ void store_tile(const MxArgs& a, float* part, const f32x16 (&acc)[FN][FM], int64_t row0, int first,
+template <int TYPE, int FN, int FM>
+__device__ __forceinline__ void store_tile(const MxArgs& a, uint8_t* lds, const f32x16 (&acc)[FN][FM], int64_t row0, int first,
                                            int rows, int64_t col0) {
-  constexpr int kCols = 32 * FN, kPitch = kCols + 4;
+  using E = std::conditional_t<TYPE == kF32, float, uint16_t>;
+  constexpr int kCols = 32 * FN, kPitch = kCols + 16 / (int)sizeof(E);
+  E* part = reinterpret_cast<E*>(lds);
   const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
   const int cols = (int)min((int64_t)kCols, a.n - col0);
 #pragma unroll
@@ -653,14 +640,13 @@ __device__ __forceinline__ void store_tile(const MxArgs& a, float* part, const f
 #pragma unroll
     for (int n = 0; n < FN; ++n)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4*>(part + r * kPitch + 32 * n + 8 * q + 4 * h) =
-            f32x4{acc[n][m][4 * q], acc[n][m][4 * q + 1], acc[n][m][4 * q + 2], acc[n][m][4 * q + 3]};
-    const int64_t to = row0 + first + 32 * m;
-    const int left = min(32, rows - first - 32 * m);
-    if (a.y_type == kF32) store_rows_piece<kF32, kCols, kPitch>(a, part, to, left, col0, cols);
-    else if (a.y_type == kF16) store_rows_piece<kF16, kCols, kPitch>(a, part, to, left, col0, cols);
-    else store_rows_piece<kBF16, kCols, kPitch>(a, part, to, left, col0, cols);
+      for (int q = 0; q < 4; ++q) {
+        const float v[4] = {acc[n][m][4 * q], acc[n][m][4 * q + 1], acc[n][m][4 * q + 2], acc[n][m][4 * q + 3]};
+        E* to = part + r * kPitch + 32 * n + 8 * q + 4 * h;
+        if constexpr (TYPE == kF32) *reinterpret_cast<f32x4*>(to) = f32x4{v[0], v[1], v[2], v[3]};
+        else *reinterpret_cast<u32x2*>(to) = u32x2{pack2<TYPE>(v[0], v[1]), pack2<TYPE>(v[2], v[3])};
+      }
+    store_rows_piece<E, kCols, kPitch>(a, part, row0 + first + 32 * m, min(32, rows - first - 32 * m), col0, cols);
   }
 }
 
@@ -883,7 +869,12 @@ mx_tile_kernel(MxArgs a) {
   asm volatile("" ::: "memory");
   constexpr int kPart = 32 * (32 * FN + 4);
   static_assert(T::kWaves * kPart * 4 <= T::kLds, "the parts fit");
-  store_tile<FN, FM>(a, reinterpret_cast<float*>(lds) + wave * kPart, acc, row0, 32 * FM * wm, rows, (int64_t)nt * T::kBN + 32 * FN * wn);
+  uint8_t* part = lds + wave * kPart * 4;
+  const int first = 32 * FM * wm;
+  const int64_t col0 = (int64_t)nt * T::kBN + 32 * FN * wn;
+  if (a.y_type == kF32) store_tile<kF32, FN, FM>(a, part, acc, row0, first, rows, col0);
+  else if (a.y_type == kF16) store_tile<kF16, FN, FM>(a, part, acc, row0, first, rows, col0);
+  else store_tile<kBF16, FN, FM>(a, part, acc, row0, first, rows, col0);
 }
 
 template <int FMT, int FN, int FM, int WN, int WM, int S, bool GROUPED>
