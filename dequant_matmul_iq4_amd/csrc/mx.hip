@@ -180,13 +180,28 @@ __device__ __forceinline__ void store_y4(const MxArgs& a, int64_t row, int64_t c
 }
 
 // ---- rows by expert -------------------------------------------------------------------------
-// Expert e's rows [o0, o1), clamped to [0, m]: whatever the offsets hold, no row outside is
-// touched.
-__device__ __forceinline__ void expert_rows(const MxArgs& a, int e, int& o0, int& o1) {
-  const int m = (int)a.m, el = min(e, a.n_expert - 1);
-  o0 = min(max(a.offsets[el], 0), m);
-  o1 = min(max(a.offsets[el + 1], o0), m);
-  if (e >= a.n_expert) o1 = o0;
+// The rows [o0[c], o1[c]) of experts e0 + 64 c + lane, clamped to [0, m]: whatever the offsets
+// hold, no row outside is touched.  All loads at once; the upper two sets only if they hold an expert
+// (nothing is to be done for them if this says false).
+constexpr int kGroupExperts = 256;
+__device__ __forceinline__ bool expert_rows(const MxArgs& a, int e0, int (&o0)[4], int (&o1)[4]) {
+  const int m = (int)a.m, lane = threadIdx.x & 63;
+  const bool upper = e0 + 128 < a.n_expert;
+  auto load = [&](int c) {
+    const int el = min(e0 + 64 * c + lane, a.n_expert - 1);
+    o0[c] = a.offsets[el];
+    o1[c] = a.offsets[el + 1];
+  };
+  auto clamp = [&](int c) {
+    o0[c] = min(max(o0[c], 0), m);
+    o1[c] = e0 + 64 * c + lane < a.n_expert ? min(max(o1[c], o0[c]), m) : o0[c];
+  };
+  load(0), load(1);
+  if (upper) load(2), load(3);
+  else o0[2] = o1[2] = o0[3] = o1[3] = 0;
+  clamp(0), clamp(1);
+  if (upper) clamp(2), clamp(3);
+  return upper;
 }
 
 // Sums of a value over lanes 0 .. own (one wave, without LDS: row shifts and broadcasts).
@@ -201,43 +216,43 @@ __device__ __forceinline__ int scan64(int v) {
 }
 
 // The tiles of `bm` rows that the experts' rows make, found by every wave on its own from the
-// offsets: lanes hold the experts 64 c + lane, four c at a time (all loads at once).
-constexpr int kGroupExperts = 256;
+// offsets: lanes hold the experts 64 c + lane, four c at a time.
 struct ExpertTiles {
   int row[4], rows[4], upto[4];  // first row, rows, tiles of the group's experts up to this one
   int total;                     // tiles of the group
 };
 __device__ __forceinline__ ExpertTiles group_tiles(const MxArgs& a, int e0, int bm) {
   ExpertTiles g;
-  int o0[4], o1[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) expert_rows(a, e0 + 64 * c + (threadIdx.x & 63), o0[c], o1[c]);
+  int o1[4];
+  const bool upper = expert_rows(a, e0, g.row, o1);
   g.total = 0;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    g.row[c] = o0[c];
-    g.rows[c] = o1[c] - o0[c];
+  auto add = [&](int c) {
+    g.rows[c] = o1[c] - g.row[c];
     g.upto[c] = g.total + scan64((g.rows[c] + bm - 1) / bm);
     g.total = __builtin_amdgcn_readlane(g.upto[c], 63);
-  }
+  };
+  add(0), add(1);
+  if (upper) add(2), add(3);
+  else g.rows[2] = g.rows[3] = 0, g.upto[2] = g.upto[3] = g.total;
   return g;
 }
-// Tile `t` of the group: its expert, first row and rows.  False: t >= g.total.
-__device__ __forceinline__ bool group_find(ExpertTiles g, int e0, int t, int bm, int& e, int64_t& row0, int& rows) {
+// Tile t < g.total of the group: its expert, first row and rows.
+__device__ __forceinline__ void group_find(const ExpertTiles& g, int e0, int t, int bm, int& e, int64_t& row0, int& rows) {
+  int c = 0, row = g.row[0], count = g.rows[0], upto = g.upto[0];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint64_t past = __ballot(g.upto[c] > t);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      const int mine = __builtin_amdgcn_readlane(g.rows[c], l);
-      const int at = (t - (__builtin_amdgcn_readlane(g.upto[c], l) - (mine + bm - 1) / bm)) * bm;  // rows before it
-      e = e0 + 64 * c + l;
-      row0 = __builtin_amdgcn_readlane(g.row[c], l) + at;
-      rows = min(bm, mine - at);
-      return true;
-    }
+  for (int q = 1; q < 4; ++q) {  // (selects: an index would put the sets into memory)
+    const bool past = __builtin_amdgcn_readlane(g.upto[q - 1], 63) <= t;
+    c = past ? q : c;
+    row = past ? g.row[q] : row;
+    count = past ? g.rows[q] : count;
+    upto = past ? g.upto[q] : upto;
   }
-  return false;
+  const int l = __builtin_ctzll(__ballot(upto > t) | 1ull << 63);
+  const int mine = __builtin_amdgcn_readlane(count, l);
+  const int at = (t - (__builtin_amdgcn_readlane(upto, l) - (mine + bm - 1) / bm)) * bm;  // rows before it
+  e = e0 + 64 * c + l;
+  row0 = __builtin_amdgcn_readlane(row, l) + at;
+  rows = min(bm, mine - at);
 }
 
 // Activation row of a pair (or of output row p, without pairs), inside the buffer whatever
@@ -282,8 +297,7 @@ __global__ void __launch_bounds__(64 * NW) mx_rows_kernel(MxArgs a) {
     int o0 = 0, o1 = 0, e = -1;
     for (int e0 = 0; e0 < a.n_expert; e0 += kGroupExperts) {
       int b0[4], b1[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) expert_rows(a, e0 + 64 * q + lane, b0[q], b1[q]);
+      expert_rows(a, e0, b0, b1);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint64_t in = __ballot(b0[q] <= i && i < b1[q]);
@@ -509,7 +523,7 @@ __device__ __forceinline__ bool place_tile(const MxArgs& a, int bn, int bm, int&
       if (e0 >= a.n_expert) return false;
       g = group_tiles(a, e0, bm);
     }
-    if (!group_find(g, e0, t, bm, e, row0, rows)) return false;
+    group_find(g, e0, t, bm, e, row0, rows);
     W += e * a.w_stride;
   } else {
     const uint32_t mt_n = ((uint32_t)a.m + bm - 1) / bm;
