@@ -265,30 +265,28 @@ __device__ __forceinline__ int act_row(const MxArgs& a, int p) {
 }
 
 // ---- few rows -----------------------------------------------------------------------------
-// A workgroup of NW waves: NW / KS neighbouring row tiles of W against MT x 16 rows of Y, each
-// tile's k split over KS waves (wave s takes the quads s, s + KS, ...), whose sums are added
-// through LDS in the waves' order.  Every operand goes from memory straight into registers, the
+// A workgroup of KS waves: a row tile of W against MT x 16 rows of Y, its k split over the waves
+// (wave s takes the quads s, s + KS, ...), whose sums are added through LDS in the waves'
+// order.  (One tile a workgroup: a wave's place is free as soon as it ends.  Four waves of one
+// tile each: 128 experts of 2048 x 768, 128 pairs 16.1 us, one wave 15.1; 32 pairs of 1536 x 2048,
+// MXFP8 12.8 for 12.0; 50000 x 2048, m = 4 13.9 for 12.6.)  Every operand goes from memory straight into registers, the
 // rows one quad (four tiles along k) ahead of their products, the weights kAhead quads.
 //
 // Bound by the weights' way from memory: a row tile's quad is 4.3 KB for 4 (MXFP8 8)
 // instructions of 16 clocks.  The waves over k are there to have enough of it under way.  In
 // graphs of launches: 4096 x 4096, m = 1 3.3 us (2.7 TB/s; an empty launch takes 1.7); 2560 x 6144,
-// m = 4, MXFP8 4.9; 128 experts of 1536 x 2048, 32 pairs, MXFP8 12.5 (2.5 TB/s).
+// m = 4, MXFP8 4.9; 128 experts of 1536 x 2048, 32 pairs, MXFP8 12.1 (2.6 TB/s).
 //
 // Rows by expert: workgroup column i stands for output row i; it works if row i begins a tile
 // of its expert (MT x 16 rows from the expert's first on), so a wave finds its expert with one
 // comparison per expert and no sum over them.
-template <int FMT, int MT, int KS, int NW, bool GROUPED>
-__global__ void __launch_bounds__(64 * NW) mx_rows_kernel(MxArgs a) {
-  __shared__ f32x4 part[KS > 1 ? NW * MT * 64 : 1];
-  constexpr int kTiles = NW / KS, kWords = Act<FMT>::kWords / 4, kAhead = 2;
+template <int FMT, int MT, int KS, bool GROUPED>
+__global__ void __launch_bounds__(64 * KS) mx_rows_kernel(MxArgs a) {
+  __shared__ f32x4 part[KS > 1 ? KS * MT * 64 : 1];
+  constexpr int kWords = Act<FMT>::kWords / 4, kAhead = 2;
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int slice = wave % KS;
-  const int64_t rt_n = mx_row_tiles(a.n), cols = (rt_n + kTiles - 1) / kTiles;
-  const int64_t col = blockIdx.x % cols, at = blockIdx.x / cols;
-  const int64_t rt_raw = col * kTiles + wave / KS;
-  const int64_t rt = min(rt_raw, rt_n - 1);  // past the last tile: the last again, not stored
+  const int slice = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t rt_n = mx_row_tiles(a.n), rt = blockIdx.x % rt_n, at = blockIdx.x / rt_n;
   const uint8_t* W = a.W;
   int64_t row0 = at * (16 * MT);
   int rows = 16 * MT;
@@ -393,36 +391,33 @@ __global__ void __launch_bounds__(64 * NW) mx_rows_kernel(MxArgs a) {
       load_w(u + kAhead, w[v]);
     }
   }
-  const bool mine = rt_raw < rt_n;
   if constexpr (KS > 1) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) part[(wave * MT + i) * 64 + lane] = acc[i];
+    for (int i = 0; i < MT; ++i) part[(slice * MT + i) * 64 + lane] = acc[i];
     __syncthreads();
-    // wave s of a tile adds up and stores the pieces s, s + KS, ...
-    const int w0 = wave - slice;
+    // wave s adds up and stores the pieces s, s + KS, ...
     for (int i = slice; i < MT; i += KS) {
-      f32x4 s = part[(w0 * MT + i) * 64 + lane];
+      f32x4 s = part[i * 64 + lane];
 #pragma unroll
       for (int w = 1; w < KS; ++w) {
-        const f32x4 v = part[((w0 + w) * MT + i) * 64 + lane];
+        const f32x4 v = part[(w * MT + i) * 64 + lane];
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[k] = s[k] + v[k];
       }
-      if (mine && 16 * i + c < rows) store_y4(a, row0 + 16 * i + c, rt * 16 + 4 * g, s);
+      if (16 * i + c < rows) store_y4(a, row0 + 16 * i + c, rt * 16 + 4 * g, s);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      if (mine && 16 * i + c < rows) store_y4(a, row0 + 16 * i + c, rt * 16 + 4 * g, acc[i]);
+      if (16 * i + c < rows) store_y4(a, row0 + 16 * i + c, rt * 16 + 4 * g, acc[i]);
   }
 }
 
-template <int FMT, int MT, int KS, int NW, bool GROUPED>
+template <int FMT, int MT, int KS, bool GROUPED>
 static int launch_rows_ks(const MxArgs& a, hipStream_t s) {
-  const int64_t cols = (mx_row_tiles(a.n) + NW / KS - 1) / (NW / KS);
-  const int64_t groups = cols * (GROUPED ? a.m : (a.m + 16 * MT - 1) / (16 * MT));
-  if (int e = check_grid(groups, 64 * NW)) return e;
-  hipLaunchKernelGGL((mx_rows_kernel<FMT, MT, KS, NW, GROUPED>), dim3((unsigned)groups), dim3(64 * NW), 0, s, a);
+  const int64_t groups = mx_row_tiles(a.n) * (GROUPED ? a.m : (a.m + 16 * MT - 1) / (16 * MT));
+  if (int e = check_grid(groups, 64 * KS)) return e;
+  hipLaunchKernelGGL((mx_rows_kernel<FMT, MT, KS, GROUPED>), dim3((unsigned)groups), dim3(64 * KS), 0, s, a);
   return check_launch("mx_rows_kernel");
 }
 
@@ -436,10 +431,10 @@ static int launch_rows(const MxArgs& a, hipStream_t s) {
   int ks = 1;
   while (ks < 8 && ks < kq_n && waves * ks < 2048) ks *= 2;
   switch (ks) {
-    case 1: return launch_rows_ks<FMT, MT, 1, 4, GROUPED>(a, s);
-    case 2: return launch_rows_ks<FMT, MT, 2, 4, GROUPED>(a, s);
-    case 4: return launch_rows_ks<FMT, MT, 4, 4, GROUPED>(a, s);
-    default: return launch_rows_ks<FMT, MT, 8, 8, GROUPED>(a, s);
+    case 1: return launch_rows_ks<FMT, MT, 1, GROUPED>(a, s);
+    case 2: return launch_rows_ks<FMT, MT, 2, GROUPED>(a, s);
+    case 4: return launch_rows_ks<FMT, MT, 4, GROUPED>(a, s);
+    default: return launch_rows_ks<FMT, MT, 8, GROUPED>(a, s);
   }
 }
 
