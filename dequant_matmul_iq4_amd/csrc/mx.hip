@@ -453,7 +453,7 @@ static int launch_rows(const MxArgs& a, hipStream_t s) {
 // LDS read; the counts of copies in flight are worked out below.
 //
 // What bounds it: the matrix pipe and what interrupts it.  13056 x 14336 x 4096 in MXFP4
-// takes 403-434 us by the card (3.8 PFLOP/s; the same instructions alone reach 7.7): 60 % of the
+// takes 399-434 us by the card (3.8 PFLOP/s; the same instructions alone reach 7.7): 60 % of the
 // clocks have a matrix instruction running.  A workgroup of 256 x 128 spends 1.9 us before its
 // first copies are issued, 27 in the loop and 3 storing, and the CU's other workgroup fills only a
 // part of that.  Without the copies the loop takes 20 us, without the matrix instructions 17.
