@@ -255,8 +255,7 @@ __device__ __forceinline__ void group_find(const ExpertTiles& g, int e0, int t, 
   rows = min(bm, mine - at);
 }
 
-// Activation row of a pair (or of output row p, without pairs), inside the buffer whatever
-// `pairs` holds.
+// Activation row of a pair (or p itself, without pairs), inside the buffer whatever `pairs` holds.
 __device__ __forceinline__ int act_row(const MxArgs& a, int p) {
   // p / top_k: p is below 2^22, so (p + 1/2) / top_k is further from a whole number (1 / (2 top_k))
   // than the product's error (2^-23 of it)
@@ -480,6 +479,10 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 __device__ __forceinline__ void copy16(const void* base, uint32_t voff, uint32_t lds) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(base), "{m0}"(lds) : "memory");
 }
+// The same from an address of the lane's own.
+__device__ __forceinline__ void copy16(const uint8_t* at, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(at), "{m0}"(lds) : "memory");
+}
 
 // A pointer that is the same in all lanes, in scalar registers.
 __device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
@@ -659,8 +662,10 @@ __device__ __forceinline__ void store_tile(const MxArgs& a, uint8_t* lds, const 
   }
 }
 
+// FAR: the rows a tile reads may lie 4 GiB apart or more; each lane then holds their addresses, and not
+// 32-bit offsets from one base.
 // waves a SIMD: registers are given out so that as many workgroups share a CU as LDS allows (two at most)
-template <int FMT, int FN, int FM, int WN, int WM, int S, bool GROUPED>
+template <int FMT, int FN, int FM, int WN, int WM, int S, bool GROUPED, bool FAR>
 __global__ void __launch_bounds__(64 * WN * WM)
 __attribute__((amdgpu_waves_per_eu(Tile<FMT, FN, FM, WN, WM, S>::kWaves / 4 * (Tile<FMT, FN, FM, WN, WM, S>::kLds <= 80 * 1024 ? 2 : 1))))
 mx_tile_kernel(MxArgs a) {
@@ -684,21 +689,23 @@ mx_tile_kernel(MxArgs a) {
 #pragma unroll
   for (int i = 0; i < T::kCW; ++i) wt[i] = scalar(W + (int64_t)min(rt0 + wave * T::kCW + i, rt_n - 1) * (kt_n * (int64_t)kMxTileBytes));
   // X: kilobytes wave * kCX ..; rows past the last repeat it.  (By expert: the pair ids are
-  // loaded here, and used after W's first copies have been issued.)
-  uint32_t xo[T::kCX], xso[T::kCXS];
+  // loaded here, and used after W's first copies have been issued.)  Without pair ids a tile's
+  // rows lie one after another and are counted from its first.
+  std::conditional_t<FAR, const uint8_t*, uint32_t> xo[T::kCX], xso[T::kCXS];
+  uint32_t xr[T::kCX], xsr[T::kCXS];
   int xsl[T::kCXS];
   auto row_of = [&](int row) -> uint32_t {
     const uint32_t src = min(row, rows - 1);
-    if constexpr (GROUPED) return a.pairs ? (uint32_t)a.pairs[row0 + src] : (uint32_t)row0 + src;
+    if constexpr (GROUPED) return a.pairs ? (uint32_t)a.pairs[row0 + src] : src;
     return src;
   };
 #pragma unroll
-  for (int i = 0; i < T::kCX; ++i) xo[i] = row_of(((wave * T::kCX + i) * 64 + lane) / T::kChunks);
+  for (int i = 0; i < T::kCX; ++i) xr[i] = row_of(((wave * T::kCX + i) * 64 + lane) / T::kChunks);
 #pragma unroll
   for (int i = 0; i < T::kCXS; ++i) {
     const int kb = (wave * T::kCXS + i) % (T::kXS / 1024);
     xsl[i] = T::kWS + kb * 1024;
-    xso[i] = row_of(kb * 64 + lane);
+    xsr[i] = row_of(kb * 64 + lane);
   }
   __builtin_amdgcn_sched_barrier(0);
   // scales: every wave issues the same number of copies, some of them twice (the same bytes
@@ -713,10 +720,16 @@ mx_tile_kernel(MxArgs a) {
     const int rt = min(rt0 + 4 * kb + (lane >> 4), rt_n - 1) - rt0;
     wso[i] = (uint32_t)(rt * kq_n) * kMxScaleBytes + 16 * (lane & 15);
   }
-  const uint8_t* xbase = scalar(a.codes + (GROUPED ? 0 : row0 * a.ldq));
-  const uint8_t* xsbase = scalar(a.scales + (GROUPED ? 0 : row0 * a.lds));
+  const int64_t xfirst = GROUPED && a.pairs ? 0 : row0;
+  const uint8_t* xbase = scalar(a.codes + xfirst * a.ldq);
+  const uint8_t* xsbase = scalar(a.scales + xfirst * a.lds);
   const uint8_t* wsbase = scalar(W + mx_code_plane(a.n, a.k) + (int64_t)rt0 * (kq_n * kMxScaleBytes));
 
+  // from where `at` says, `ahead` bytes along the row
+  auto copy_x = [&](const uint8_t* base, int64_t ahead, auto at, uint32_t to) {
+    if constexpr (FAR) copy16(at + ahead, to);
+    else copy16(base + ahead, at, to);
+  };
   // (steps and quads past the last copy it again: the counts hold to the end)
   auto copy_part = [&](int t, int i0, int i1) {  // copies i0 .. i1 - 1 of this wave's kC
     const uint32_t st = lds0 + (uint32_t)(t % S) * T::kStage;
@@ -725,7 +738,7 @@ mx_tile_kernel(MxArgs a) {
     for (int i = 0; i < T::kC; ++i) {
       if (i < i0 || i >= i1) continue;
       if (i < T::kCW) copy16(wt[i] + (int64_t)k * kMxTileBytes, 16 * lane, st + (wave * T::kCW + i) * 1024);
-      else copy16(xbase + (int64_t)k * T::kRowB, xo[i - T::kCW], st + T::kWBytes + (wave * T::kCX + i - T::kCW) * 1024);
+      else copy_x(xbase, (int64_t)k * T::kRowB, xo[i - T::kCW], st + T::kWBytes + (wave * T::kCX + i - T::kCW) * 1024);
     }
   };
   auto copy_wscales = [&](int q) {
@@ -734,7 +747,7 @@ mx_tile_kernel(MxArgs a) {
   };
   auto copy_xscales = [&](int q) {
 #pragma unroll
-    for (int i = 0; i < T::kCXS; ++i) copy16(xsbase + (int64_t)min(q, kq_n - 1) * 16, xso[i], lds0 + S * T::kStage + xsl[i]);
+    for (int i = 0; i < T::kCXS; ++i) copy_x(xsbase, (int64_t)min(q, kq_n - 1) * 16, xso[i], lds0 + S * T::kStage + xsl[i]);
   };
 
   // ---- operands from LDS --------------------------------------------------------------------
@@ -810,13 +823,15 @@ mx_tile_kernel(MxArgs a) {
   for (int i = 0; i < T::kCX; ++i) {
     const int at = (wave * T::kCX + i) * 64 + lane, row = at / T::kChunks, place = at % T::kChunks;
     const int chunk = place ^ (FMT == kRowsMxfp4 ? (row >> 2) & 3 : (row >> 1) & 7);
-    if constexpr (GROUPED) xo[i] = act_row(a, (int)xo[i]);
-    xo[i] = xo[i] * (uint32_t)a.ldq + 16 * chunk;
+    if constexpr (GROUPED) xr[i] = act_row(a, (int)xr[i]);
+    if constexpr (FAR) xo[i] = xbase + (int64_t)xr[i] * a.ldq + 16 * chunk;
+    else xo[i] = xr[i] * (uint32_t)a.ldq + 16 * chunk;
   }
 #pragma unroll
   for (int i = 0; i < T::kCXS; ++i) {
-    if constexpr (GROUPED) xso[i] = act_row(a, (int)xso[i]);
-    xso[i] *= (uint32_t)a.lds;
+    if constexpr (GROUPED) xsr[i] = act_row(a, (int)xsr[i]);
+    if constexpr (FAR) xso[i] = xsbase + (int64_t)xsr[i] * a.lds;
+    else xso[i] = xsr[i] * (uint32_t)a.lds;
   }
   copy_xscales(0);
 #pragma unroll
@@ -886,12 +901,12 @@ mx_tile_kernel(MxArgs a) {
   else store_tile<kBF16, FN, FM>(a, part, acc, row0, first, rows, col0);
 }
 
-template <int FMT, int FN, int FM, int WN, int WM, int S, bool GROUPED>
+template <int FMT, int FN, int FM, int WN, int WM, int S, bool GROUPED, bool FAR = false>
 static int launch_tiles(const MxArgs& a, hipStream_t s) {
   using T = Tile<FMT, FN, FM, WN, WM, S>;
   const int64_t groups = tile_grid(a, T::kBN, T::kBM);
   if (int e = check_grid(groups, 64 * T::kWaves)) return e;
-  hipLaunchKernelGGL((mx_tile_kernel<FMT, FN, FM, WN, WM, S, GROUPED>), dim3((unsigned)groups), dim3(64 * T::kWaves), 0, s, a);
+  hipLaunchKernelGGL((mx_tile_kernel<FMT, FN, FM, WN, WM, S, GROUPED, FAR>), dim3((unsigned)groups), dim3(64 * T::kWaves), 0, s, a);
   return check_launch("mx_tile_kernel");
 }
 
@@ -928,11 +943,16 @@ template <int FMT>
 static int launch_grouped(const MxArgs& a, hipStream_t s) {
   constexpr bool k4 = FMT == kRowsMxfp4;
   const int64_t experts = a.m < a.n_expert ? a.m : a.n_expert;
-  const bool wide = a.n_rows * (a.ldq > a.lds ? a.ldq : a.lds) >= ((int64_t)1 << 32);  // 32-bit row offsets
-  if (wide || a.m <= 2 * a.n_expert) return launch_rows<FMT, 1, true>(a, s);
+  if (a.m <= 2 * a.n_expert) return launch_rows<FMT, 1, true>(a, s);
+  // with pair ids a tile's rows may lie anywhere in X, without them they are neighbours.  (8 experts of
+  // 4096 x 14336, MXFP8, 310,000 gathered rows in 4.4 GB: 20.9 ms, 1.74 PFLOP/s; 290,000 in 4.2 GB, by
+  // offsets: 19.9 ms, 1.71.)
+  const int64_t apart = (a.pairs ? a.n_rows : 128) * (a.ldq > a.lds ? a.ldq : a.lds);
+  const bool far = apart >= ((int64_t)1 << 32);
   if (a.m >= (k4 ? 32 : 64) * (int64_t)a.n_expert && ((a.n + 255) / 256) * (a.m / 128 + experts / 2) >= 192)
-    return launch_tiles<FMT, 4, 2, 2, 2, k4 ? 3 : 2, true>(a, s);
-  return launch_tiles<FMT, 2, 1, 2, 2, 4, true>(a, s);
+    return far ? launch_tiles<FMT, 4, 2, 2, 2, k4 ? 3 : 2, true, true>(a, s)
+               : launch_tiles<FMT, 4, 2, 2, 2, k4 ? 3 : 2, true>(a, s);
+  return far ? launch_tiles<FMT, 2, 1, 2, 2, 4, true, true>(a, s) : launch_tiles<FMT, 2, 1, 2, 2, 4, true>(a, s);
 }
 
 int launch_mx_gemm(MxArgs a, int fmt, hipStream_t s) {

@@ -380,6 +380,87 @@ def test_grouped_no_rows_at_all():
     assert np.all(y == -7.0)
 
 
+def spread_rows(x, k, fmt, ldq):
+    """Compact rows of X on the device (codes, scales) with `ldq` bytes between the codes' rows."""
+    c, s = iq4.iq4_rows_bytes(FMT[fmt], k)
+    q = torch.empty(len(x[0]) * ldq, dtype=torch.uint8, device="cuda")
+    rows = q.view(len(x[0]), ldq)
+    rows[:, :c] = 0
+    rows[:, : x[0].shape[1]] = dev(x[0])
+    d = torch.zeros(len(x[1]), s, dtype=torch.uint8, device="cuda")
+    d[:, : k // 32] = dev(x[1])
+    return q, d, ldq, s
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_many_rows_past_4_gib(fmt, gather):
+    """X of 4.6 GB and some 70,000 rows: such a call is an ordinary one of the documented sizes.
+    The rows are 64 KB apart; the same rows side by side must give the same bits (all sums are exact)."""
+    note(f"mx grouped: 70001 rows of X in 4.6 GB, pairs {gather}, {fmt}")
+    counts, n, k, top = [40000, 1, 0, 30000], 16384, 160, 2
+    e, m = len(counts), sum(counts)
+    w, dense = bank(400, e, n, k)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    x = exact_rows(11, fmt, m, k)
+    q, d, ldq, lds = spread_rows(x, k, fmt, 1 << 16)
+    pairs = np.random.default_rng(12).permutation(m * top)[:m] if gather else None
+    row = pairs // top if gather else np.arange(m)
+    assert q.numel() >= 1 << 32 and row.max() > m - 10
+    doff = dev(off.astype(np.int32))
+    y = torch.full((m + 1, n), -7.0, dtype=torch.float16, device="cuda")
+    iq4.iq4_mx_grouped_gemm(w, e, n, k, FMT[fmt], q, ldq, d, lds, m, doff, dev(pairs.astype(np.int32)) if gather else None,
+                            top, m, y, iq4.IQ4_F16, n)
+    assert bool((y[m] == -7.0).all())
+    del q
+    near, dn, ldn, lsn = stored(fmt, x[0][row], x[1][row], k)
+    z = torch.full((m, n), -7.0, dtype=torch.float16, device="cuda")
+    iq4.iq4_mx_grouped_gemm(w, e, n, k, FMT[fmt], near, ldn, dn, lsn, m, doff, None, 0, m, z, iq4.IQ4_F16, n)
+    assert torch.equal(y[:m].view(torch.int16), z.view(torch.int16))
+    for i in (0, 1, 63, 64, 39999, 40000, 40001, 40002, m - 65, m - 1):
+        r = dense[int(np.searchsorted(off, i, side="right")) - 1] @ value(fmt, x[0][row[i]][None], x[1][row[i]][None])[0]
+        assert np.array_equal(host(y[i].double()), rounder("f16")(r)), i
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("ldq", [(1 << 25) - 64, 1 << 25])
+def test_grouped_rows_of_a_tile_2_to_4_gib_apart(fmt, ldq):
+    """The last rows of a tile begin past 2^31 bytes from its first one (and, of X, short of 2^32 and past it)."""
+    note(f"mx grouped: 127 rows {ldq} bytes apart {fmt}")
+    counts, n, k = [3, 121, 0, 3], 200, 160
+    e, m = len(counts), sum(counts)
+    w, dense = bank(500, e, n, k)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    expert = np.repeat(np.arange(e), counts)
+    x = exact_rows(13, fmt, m, k)
+    dx = value(fmt, *x)
+    q, d, ldq, lds = spread_rows(x, k, fmt, ldq)
+    assert (m - 1) * ldq > 1 << 31
+    pairs = np.random.default_rng(14).permutation(m)
+    for p in (None, pairs):
+        row = np.arange(m) if p is None else p
+        r = np.stack([dense[expert[i]] @ dx[row[i]] for i in range(m)])
+        y = torch.full((m, n), -7.0, device="cuda")
+        iq4.iq4_mx_grouped_gemm(w, e, n, k, FMT[fmt], q, ldq, d, lds, m, dev(off.astype(np.int32)),
+                                None if p is None else dev(p.astype(np.int32)), 1, m, y, iq4.IQ4_F32, n)
+        assert np.array_equal(host(y), r)
+
+
+def test_grouped_garbage_offsets_and_pairs_with_rows_far_apart():
+    """As test_grouped_offsets_and_pairs_out_of_range, rows of X so far apart that lanes hold addresses."""
+    note("mx grouped: offsets and pairs out of range, rows 64 MB apart")
+    e, n, k, cap, fmt = 5, 40, 160, 66, "mxfp4"
+    w, _ = bank(100, e, n, k)
+    q, d, ldq, lds = spread_rows(exact_rows(5, fmt, cap, k), k, fmt, 1 << 26)
+    for off in ([-5, 10, 7, 90, 20, 1 << 30], [0, 60, 60, 60, 60, 60], [1 << 30] * 6, [60, 50, 40, 30, 20, 10]):
+        for pairs in (None, [-(1 << 31), (1 << 31) - 1, 59, -1, 0, 65] * 11):
+            y = torch.full((cap + 3, n + 1), -7.0, device="cuda")
+            iq4.iq4_mx_grouped_gemm(w, e, n, k, FMT[fmt], q, ldq, d, lds, cap, dev(np.asarray(off, np.int32)),
+                                    None if pairs is None else dev(np.asarray(pairs, np.int32)), 2, cap, y, iq4.IQ4_F32, n + 1)
+            got = host(y)
+            assert np.all(got[cap:] == -7.0) and np.all(got[:, n:] == -7.0)
+
+
 @pytest.mark.parametrize("tokens,hidden,inter,experts,top", [(4, 512, 256, 16, 4), (90, 512, 384, 12, 3)])
 def test_layer(tokens, hidden, inter, experts, top):
     """A run of the calls as a layer makes them: norm (residual added) to rows, routing,
