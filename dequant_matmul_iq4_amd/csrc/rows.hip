@@ -122,6 +122,14 @@ __global__ void __launch_bounds__(256) dequant_rows_kernel(RowsIn in, uint32_t m
 template <int FMT>
 static int launch_dequant_fmt(RowsIn in, int64_t m, int64_t k, int out_type, void* out, int64_t ldo, hipStream_t s) {
   const uint32_t pieces = (uint32_t)(k / (out_type == kF32 ? 4 : 8));
+  // a launch has fewer than 2^32 threads: the largest binary32 results (2^34 values) are made in two
+  if (m * pieces > ((int64_t)1 << 32) - 256) {
+    const int64_t half = m / 2;
+    if (int e = launch_dequant_fmt<FMT>(in, half, k, out_type, out, ldo, s)) return e;
+    in.codes += half * in.ldq;
+    in.scales += half * in.lds;
+    return launch_dequant_fmt<FMT>(in, m - half, k, out_type, static_cast<float*>(out) + half * ldo, ldo, s);
+  }
   const dim3 grid((unsigned)((m * pieces + 255) / 256));
   const bool st = streams(out_type, m, k);
 #define IQ4_DEQ(T)                                                                                                       \

@@ -324,3 +324,50 @@ def test_rows_more_than_32_bits_apart():
     two = torch.stack([q[:512], q[fq:]])
     same_rows("mxfp8", k, two, d, oracle.quantize_rows(yr, "mxfp8"))
     assert bool((q[512:fq] == 0xEE).all())
+
+
+@pytest.mark.parametrize("m,k", [(1 << 14, 1 << 20), ((1 << 14) + 1, (1 << 20) - 64), (1 << 21, 1 << 13)])
+def test_largest_calls(m, k):
+    """m * k up to the documented 2^34: the binary32 decode alone would take 2^32 lanes.  Every call's rows
+    are those of calls of a few thousand rows."""
+    note(f"rows: {m} x {k}, decoded, quantised and normed at once and in parts")
+    assert (1 << 34) - m * k <= 1 << 20 and m * k <= 1 << 34
+    step = (1 << 30) // k
+    f4, f8 = FMT["mxfp4"], FMT["mxfp8"]
+    q, d, ldq, lds = row_buffers("mxfp4", m, k)
+    n = min(step, 1024)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    codes = torch.randint(0, 256, (n, ldq), dtype=torch.uint8, device="cuda", generator=g)
+    codes[:, k // 2:] = 0
+    d[:, : k // 32] = torch.randint(120, 134, (1, k // 32), dtype=torch.uint8, device="cuda", generator=g)
+    d[:, k // 32:] = 0
+    for i in range(0, m, n):  # every run of rows its own
+        q[i:i + n] = (codes ^ ((7 * (i // n) + 1) % 256))[: m - i]
+    q[:, k // 2:] = 0
+    out = torch.full((m, k), -7.0, device="cuda")
+    iq4.iq4_dequant_rows(q, ldq, d, lds, f4, m, k, iq4.IQ4_F32, out, k)
+    small = torch.empty(step, k, device="cuda")
+    for i in range(0, m, step):
+        rows = min(step, m - i)
+        iq4.iq4_dequant_rows(q[i:], ldq, d[i:], lds, f4, rows, k, iq4.IQ4_F32, small, k)
+        assert torch.equal(out[i:i + rows].view(torch.int32), small[:rows].view(torch.int32)), i
+    for i in (0, m // 2 - 1, m // 2, m - 1):
+        want = oracle.dequant_rows(host(q[i:i + 1, : k // 2]), host(d[i:i + 1, : k // 32]), "mxfp4")
+        assert np.array_equal(host(out[i]).astype(np.float64), want[0]), i
+    del q, d, small
+    for norm_too in (False, True):
+        q, d, ldq, lds = row_buffers("mxfp8", m, k)
+        q2, d2, _, _ = row_buffers("mxfp8", step, k)
+
+        def call(x, rows, q, d):
+            if norm_too:
+                iq4.iq4_rmsnorm(x, k, None, 0, iq4.IQ4_F32, rows, k, None, 1e-6, None, 0, None, 0, 0, f8, q, ldq, d, lds)
+            else:
+                iq4.iq4_quantize_rows(x, iq4.IQ4_F32, rows, k, k, f8, q, ldq, d, lds)
+
+        call(out, m, q, d)
+        for i in range(0, m, step):
+            rows = min(step, m - i)
+            call(out[i:], rows, q2, d2)
+            assert torch.equal(q[i:i + rows], q2[:rows]) and torch.equal(d[i:i + rows], d2[:rows]), i
+        del q, d, q2, d2
