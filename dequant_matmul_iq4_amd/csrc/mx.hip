@@ -605,6 +605,13 @@ struct Tile {
   }
 };
 
+// Lanes of a wave read what others of it wrote to LDS: the hardware keeps a wave's accesses in order,
+// and this keeps the compiler from moving them past each other.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // `rows` x `cols` values of Y's type in LDS (rows of PITCH, at most 32 x COLS) to Y from (row0,
 // col0) on, by one wave: eight columns a lane, past the L2 (nothing here reads Y again: the long
 // prompt's 374 MB of results took 428 us with ordinary stores and 412 with these).
@@ -658,7 +665,9 @@ __device__ __forceinline__ void store_tile(const MxArgs& a, uint8_t* lds, const 
         if constexpr (TYPE == kF32) *reinterpret_cast<f32x4*>(to) = f32x4{v[0], v[1], v[2], v[3]};
         else *reinterpret_cast<u32x2*>(to) = u32x2{pack2<TYPE>(v[0], v[1]), pack2<TYPE>(v[2], v[3])};
       }
+    wave_fence();
     store_rows_piece<E, kCols, kPitch>(a, part, row0 + first + 32 * m, min(32, rows - first - 32 * m), col0, cols);
+    wave_fence();
   }
 }
 
