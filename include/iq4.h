@@ -495,8 +495,10 @@ int iq4_mx_pack_weights(const void* codes, int64_t ldq, const void* scales, int6
  *   y       [m][ldy] of y_dtype (IQ4_F32, IQ4_F16, IQ4_BF16), ldy >= n, element aligned;
  *           columns n .. ldy - 1 are left alone.
  *   m >= 0 (0: no-op), any n >= 1, k % 32 == 0.  No workspace.
- * Deterministic; for m <= 16 each row is bitwise the m = 1 call's.  Every product is exact,
- * MXFP8 ones too (the instruction alone loses some: the kernels multiply in two parts).
+ * Deterministic; for m <= 16 each row is bitwise the m = 1 call's.  The products enter the sums
+ * exactly, MXFP8 ones too (the instruction alone loses some: the kernels multiply in two
+ * parts), and the sums round as fp32 additions in some order do: exact where every partial sum
+ * is a binary32 value, otherwise within (k - 1) * 2^-24 of the sum of the magnitudes.
  * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED (k % 32, sizes; a grid of 2^32 threads).
  */
 int iq4_mx_gemm(const void* packed, int64_t n, int64_t k, int32_t fmt, const void* codes, int64_t ldq,

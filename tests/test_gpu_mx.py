@@ -270,6 +270,61 @@ def test_few_rows_equal_single_rows_bitwise(fmt, n, k):
             assert bits_equal(y[i:i + 1], ones[i]), (m, i)
 
 
+@pytest.mark.parametrize("m", [7, 30, 200])
+def test_8_bit_sums_of_one_scale_are_exact(m):
+    """With one scale for all blocks, sums of 128 products that binary32 can hold are the exact ones: of all
+    E4M3 codes of magnitude 2 and above (products with E2M1 are multiples of 2^-3, the sums below
+    128 * 448 * 6 < 2^19: 22 bits), of all below 2 (multiples of 2^-10, below 128 * 1.875 * 6 < 2^11: 21
+    bits), and of all up to 15 (multiples of 2^-10, below 128 * 15 * 6 < 2^14: 24 bits)."""
+    note(f"mx gemm: E4M3 codes with one scale, {m} rows")
+    n, k = 96, 128
+    rng = np.random.default_rng(m)
+    cw = rng.integers(0, 256, (n, k // 2)).astype(np.uint8)
+    cw[::3] = rng.choice(np.array([0x77, 0x71, 0x17, 0x9F, 0xF1, 0x79, 0x11], np.uint8), (n // 3, k // 2))  # +-6 and +-1/2
+    sw, sx = np.full((n, 4), 127, np.uint8), np.full((m, 4), 127, np.uint8)
+    w, dw = packed(cw, sw, n, k), value("mxfp4", cw, sw)
+    ends = np.array([0x7E, 0xFE, 0x41, 0xC1, 0x40, 0x43], np.uint8)  # 448, 2.25, 2, 2.75
+    for name, mags in {"high": np.arange(0x40, 0x7F), "low": np.arange(0x40), "both": np.arange(0x58)}.items():
+        c = (rng.choice(mags, (m, k)) | rng.choice([0, 0x80], (m, k))).astype(np.uint8)
+        if name == "high":
+            c[::2] = rng.choice(ends, c[::2].shape)
+        r = oracle.mx_product(dw, value("mxfp8", c, sx))
+        assert np.array_equal(r, r.astype(np.float32))
+        y = product(w, (c, sx), "mxfp8", n, k, m, "f32")
+        assert np.array_equal(y, r), (name, float(np.max(np.abs(y - r))))
+
+
+@pytest.mark.parametrize("m", [7, 30, 200])
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_scales_that_differ_inside_a_row(fmt, m):
+    """Any order of binary32 additions gives the exact sum here.  First, blocks up to 2^9 (MXFP8 2^6) apart: the
+    products are multiples of 2^-2 * 2^-9 (2^-4 * 2^-6), the sums below 128 * 6 * 6 < 2^13 (128 * 15 * 6 <
+    2^14), 24 bits.  Then a single product of 1 beside three blocks 2^-20 (2^-18) below it: multiples of
+    2^-22, sums below 1 + 96 * 36 * 2^-20 < 2 (1 + 96 * 90 * 2^-18 < 2), 23 bits."""
+    note(f"mx gemm: scales that differ inside a row, {m} rows {fmt}")
+    n, k = 96, 128
+    rng = np.random.default_rng(m)
+    low = 5 if fmt == "mxfp4" else 3
+    cw, _ = exact_weights(5, n, k)
+    c, _ = exact_rows(6, fmt, m, k)
+    sw = (127 - rng.integers(0, low + 1, (n, 4))).astype(np.uint8)
+    sx = (127 - rng.integers(0, (4 if fmt == "mxfp4" else 3) + 1, (m, 4))).astype(np.uint8)
+    r = oracle.mx_product(value("mxfp4", cw, sw), value(fmt, c, sx))
+    assert np.array_equal(product(packed(cw, sw, n, k), (c, sx), fmt, n, k, m, "f32"), r)
+    for block in range(4):
+        bw, bx = cw.copy(), c.copy()
+        sw, sx = np.full((n, 4), 117, np.uint8), np.full((m, 4), 117 if fmt == "mxfp4" else 119, np.uint8)
+        sw[:, block], sx[:, block] = 127, 127
+        bw[:, 16 * block:16 * block + 16] = 0
+        bw[:, 16 * block + 3] = 0x02  # 1
+        each = 16 if fmt == "mxfp4" else 32
+        bx[:, each * block:each * block + each] = 0
+        bx[:, each * block + 3 * each // 16] = 0x02 if fmt == "mxfp4" else 0x38
+        r = oracle.mx_product(value("mxfp4", bw, sw), value(fmt, bx, sx))
+        assert np.all(np.abs(r - 1) < 0.5)
+        assert np.array_equal(product(packed(bw, sw, n, k), (bx, sx), fmt, n, k, m, "f32"), r), block
+
+
 # ---- by expert ------------------------------------------------------------------------------
 
 
