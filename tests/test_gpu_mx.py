@@ -325,6 +325,34 @@ def test_scales_that_differ_inside_a_row(fmt, m):
         assert np.array_equal(product(packed(bw, sw, n, k), (bx, sx), fmt, n, k, m, "f32"), r), block
 
 
+def tiles(n, m, bn, bm):
+    return -(-n // bn) * -(-m // bm)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("m,n", [(1100, 6392), (900, 6144), (300, 5000), (100, 1000), (20, 1000), (9, 1000)])
+def test_exact_sums_over_many_steps(fmt, m, n):
+    """19 steps of 128 elements, five quads of scales, results stored 16 bytes at a time: 256 x 128 tiles (from 224 of
+    them), 128 x 128 (MXFP4) and 128 x 64 (from 160), 64 x 64, and the kernel for few rows.  All sums are
+    exact: E2M1 products are multiples of 2^-4 and at most 144, and 2336 * 144 < 2^24 * 2^-4; E4M3 ones, with
+    weight scales 127 and 128 and row scales 126 and 127, multiples of 2^-5 and at most 180, and
+    2336 * 180 < 2^24 * 2^-5."""
+    note(f"mx gemm exact: {m} x {n} x 2336 {fmt}")
+    k = 2336
+    assert (tiles(n, m, 256, 128) >= 224) == (m == 1100)
+    assert (tiles(n, m, 128, 128) >= 160) == (m >= 900) and (tiles(n, m, 128, 64) >= 160) == (m >= 300)
+    cw, sw = exact_weights(m, n, k)
+    c, sx = exact_rows(m, fmt, m, k)
+    if fmt == "mxfp8":
+        sw, sx = np.maximum(sw, 127), np.minimum(sx, 127)
+    r = oracle.mx_product(value("mxfp4", cw, sw), value(fmt, c, sx))
+    w = packed(cw, sw, n, k)
+    for out in TYPES:
+        with np.errstate(over="ignore"):
+            want = rounder(out)(r)
+        assert np.array_equal(product(w, (c, sx), fmt, n, k, m, out), want), out
+
+
 # ---- by expert ------------------------------------------------------------------------------
 
 
@@ -514,6 +542,39 @@ def test_grouped_garbage_offsets_and_pairs_with_rows_far_apart():
                                     None if pairs is None else dev(np.asarray(pairs, np.int32)), 2, cap, y, iq4.IQ4_F32, n + 1)
             got = host(y)
             assert np.all(got[cap:] == -7.0) and np.all(got[:, n:] == -7.0)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("counts,n", [([300, 0, 129, 340], 7168), ([30, 0, 129, 2, 65], 200), ([1, 0, 2, 1, 3], 1000)])
+def test_grouped_over_many_steps(fmt, counts, n):
+    """10 steps, three quads of scales: 256 x 128 tiles (28 of them side by side, some 6 + 4 / 2 high: at least
+    192, and 64 rows an expert), 128 x 64, and few rows; in each, rows of X side by side, gathered, and gathered from 4 GiB
+    and more.  E2M1 products are multiples of 2^-4, at most 144: 1184 * 144 < 2^20.  E4M3 ones, with row
+    scales 126 and 127, multiples of 2^-6, at most 180: 1184 * 180 < 2^18."""
+    note(f"mx grouped: {counts} {n} x 1184 {fmt}")
+    e, total, k, top = len(counts), sum(counts), 1184, 2
+    assert (-(-n // 256) * (total // 128 + e // 2) >= 192) == (n == 7168) and (total <= 2 * e) == (n == 1000)
+    w, dense = bank(600, e, n, k)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    rows = {"side by side": (total, None), "gathered": ((total + 1) // 2, np.random.default_rng(15).permutation(total))}
+    for name, (count, pairs) in rows.items():
+        c, sx = exact_rows(16, fmt, count, k)
+        if fmt == "mxfp8":
+            sx = np.minimum(sx, 127)
+        dx = value(fmt, c, sx)
+        dx = dx if pairs is None else dx[pairs // top]
+        r = np.concatenate([dx[off[i]:off[i + 1]] @ dense[i].T for i in range(e)])
+        for out in TYPES:
+            y = grouped(w, e, n, k, fmt, (c, sx), off, pairs, top, total, out)
+            assert np.array_equal(y, rounder(out)(r)), (name, out)
+        if pairs is None:
+            continue
+        q, d, ldq, lds = spread_rows((c, sx), k, fmt, ((1 << 32) // count + 64) // 64 * 64)
+        assert count * ldq >= 1 << 32
+        y = torch.full((total, n), -7.0, device="cuda")
+        iq4.iq4_mx_grouped_gemm(w, e, n, k, FMT[fmt], q, ldq, d, lds, count, dev(off.astype(np.int32)),
+                                dev(pairs.astype(np.int32)), top, total, y, iq4.IQ4_F32, n)
+        assert np.array_equal(host(y), r), "far apart"
 
 
 @pytest.mark.parametrize("tokens,hidden,inter,experts,top", [(4, 512, 256, 16, 4), (90, 512, 384, 12, 3)])
