@@ -25,8 +25,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // lane 16g + c, byte j has the scale of block 4 (4 kq + j) + g.  What lies past n or k is zero
 // (a zero code times any scale below 255 adds nothing).
 // A lane moves the 16-byte blocks of four tiles and a scale word, so that the packed form is
-// written in whole kilobytes; bound by memory, and run once per matrix: 14336 x 4096, 31 MB each
-// way, 35 us (1.8 TB/s).
+// written in whole kilobytes.  Run once per matrix: 14336 x 4096, 31 MB each way, 35 us (1.8 TB/s, a
+// copy takes 12): blocks are loaded byte by byte, which spares the source any alignment.  A small matrix
+// is a launch: 128 of 1536 x 2048 in 128 calls 910 us, 7.1 each.
 __global__ void __launch_bounds__(256) mx_pack_kernel(const uint8_t* __restrict__ codes, int64_t ldq,
                                                       const uint8_t* __restrict__ scales, int64_t lds, int64_t n,
                                                       int blocks, int kt_n, int kq_n, uint8_t* __restrict__ packed) {
@@ -278,7 +279,10 @@ __device__ __forceinline__ int act_row(const MxArgs& a, int p) {
 // Bound by the weights' way from memory: a row tile's quad is 4.3 KB for 4 (MXFP8 8)
 // instructions of 16 clocks.  The waves over k are there to have enough of it under way.  In
 // graphs of launches: 4096 x 4096, m = 1 3.3 us (2.7 TB/s; an empty launch takes 1.7); 2560 x 6144,
-// m = 4, MXFP8 4.9; 128 experts of 1536 x 2048, 32 pairs, MXFP8 12.1 (2.6 TB/s).
+// m = 4, MXFP8 4.9 to 5.8 by the card; 128 experts of 1536 x 2048, 32 pairs, MXFP8 12.1 (2.6 TB/s).
+// (2560 rows and eight waves, in one run: k = 4096, a quad a wave, 5.1 us; 6144, two quads in half of the
+// waves, 5.8, in MXFP4 4.8; 8192, two in each, 6.6.  The quads' loads are all under way at once: it is the
+// bytes, the second quad and, for MXFP8, twice the loads of rows and twice the instructions.)
 //
 // Rows by expert: workgroup column i stands for output row i; it works if row i begins a tile
 // of its expert (MT x 16 rows from the expert's first on), so a wave finds its expert with one
@@ -618,7 +622,9 @@ __device__ __forceinline__ void wave_fence() {
 
 // `rows` x `cols` values of Y's type in LDS (rows of PITCH, at most 32 x COLS) to Y from (row0,
 // col0) on, by one wave: eight columns a lane, past the L2 (nothing here reads Y again: the long
-// prompt's 374 MB of results took 428 us with ordinary stores and 412 with these).
+// prompt's 374 MB of results took 428 us with ordinary stores and 412 with these).  Rows that are no
+// multiple of 16 bytes are stored element by element: 13056 x 14335 x 4096 to bf16 565 us with ldy = n, 409
+// with ldy = 14336 (f32 776, 14336 x 4096 535).
 template <typename E, int COLS, int PITCH>
 __device__ __forceinline__ void store_rows_piece(const MxArgs& a, const E* part, int64_t row0, int rows, int64_t col0,
                                                  int cols) {
@@ -926,13 +932,16 @@ static int launch_tiles(const MxArgs& a, hipStream_t s) {
 // Which kernel, by the workgroups each tile gives (times in us on an MI355X, MXFP4 unless
 // MXFP8 is named).  The larger tile reads less per product; below some 160-220 workgroups of it
 // the 256 CUs are not filled and the next smaller one is faster:
-//   256 x 128 from 224: 14336 x 4096, m = 512 (224): 22.0, 128 x 128 23.3; 5000 x 2592,
-//     m = 1024 (160): 20.9 for 17.9.  MXFP8, same m: 50.2 for 52.8; m = 333 (168): 47.3, 128 x 64 43.7.
-//   128 x 128 from 160, MXFP4 only: 4096 x 4096, m = 1024 (256): 14.9, 128 x 64 17.4; m = 512
-//     (128): 12.8 for 10.7.  MXFP8, m = 1024: 35.2 for 32.9.
-//   128 x 64 from 160, else 64 x 64: 4096 x 4096, m = 333 (192): 9.9 for 11.2; m = 256 (128): 9.8 for 8.9.
+//   256 x 128 from 224: 14336 x 4096, m = 512 (224): 21.2, 128 x 128 22.6; 5000 x 2592,
+//     m = 1024 (160): 19.6 for 17.2.  MXFP8, 128 x 64 on the other side: m = 512 47.0 for 55.2; 5000 x 2592
+//     36.4 for 28.5.
+//   128 x 128 from 160, MXFP4 only: 4096 x 4096, m = 1024 (256): 14.4, 128 x 64 16.1; m = 512
+//     (128): 12.6 for 10.3.  MXFP8: 33.3 for 29.2; 29.4 for 18.1.
+//   128 x 64 from 160, else 64 x 64: 4096 x 4096, m = 333 (192): 9.7 for 11.2; m = 256 (128): 9.6 for 8.9.
+//     MXFP8: 17.9 for 19.7; 16.7 for 14.0.
 //   Up to 32 rows straight from memory unless 64 x 64 fills the CUs: 4096 x 4096, m = 32
-//     (64): 5.2 for 6.2; 14336 x 4096 (224): 14.6 for 8.9.
+//     (64): 5.1 for 6.1; 14336 x 4096 (224): 14.4 for 8.9.  MXFP8: 7.6 for 12.1; 22.9 for 13.2 (near the border,
+//     10000 x 2592, m = 24 (157): MXFP4 6.5 for 6.9, MXFP8 13.6 for 10.1).
 template <int FMT>
 static int launch_dense(const MxArgs& a, hipStream_t s) {
   constexpr bool k4 = FMT == kRowsMxfp4;
@@ -949,9 +958,13 @@ static int launch_dense(const MxArgs& a, hipStream_t s) {
 }
 
 // By expert: how the rows fall is not known here, only their average r.  Straight from memory
-// up to r = 2 (128 experts of 1536 x 2048: r = 1 17.7 us, 128 x 64 tiles 19.6; r = 4 42.8 for
-// 37.4), 256 x 128 tiles from r = 32 (MXFP8 64) if there are enough of them (r = 64: 60.7, 128 x 64
-// 65.4; r = 16: 52.3 for 49.8; 16 experts, r = 128, some 144 tiles: 13.7 for 13.3).
+// up to r = 2: 128 experts of 1536 x 2048, r = 1 16.9 us, 128 x 64 tiles 18.4; r = 2 28.5 for 26.6; r = 4 40.9
+// for 34.1; 64 experts of 512 x 1024, r = 2 5.0 for 5.4, r = 4 6.6 for 6.4.  MXFP8: 22.0 for 24.2, 37.5 for
+// 33.2, 54.4 for 42.2; 7.4 for 7.3, 8.9 for 8.2.
+// 256 x 128 tiles from r = 32 (MXFP8 64) if there are enough of them.  128 experts of 1536 x 2048, r = 16 49.5, 128 x
+// 64 tiles 47.1; r = 32 53.2 for 53.4; r = 64 57.4 for 61.2; 16 experts, r = 128, some 144 tiles 12.9 for 11.9.  MXFP8:
+// 79.8 for 59.8, 82.0 for 64.7, 90.0 for 84.6, r = 128 113 for 121; with 128 experts of 2048 x 768 r = 32 45.9
+// for 44.9, r = 64 51.2 for 56.9; 16 experts 26.4 for 17.4.
 template <int FMT>
 static int launch_grouped(const MxArgs& a, hipStream_t s) {
   constexpr bool k4 = FMT == kRowsMxfp4;
