@@ -220,6 +220,46 @@ def test_nan_scales_and_codes(fmt, m):
     assert np.isnan(y[:, 7]).all() and np.isnan(y[m - 2]).all() and np.isfinite(y[0, :7]).all()
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("m", [5, 30, 130])
+def test_nan_blocks_as_the_quantiser_makes_them(fmt, m):
+    """A block with an infinity or a NaN is held as zero codes with a NaN scale: its row's results are NaN all the
+    same, and no other row's are.  Rows, scales and codes of both operands in one buffer, side by side."""
+    note(f"mx gemm: rows with infinities and NaN, quantised and multiplied, {m} rows {fmt}")
+    n, k = 72, 160
+    rng = np.random.default_rng(m)
+    x = rng.standard_normal((m, k)).astype(np.float32)
+    x[1, 3], x[m - 1, 159], x[2, 64:96] = np.nan, np.inf, 0
+    wf = rng.standard_normal((n, k)).astype(np.float32)
+    wf[7, 130], wf[70, 0] = -np.inf, np.nan
+
+    def held(v, f):
+        c, s = iq4.iq4_rows_bytes(FMT[f], k)
+        both = torch.full((len(v), c + s + 16), 0xEE, dtype=torch.uint8, device="cuda")
+        iq4.iq4_quantize_rows(dev(v), iq4.IQ4_F32, len(v), k, k, FMT[f], both, c + s + 16, both[:, c:], c + s + 16)
+        assert bool((both[:, c + s:] == 0xEE).all())
+        return both, c, c + s + 16
+
+    wb, wc, wld = held(wf, "mxfp4")
+    xb, xc, xld = held(x, fmt)
+    w = torch.empty(iq4.iq4_mx_packed_bytes(n, k), dtype=torch.uint8, device="cuda")
+    iq4.iq4_mx_pack_weights(wb, wld, wb[:, wc:], wld, n, k, w)
+    dw, dx = value("mxfp4", *oracle.quantize_rows(wf, "mxfp4")), value(fmt, *oracle.quantize_rows(x, fmt))
+    r, tol = bound(dw, dx, k, "f32")
+    off = dev(np.array([0, m], np.int32))
+    for by_expert in (False, True):
+        y = torch.full((m, n), -7.0, device="cuda")
+        if by_expert:
+            iq4.iq4_mx_grouped_gemm(w, 1, n, k, FMT[fmt], xb, xld, xb[:, xc:], xld, m, off, None, 0, m, y, iq4.IQ4_F32, n)
+        else:
+            iq4.iq4_mx_gemm(w, n, k, FMT[fmt], xb, xld, xb[:, xc:], xld, m, y, iq4.IQ4_F32, n)
+        got = host(y).astype(np.float64)
+        bad = np.isnan(r)
+        assert bad[[1, m - 1]].all() and bad[:, [7, 70]].all() and not bad[[0, 2]][:, :7].any()
+        assert np.array_equal(np.isnan(got), bad)
+        assert np.all(np.abs(got - r)[~bad] <= tol[~bad])
+
+
 def test_whole_range_of_8_bit_codes():
     """Every E4M3 code next to the largest ones: the largest product of a row is some 2^21
     times its smallest, and the small ones must not be lost."""

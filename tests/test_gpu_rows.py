@@ -371,3 +371,17 @@ def test_largest_calls(m, k):
             call(out[i:], rows, q2, d2)
             assert torch.equal(q[i:i + rows], q2[:rows]) and torch.equal(d[i:i + rows], d2[:rows]), i
         del q, d, q2, d2
+
+
+@pytest.mark.parametrize("k", [256, 16640])
+@pytest.mark.parametrize("t", list(TYPES))
+def test_norm_of_twice_a_row_in_place(t, k):
+    note(f"norm: x, its residual and their sum one buffer, {t}, k = {k}")
+    x, _, gain = inputs(61, 3, k, t)
+    b = floats(x, t)
+    q, d, ldq, lds = row_buffers("mxfp8", 3, k)
+    iq4.iq4_rmsnorm(b, k, b, k, TYPES[t][0], 3, k, torch.from_numpy(gain).cuda(), 1e-6, b, k, None, 0, 0, FMT["mxfp8"], q, ldq,
+                    d, lds)
+    hr, yr = norm_oracle(x, x, t, gain, 1e-6)
+    assert np.array_equal(host(b.double()), hr)
+    same_rows("mxfp8", k, q, d, oracle.quantize_rows(yr, "mxfp8"))
