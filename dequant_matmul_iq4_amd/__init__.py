@@ -81,6 +81,23 @@ SIGNATURES = {
                                    _c_i64, _c_p]),
     "iq4_mx_grouped_gemm": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i32, _c_p, _c_i64, _c_p, _c_i64, _c_i64,
                                            _c_p, _c_p, _c_i32, _c_i64, _c_p, _c_i32, _c_i64, _c_p]),
+    "iq4_g4_packed_bytes": (_c_i64, [_c_i64, _c_i64, _c_i32, _c_i32]),
+    "iq4_g4_pack_weights": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_i32, _c_p,
+                                           _c_p]),
+    "iq4_g4_qmv": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_p, _c_i32, _c_i64, _c_i64, _c_p,
+                                  _c_i32, _c_i64, _c_p]),
+    "iq4_g4_grouped_qmv": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_p, _c_i32, _c_i64,
+                                          _c_i64, _c_p, _c_p, _c_i32, _c_i64, _c_p, _c_i32, _c_i64, _c_p]),
+    "iq4_moe_dispatch": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_i64, _c_p,
+                                        _c_i32, _c_i64, _c_p]),
+    "iq4_moe_combine": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_i32, _c_i64, _c_p, _c_i64,
+                                       _c_p, _c_i32, _c_i64, _c_p]),
+    "iq4_moe_combine_grad": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_p, _c_i32, _c_i64, _c_i64, _c_p, _c_p, _c_i64,
+                                            _c_i32, _c_i64, _c_p, _c_i64, _c_p, _c_p]),
+    "iq4_swiglu": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i32, _c_i64, _c_i64, _c_p, _c_i32, _c_i64, _c_i32,
+                                  _c_p, _c_i64, _c_p, _c_i64, _c_p]),
+    "iq4_swiglu_grad": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_i32, _c_i64, _c_i64, _c_p,
+                                       _c_i64, _c_p, _c_i64, _c_p]),
 }
 
 _lib = None
@@ -287,3 +304,51 @@ def iq4_mx_grouped_gemm(packed, n_expert, n, k, fmt, codes, ldq, scales, lds, n_
                         y, y_dtype, ldy, stream=None):
     _call("iq4_mx_grouped_gemm", _ptr(packed), n_expert, n, k, fmt, _ptr(codes), ldq, _ptr(scales), lds, n_rows,
           _ptr(offsets), _ptr(pairs), top_k, n_pairs, _ptr(y), y_dtype, ldy, _stream(stream))
+
+
+def iq4_g4_packed_bytes(n, k, group, zeros) -> int:
+    return lib().iq4_g4_packed_bytes(n, k, group, zeros)
+
+
+def iq4_g4_pack_weights(codes, ldq, scales, lds, zeros, ldz, n, k, group, packed, stream=None):
+    _call("iq4_g4_pack_weights", _ptr(codes), ldq, _ptr(scales), lds, _ptr(zeros), ldz, n, k, group, _ptr(packed),
+          _stream(stream))
+
+
+def iq4_g4_qmv(packed, n, k, group, scale_dtype, zeros, x, x_dtype, ldx, m, y, y_dtype, ldy, stream=None):
+    _call("iq4_g4_qmv", _ptr(packed), n, k, group, scale_dtype, zeros, _ptr(x), x_dtype, ldx, m, _ptr(y), y_dtype, ldy,
+          _stream(stream))
+
+
+def iq4_g4_grouped_qmv(packed, n_expert, n, k, group, scale_dtype, zeros, x, x_dtype, ldx, n_rows, offsets, pairs, top_k,
+                       n_pairs, y, y_dtype, ldy, stream=None):
+    _call("iq4_g4_grouped_qmv", _ptr(packed), n_expert, n, k, group, scale_dtype, zeros, _ptr(x), x_dtype, ldx, n_rows,
+          _ptr(offsets), _ptr(pairs), top_k, n_pairs, _ptr(y), y_dtype, ldy, _stream(stream))
+
+
+def iq4_moe_dispatch(x, x_dtype, ldx, n_tok, hidden, slot_row, w, top_k, n_rows, rows, rows_dtype, ldr, stream=None):
+    _call("iq4_moe_dispatch", _ptr(x), x_dtype, ldx, n_tok, hidden, _ptr(slot_row), _ptr(w), top_k, n_rows, _ptr(rows),
+          rows_dtype, ldr, _stream(stream))
+
+
+def iq4_moe_combine(rows, rows_dtype, ldr, n_rows, slot_row, w, n_tok, top_k, hidden, add, lda, out, out_dtype, ldo,
+                    stream=None):
+    _call("iq4_moe_combine", _ptr(rows), rows_dtype, ldr, n_rows, _ptr(slot_row), _ptr(w), n_tok, top_k, hidden,
+          _ptr(add), lda, _ptr(out), out_dtype, ldo, _stream(stream))
+
+
+def iq4_moe_combine_grad(dout, dout_dtype, ldd, rows, rows_dtype, ldr, n_rows, slot_row, w, n_tok, top_k, hidden, drows,
+                         ldg, dw, stream=None):
+    _call("iq4_moe_combine_grad", _ptr(dout), dout_dtype, ldd, _ptr(rows), rows_dtype, ldr, n_rows, _ptr(slot_row),
+          _ptr(w), n_tok, top_k, hidden, _ptr(drows), ldg, _ptr(dw), _stream(stream))
+
+
+def iq4_swiglu(g, ldg, u, ldu, dtype, m, k, y, y_dtype, ldy, fmt=IQ4_ROWS_Q8_1, codes=None, ldq=0, scales=None, lds=0,
+               stream=None):
+    _call("iq4_swiglu", _ptr(g), ldg, _ptr(u), ldu, dtype, m, k, _ptr(y), y_dtype, ldy, fmt, _ptr(codes), ldq,
+          _ptr(scales), lds, _stream(stream))
+
+
+def iq4_swiglu_grad(dh, dh_dtype, lddh, g, ldg, u, ldu, dtype, m, k, dg, lddg, du, lddu, stream=None):
+    _call("iq4_swiglu_grad", _ptr(dh), dh_dtype, lddh, _ptr(g), ldg, _ptr(u), ldu, dtype, m, k, _ptr(dg), lddg,
+          _ptr(du), lddu, _stream(stream))

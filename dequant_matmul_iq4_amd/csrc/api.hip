@@ -10,8 +10,11 @@
 #include "qmv.hpp"
 #include "gemm.hpp"
 #include "moe.hpp"
+#include "g4.hpp"
 #include "mx.hpp"
 #include "rows.hpp"
+#include "slots.hpp"
+#include "swiglu.hpp"
 
 namespace iq4 {
 
@@ -616,6 +619,330 @@ int iq4_mx_grouped_gemm(const void* packed, int32_t n_expert, int64_t n, int64_t
   a.pairs = pairs;
   a.top_k = top_k;
   return launch_mx_gemm(a, fmt, as_stream(stream));
+}
+
+// ---- 4-bit weights with group scales --------------------------------------------------
+
+static int check_g4_matrix(const char* fn, int64_t n, int64_t k, int32_t group) {
+  if (n <= 0 || k <= 0) return set_error(IQ4_E_ARG, "%s: n and k must be positive", fn);
+  if (group != 32 && group != 64 && group != 128)
+    return set_error(IQ4_E_UNSUPPORTED, "%s: group must be 32, 64 or 128 (group=%d)", fn, group);
+  if (k % kQK || k > ((int64_t)1 << 20) || n > ((int64_t)1 << 24))
+    return set_error(IQ4_E_UNSUPPORTED, "%s: k must be a multiple of 32, k <= 2^20, n <= 2^24 (n=%lld k=%lld)", fn,
+                     (long long)n, (long long)k);
+  return IQ4_OK;
+}
+
+int64_t iq4_g4_packed_bytes(int64_t n, int64_t k, int32_t group, int32_t zeros) {
+  if (n <= 0 || k <= 0 || (group != 32 && group != 64 && group != 128) || k % kQK || k > ((int64_t)1 << 20) ||
+      n > ((int64_t)1 << 24))
+    return -1;
+  return g4_packed_bytes(n, k, group, zeros != 0);
+}
+
+int iq4_g4_pack_weights(const void* codes, int64_t ldq, const void* scales, int64_t lds, const void* zeros, int64_t ldz,
+                        int64_t n, int64_t k, int32_t group, void* packed, void* stream) {
+  const char* fn = "iq4_g4_pack_weights";
+  clear_error();
+  if (int e = check_g4_matrix(fn, n, k, group)) return e;
+  const int64_t groups = (k + group - 1) / group;
+  if (ldq < k / 2 || lds < groups || (zeros && ldz < groups))
+    return set_error(IQ4_E_ARG, "%s: ldq must be >= k / 2, lds and ldz >= the groups of a row", fn);
+  if (!codes || !scales || !packed) return set_error(IQ4_E_ARG, "%s: null pointer", fn);
+  if (!aligned(packed, 256)) return set_error(IQ4_E_ALIGN, "%s: packed must be 256-byte aligned", fn);
+  if (g4_row_tiles(n) * g4_k_quads(k) * 64 >= ((int64_t)1 << 32) - 256)
+    return set_error(IQ4_E_UNSUPPORTED, "%s: n * k too large", fn);
+  const uint8_t* p = static_cast<const uint8_t*>(packed);
+  const uint8_t* c = static_cast<const uint8_t*>(codes);
+  const uint8_t* d = static_cast<const uint8_t*>(scales);
+  const uint8_t* z = static_cast<const uint8_t*>(zeros);
+  const int64_t bytes = g4_packed_bytes(n, k, group, zeros != nullptr);
+  if ((c < p + bytes && p < c + (n - 1) * ldq + k / 2) || (d < p + bytes && p < d + 2 * ((n - 1) * lds + groups)) ||
+      (z && z < p + bytes && p < z + (n - 1) * ldz + groups))
+    return set_error(IQ4_E_ARG, "%s: packed overlaps codes, scales or zeros", fn);
+  G4Pack a{};
+  a.codes = c;
+  a.ldq = ldq;
+  a.scales = static_cast<const uint16_t*>(scales);
+  a.lds = lds;
+  a.zeros = z;
+  a.ldz = ldz;
+  a.n = n;
+  a.k = k;
+  a.group = group;
+  a.packed = static_cast<uint8_t*>(packed);
+  return launch_g4_pack(a, as_stream(stream));
+}
+
+static inline bool elem_aligned(const void* p, int32_t type) { return aligned(p, type == IQ4_F32 ? 4 : 2); }
+
+static int check_g4_args(const char* fn, int64_t n, int64_t k, int32_t group, int32_t scale_dtype, int32_t x_dtype,
+                         int32_t y_dtype, int64_t m) {
+  if (int e = check_g4_matrix(fn, n, k, group)) return e;
+  if (scale_dtype != IQ4_F16 && scale_dtype != IQ4_BF16)
+    return set_error(IQ4_E_ARG, "%s: scale_dtype must be IQ4_F16 or IQ4_BF16", fn);
+  if (!is_type(x_dtype) || !is_type(y_dtype))
+    return set_error(IQ4_E_ARG, "%s: x_dtype and y_dtype must be IQ4_F32, IQ4_F16 or IQ4_BF16", fn);
+  if (m < 0) return set_error(IQ4_E_ARG, "%s: the number of rows must be >= 0", fn);
+  if (m > ((int64_t)1 << 21)) return set_error(IQ4_E_UNSUPPORTED, "%s: at most 2^21 rows", fn);
+  return IQ4_OK;
+}
+
+static int check_g4_buffers(const char* fn, const void* packed, int64_t n, int64_t k, const void* x, int32_t x_dtype,
+                            int64_t ldx, const void* y, int32_t y_dtype, int64_t ldy) {
+  if (ldx < k || ldy < n) return set_error(IQ4_E_ARG, "%s: ldx must be >= k and ldy >= n", fn);
+  if (!packed || !x || !y) return set_error(IQ4_E_ARG, "%s: null pointer", fn);
+  if (!aligned(packed, 256) || !elem_aligned(x, x_dtype) || !elem_aligned(y, y_dtype))
+    return set_error(IQ4_E_ALIGN, "%s: packed must be 256-byte, x and y element aligned", fn);
+  return IQ4_OK;
+}
+
+int iq4_g4_qmv(const void* packed, int64_t n, int64_t k, int32_t group, int32_t scale_dtype, int32_t zeros,
+               const void* x, int32_t x_dtype, int64_t ldx, int64_t m, void* y, int32_t y_dtype, int64_t ldy,
+               void* stream) {
+  const char* fn = "iq4_g4_qmv";
+  clear_error();
+  if (int e = check_g4_args(fn, n, k, group, scale_dtype, x_dtype, y_dtype, m)) return e;
+  if (m == 0) return IQ4_OK;
+  if (int e = check_g4_buffers(fn, packed, n, k, x, x_dtype, ldx, y, y_dtype, ldy)) return e;
+  G4Args a{};
+  a.W = static_cast<const uint8_t*>(packed);
+  a.n = n;
+  a.k = k;
+  a.group = group;
+  a.scale_type = scale_dtype;
+  a.zeros = zeros != 0;
+  a.x = x;
+  a.ldx = ldx;
+  a.n_rows = a.m = m;
+  a.y = y;
+  a.y_type = y_dtype;
+  a.ldy = ldy;
+  return launch_g4_qmv(a, x_dtype, as_stream(stream));
+}
+
+int iq4_g4_grouped_qmv(const void* packed, int32_t n_expert, int64_t n, int64_t k, int32_t group, int32_t scale_dtype,
+                       int32_t zeros, const void* x, int32_t x_dtype, int64_t ldx, int64_t n_rows,
+                       const int32_t* offsets, const int32_t* pairs, int32_t top_k, int64_t n_pairs, void* y,
+                       int32_t y_dtype, int64_t ldy, void* stream) {
+  const char* fn = "iq4_g4_grouped_qmv";
+  clear_error();
+  if (int e = check_g4_args(fn, n, k, group, scale_dtype, x_dtype, y_dtype, n_pairs)) return e;
+  if (n_expert < 1 || n_expert > 1024) return set_error(IQ4_E_ARG, "%s: need 1 <= n_expert <= 1024", fn);
+  if (pairs && top_k < 1) return set_error(IQ4_E_ARG, "%s: top_k must be >= 1", fn);
+  if (n_rows < 0 || n_rows > (int64_t)1 << 30) return set_error(IQ4_E_ARG, "%s: n_rows must be 0 .. 2^30", fn);
+  if (n_pairs == 0) return IQ4_OK;
+  if (pairs ? n_rows * (int64_t)top_k < n_pairs : n_rows < n_pairs)
+    return set_error(IQ4_E_ARG, "%s: n_rows (times top_k, with pairs) must be >= n_pairs", fn);
+  if (!offsets) return set_error(IQ4_E_ARG, "%s: null pointer", fn);
+  if (!aligned(offsets, 4) || !aligned(pairs, 4))
+    return set_error(IQ4_E_ALIGN, "%s: offsets and pairs must be 4-byte aligned", fn);
+  if (int e = check_g4_buffers(fn, packed, n, k, x, x_dtype, ldx, y, y_dtype, ldy)) return e;
+  G4Args a{};
+  a.W = static_cast<const uint8_t*>(packed);
+  a.zeros = zeros != 0;
+  a.w_stride = g4_packed_bytes(n, k, group, a.zeros);
+  a.n = n;
+  a.k = k;
+  a.group = group;
+  a.scale_type = scale_dtype;
+  a.x = x;
+  a.ldx = ldx;
+  a.n_rows = n_rows;
+  a.m = n_pairs;
+  a.y = y;
+  a.y_type = y_dtype;
+  a.ldy = ldy;
+  a.offsets = offsets;
+  a.n_expert = n_expert;
+  a.pairs = pairs;
+  a.top_k = top_k;
+  return launch_g4_qmv(a, x_dtype, as_stream(stream));
+}
+
+// ---- tokens' rows into the experts' order and back ------------------------------------
+
+static int check_slots(const char* fn, int64_t n_tok, int32_t top_k, int64_t n_rows, int64_t hidden, int32_t t1,
+                       int32_t t2) {
+  if (n_tok < 0 || n_rows < 0 || hidden <= 0)
+    return set_error(IQ4_E_ARG, "%s: n_tok and n_rows must be >= 0 and hidden positive", fn);
+  if (top_k < 1 || top_k > 16) return set_error(IQ4_E_ARG, "%s: need 1 <= top_k <= 16 (top_k=%d)", fn, top_k);
+  if (!is_type(t1) || !is_type(t2)) return set_error(IQ4_E_ARG, "%s: dtypes must be IQ4_F32, IQ4_F16 or IQ4_BF16", fn);
+  if (n_tok > ((int64_t)1 << 24) / top_k || n_rows > ((int64_t)1 << 24) || hidden > ((int64_t)1 << 20))
+    return set_error(IQ4_E_UNSUPPORTED, "%s: n_tok * top_k <= 2^24, n_rows <= 2^24, hidden <= 2^20", fn);
+  return IQ4_OK;
+}
+
+// A buffer of rows at any element's address.
+static int check_any(const char* fn, const char* what, const void* p, int32_t type, int64_t k, int64_t ld) {
+  if (ld < k) return set_error(IQ4_E_ARG, "%s: the row stride of %s must hold a row", fn, what);
+  if (!p) return set_error(IQ4_E_ARG, "%s: null pointer (%s)", fn, what);
+  if (!elem_aligned(p, type)) return set_error(IQ4_E_ALIGN, "%s: %s must be element aligned", fn, what);
+  return IQ4_OK;
+}
+
+static int check_slot_lists(const char* fn, const int32_t* slot_row, const float* w, const float* dw) {
+  if (!slot_row) return set_error(IQ4_E_ARG, "%s: null pointer (slot_row)", fn);
+  if (!aligned(slot_row, 4) || !aligned(w, 4) || !aligned(dw, 4))
+    return set_error(IQ4_E_ALIGN, "%s: slot_row and weights must be 4-byte aligned", fn);
+  return IQ4_OK;
+}
+
+int iq4_moe_dispatch(const void* x, int32_t x_dtype, int64_t ldx, int64_t n_tok, int64_t hidden,
+                     const int32_t* slot_row, const float* w, int32_t top_k, int64_t n_rows, void* rows,
+                     int32_t rows_dtype, int64_t ldr, void* stream) {
+  const char* fn = "iq4_moe_dispatch";
+  clear_error();
+  if (int e = check_slots(fn, n_tok, top_k, n_rows, hidden, x_dtype, rows_dtype)) return e;
+  if (n_tok == 0 || n_rows == 0) return IQ4_OK;
+  if (int e = check_any(fn, "x", x, x_dtype, hidden, ldx)) return e;
+  if (int e = check_any(fn, "rows", rows, rows_dtype, hidden, ldr)) return e;
+  if (int e = check_slot_lists(fn, slot_row, w, nullptr)) return e;
+  SlotArgs a{};
+  a.slot_row = slot_row;
+  a.w = w;
+  a.n_tok = n_tok;
+  a.n_rows = n_rows;
+  a.hidden = hidden;
+  a.top_k = top_k;
+  a.tok = x;
+  a.ldt = ldx;
+  a.out = rows;
+  a.ldo = ldr;
+  return launch_dispatch(a, x_dtype, rows_dtype, as_stream(stream));
+}
+
+int iq4_moe_combine(const void* rows, int32_t rows_dtype, int64_t ldr, int64_t n_rows, const int32_t* slot_row,
+                    const float* w, int64_t n_tok, int32_t top_k, int64_t hidden, const void* add, int64_t lda,
+                    void* out, int32_t out_dtype, int64_t ldo, void* stream) {
+  const char* fn = "iq4_moe_combine";
+  clear_error();
+  if (int e = check_slots(fn, n_tok, top_k, n_rows, hidden, rows_dtype, out_dtype)) return e;
+  if (n_tok == 0) return IQ4_OK;
+  if (n_rows > 0)
+    if (int e = check_any(fn, "rows", rows, rows_dtype, hidden, ldr)) return e;
+  if (int e = check_any(fn, "out", out, out_dtype, hidden, ldo)) return e;
+  if (add) {
+    if (int e = check_any(fn, "add", add, out_dtype, hidden, lda)) return e;
+    // the sum may be stored over the addend, row for row
+    if (add == out && lda != ldo) return set_error(IQ4_E_ARG, "%s: out stored over add needs the same row stride", fn);
+  }
+  if (int e = check_slot_lists(fn, slot_row, w, nullptr)) return e;
+  SlotArgs a{};
+  a.slot_row = slot_row;
+  a.w = w;
+  a.n_tok = n_tok;
+  a.n_rows = n_rows;
+  a.hidden = hidden;
+  a.top_k = top_k;
+  a.tok = add;
+  a.ldt = lda;
+  a.rows = rows;
+  a.ldr = ldr;
+  a.out = out;
+  a.ldo = ldo;
+  return launch_combine_rows(a, rows_dtype, out_dtype, as_stream(stream));
+}
+
+int iq4_moe_combine_grad(const void* dout, int32_t dout_dtype, int64_t ldd, const void* rows, int32_t rows_dtype,
+                         int64_t ldr, int64_t n_rows, const int32_t* slot_row, const float* w, int64_t n_tok,
+                         int32_t top_k, int64_t hidden, void* drows, int64_t ldg, float* dw, void* stream) {
+  const char* fn = "iq4_moe_combine_grad";
+  clear_error();
+  if (int e = check_slots(fn, n_tok, top_k, n_rows, hidden, dout_dtype, rows_dtype)) return e;
+  if (n_tok == 0) return IQ4_OK;
+  if (!drows && !dw) return set_error(IQ4_E_ARG, "%s: null pointer (both drows and dw)", fn);
+  if (int e = check_any(fn, "dout", dout, dout_dtype, hidden, ldd)) return e;
+  if (n_rows > 0 && dw)
+    if (int e = check_any(fn, "rows", rows, rows_dtype, hidden, ldr)) return e;
+  if (n_rows > 0 && drows)
+    if (int e = check_any(fn, "drows", drows, rows_dtype, hidden, ldg)) return e;
+  if (int e = check_slot_lists(fn, slot_row, w, dw)) return e;
+  SlotArgs a{};
+  a.slot_row = slot_row;
+  a.w = w;
+  a.n_tok = n_tok;
+  a.n_rows = n_rows;
+  a.hidden = hidden;
+  a.top_k = top_k;
+  a.tok = dout;
+  a.ldt = ldd;
+  a.rows = rows;
+  a.ldr = ldr;
+  a.out = drows;
+  a.ldo = ldg;
+  a.dw = dw;
+  return launch_combine_grad(a, dout_dtype, rows_dtype, as_stream(stream));
+}
+
+// ---- SwiGLU -----------------------------------------------------------------------------
+
+static int check_swiglu(const char* fn, int32_t t1, int32_t t2, int64_t m, int64_t k) {
+  if (!is_type(t1) || !is_type(t2)) return set_error(IQ4_E_ARG, "%s: dtypes must be IQ4_F32, IQ4_F16 or IQ4_BF16", fn);
+  if (m < 0 || k <= 0) return set_error(IQ4_E_ARG, "%s: m must be >= 0 and k positive", fn);
+  if (k > ((int64_t)1 << 20) || m > ((int64_t)1 << 21) || m * k > ((int64_t)1 << 34))
+    return set_error(IQ4_E_UNSUPPORTED, "%s: k <= 2^20, m <= 2^21, m * k <= 2^34 (m=%lld k=%lld)", fn, (long long)m,
+                     (long long)k);
+  return IQ4_OK;
+}
+
+int iq4_swiglu(const void* g, int64_t ldg, const void* u, int64_t ldu, int32_t dtype, int64_t m, int64_t k, void* y,
+               int32_t y_dtype, int64_t ldy, int32_t fmt, void* codes, int64_t ldq, void* scales, int64_t lds,
+               void* stream) {
+  const char* fn = "iq4_swiglu";
+  clear_error();
+  if (int e = check_swiglu(fn, dtype, y ? y_dtype : dtype, m, k)) return e;
+  if (codes)
+    if (int e = check_rows_format(fn, fmt, m, k)) return e;
+  if (m == 0) return IQ4_OK;
+  if (!y && !codes) return set_error(IQ4_E_ARG, "%s: null pointer (both y and codes)", fn);
+  if (int e = check_any(fn, "g", g, dtype, k, ldg)) return e;
+  if (int e = check_any(fn, "u", u, dtype, k, ldu)) return e;
+  if (y)
+    if (int e = check_any(fn, "y", y, y_dtype, k, ldy)) return e;
+  if (codes)
+    if (int e = check_rows(fn, fmt, k, codes, ldq, scales, lds)) return e;
+  SwigluArgs a{};
+  a.g = g;
+  a.u = u;
+  a.ldg = ldg;
+  a.ldu = ldu;
+  a.m = m;
+  a.k = k;
+  a.y = y;
+  a.y_type = y_dtype;
+  a.ldy = ldy;
+  a.fmt = codes ? fmt : -1;
+  a.o = RowsOut{static_cast<uint8_t*>(codes), ldq, static_cast<uint8_t*>(scales), lds};
+  return launch_swiglu(a, dtype, as_stream(stream));
+}
+
+int iq4_swiglu_grad(const void* dh, int32_t dh_dtype, int64_t lddh, const void* g, int64_t ldg, const void* u,
+                    int64_t ldu, int32_t dtype, int64_t m, int64_t k, void* dg, int64_t lddg, void* du, int64_t lddu,
+                    void* stream) {
+  const char* fn = "iq4_swiglu_grad";
+  clear_error();
+  if (int e = check_swiglu(fn, dh_dtype, dtype, m, k)) return e;
+  if (m == 0) return IQ4_OK;
+  if (int e = check_any(fn, "dh", dh, dh_dtype, k, lddh)) return e;
+  if (int e = check_any(fn, "g", g, dtype, k, ldg)) return e;
+  if (int e = check_any(fn, "u", u, dtype, k, ldu)) return e;
+  if (int e = check_any(fn, "dg", dg, dtype, k, lddg)) return e;
+  if (int e = check_any(fn, "du", du, dtype, k, lddu)) return e;
+  SwigluGradArgs a{};
+  a.dh = dh;
+  a.g = g;
+  a.u = u;
+  a.lddh = lddh;
+  a.ldg = ldg;
+  a.ldu = ldu;
+  a.m = m;
+  a.k = k;
+  a.dg = dg;
+  a.du = du;
+  a.lddg = lddg;
+  a.lddu = lddu;
+  return launch_swiglu_grad(a, dh_dtype, dtype, as_stream(stream));
 }
 
 }  // extern "C"

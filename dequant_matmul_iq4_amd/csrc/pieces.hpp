@@ -1,0 +1,122 @@
+// pieces.hpp -- rows of floats of any length and element alignment, read and written in
+// pieces of P consecutive elements a lane.  A whole piece is one wide access (the device
+// takes them at any element's address); the last piece of a row that is no multiple of P
+// goes element by element.
+#pragma once
+#include "common.hpp"
+#include "rows.hpp"
+
+namespace iq4 {
+
+inline int type_bytes(int t) { return t == kF32 ? 4 : 2; }
+
+#ifdef __HIPCC__
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+
+// (Not templates over the vector: a type passed as a template argument loses its alignment.)
+template <bool STREAM>
+__device__ __forceinline__ u32x4 get16(const void* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(static_cast<const u32x4_any*>(p));
+  return *static_cast<const u32x4_any*>(p);
+}
+template <bool STREAM>
+__device__ __forceinline__ u32x2 get8(const void* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(static_cast<const u32x2_any*>(p));
+  return *static_cast<const u32x2_any*>(p);
+}
+template <bool STREAM>
+__device__ __forceinline__ void put16(void* p, u32x4 v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<u32x4_any*>(p));
+  else *static_cast<u32x4_any*>(p) = v;
+}
+template <bool STREAM>
+__device__ __forceinline__ void put8(void* p, u32x2 v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<u32x2_any*>(p));
+  else *static_cast<u32x2_any*>(p) = v;
+}
+
+// Elements at .. at + P - 1 of a row, `left` of which exist (the others are zero), as binary32.
+template <int TYPE, int P, bool STREAM = false>
+__device__ __forceinline__ void load_piece(const void* row, int64_t at, int left, float (&v)[P]) {
+  if constexpr (TYPE == kF32) {
+    const float* p = static_cast<const float*>(row) + at;
+    if (left >= P) {
+#pragma unroll
+      for (int q = 0; q < P / 4; ++q) {
+        const u32x4 w = get16<STREAM>(p + 4 * q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * q + i] = __uint_as_float(w[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = i < left ? p[i] : 0.f;
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(row) + at;
+    uint32_t w[P / 2];
+    if (left >= P) {
+      if constexpr (P == 8) {
+        const u32x4 x = get16<STREAM>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = x[i];
+      } else {
+        const u32x2 x = get8<STREAM>(p);
+        w[0] = x[0], w[1] = x[1];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < P / 2; ++i) {
+        w[i] = 2 * i < left ? p[2 * i] : 0u;
+        if (2 * i + 1 < left) w[i] |= (uint32_t)p[2 * i + 1] << 16;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) {
+      if constexpr (TYPE == kF16) {
+        v[2 * i] = h2f((uint16_t)(w[i] & 0xFFFFu));
+        v[2 * i + 1] = h2f((uint16_t)(w[i] >> 16));
+      } else {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
+// The same elements rounded (once, to nearest even) to TYPE and written.
+template <int TYPE, int P, bool STREAM = false>
+__device__ __forceinline__ void store_piece(void* row, int64_t at, int left, const float (&v)[P]) {
+  if constexpr (TYPE == kF32) {
+    float* p = static_cast<float*>(row) + at;
+    if (left >= P) {
+#pragma unroll
+      for (int q = 0; q < P / 4; ++q) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[4 * q + i]);
+        put16<STREAM>(p + 4 * q, w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (i < left) p[i] = v[i];
+    }
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(row) + at;
+    uint32_t w[P / 2];
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) w[i] = pack2<TYPE>(v[2 * i], v[2 * i + 1]);
+    if (left >= P) {
+      if constexpr (P == 8) put16<STREAM>(p, u32x4{w[0], w[1], w[2], w[3]});
+      else put8<STREAM>(p, u32x2{w[0], w[1]});
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (i < left) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+}
+#endif  // __HIPCC__
+
+}  // namespace iq4

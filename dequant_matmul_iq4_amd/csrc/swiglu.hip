@@ -1,0 +1,119 @@
+// swiglu.hip -- h = silu(g) * u between an expert's (or a dense layer's) two products,
+// quantised for the second one in the same pass, and its gradient.  With
+// s = 1 / (1 + e^-g):
+//   h = g s u;   du = dh g s,   dg = dh u s (1 + g (1 - s)).
+#include "pieces.hpp"
+#include "swiglu.hpp"
+
+namespace iq4 {
+
+// 1 / (1 + e^-g) in binary32.  e^-g = 2^-(g log2 e) with the product's rounding error carried
+// along (its relative weight in the result grows with |g|); beyond +-88 the power leaves binary32.
+__device__ __forceinline__ float sigmoid(float g) {
+  const float x = fminf(fmaxf(-g, -88.f), 88.f);
+  const float hi = x * 1.44269502f;
+  const float lo = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -hi));
+  const float e = __builtin_amdgcn_exp2f(hi);
+  const float s = __builtin_amdgcn_rcpf(1.0f + fmaf(e, lo * 0.693147182f, e));
+  return g < -88.f ? 0.f : s;
+}
+
+template <int T>
+__global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a, uint32_t octs) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  const uint32_t r = i / octs;
+  const int oct = (int)(i - r * octs);
+  const bool live = r < a.m;
+  const int left = (int)min<int64_t>(a.k - 8 * (int64_t)oct, 8);
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (live && left > 0) {
+    float g[8], u[8];
+    load_piece<T, 8>(static_cast<const char*>(a.g) + r * a.ldg * (T == kF32 ? 4 : 2), 8 * (int64_t)oct, left, g);
+    load_piece<T, 8>(static_cast<const char*>(a.u) + r * a.ldu * (T == kF32 ? 4 : 2), 8 * (int64_t)oct, left, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (g[e] * sigmoid(g[e])) * u[e];
+    if (a.y) {
+      char* y = static_cast<char*>(a.y) + r * a.ldy * (a.y_type == kF32 ? 4 : 2);
+      if (a.y_type == kF32) store_piece<kF32, 8>(y, 8 * (int64_t)oct, left, v);
+      else if (a.y_type == kF16) store_piece<kF16, 8>(y, 8 * (int64_t)oct, left, v);
+      else store_piece<kBF16, 8>(y, 8 * (int64_t)oct, left, v);
+    }
+  }
+  if (a.fmt < 0) return;
+  store_rows8(a.o, a.fmt, r, oct, v, live);
+  if (live && a.fmt != kRowsQ8_1 && oct == (int)octs - 1)
+    for (int b = octs / 4; b < (int)((a.k + 511) / 512 * 16); ++b) a.o.scales[r * a.o.lds + b] = 0;
+}
+
+// Rows go in as many launches as keep each below 2^32 threads.
+int launch_swiglu(const SwigluArgs& a0, int type, hipStream_t s) {
+  SwigluArgs a = a0;
+  const bool mx = a.fmt == kRowsMxfp4 || a.fmt == kRowsMxfp8;
+  const uint32_t octs = (uint32_t)((mx ? (a.k + 127) / 128 * 128 : a.k + 7) / 8);
+  const int64_t most = ((int64_t)1 << 31) / octs;
+  for (int64_t left = a0.m; left > 0; left -= a.m) {
+    a.m = left < most ? left : most;
+    const dim3 grid((unsigned)((a.m * octs + 255) / 256));
+    if (type == kF32) hipLaunchKernelGGL(swiglu_kernel<kF32>, grid, dim3(256), 0, s, a, octs);
+    else if (type == kF16) hipLaunchKernelGGL(swiglu_kernel<kF16>, grid, dim3(256), 0, s, a, octs);
+    else hipLaunchKernelGGL(swiglu_kernel<kBF16>, grid, dim3(256), 0, s, a, octs);
+    if (int e = check_launch("swiglu_kernel")) return e;
+    a.g = static_cast<const char*>(a.g) + a.m * a.ldg * type_bytes(type);
+    a.u = static_cast<const char*>(a.u) + a.m * a.ldu * type_bytes(type);
+    if (a.y) a.y = static_cast<char*>(a.y) + a.m * a.ldy * type_bytes(a.y_type);
+    if (a.fmt >= 0) a.o.codes += a.m * a.o.ldq, a.o.scales += a.m * a.o.lds;
+  }
+  return 0;
+}
+
+template <int TD, int T>
+__global__ void __launch_bounds__(256) swiglu_grad_kernel(SwigluGradArgs a, uint32_t pieces) {
+  constexpr int P = (TD == kF32 || T == kF32) ? 4 : 8, kSize = T == kF32 ? 4 : 2;
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  const uint32_t r = i / pieces;
+  if (r >= a.m) return;
+  const int64_t at = (int64_t)(i - r * pieces) * P;
+  const int left = (int)min<int64_t>(a.k - at, P);
+  float d[P], g[P], u[P], x[P], z[P];
+  load_piece<TD, P>(static_cast<const char*>(a.dh) + r * a.lddh * (TD == kF32 ? 4 : 2), at, left, d);
+  load_piece<T, P>(static_cast<const char*>(a.g) + r * a.ldg * kSize, at, left, g);
+  load_piece<T, P>(static_cast<const char*>(a.u) + r * a.ldu * kSize, at, left, u);
+#pragma unroll
+  for (int e = 0; e < P; ++e) {
+    const float s = sigmoid(g[e]);
+    z[e] = d[e] * (g[e] * s);
+    x[e] = (d[e] * u[e]) * (s * fmaf(g[e], 1.0f - s, 1.0f));
+  }
+  store_piece<T, P>(static_cast<char*>(a.dg) + r * a.lddg * kSize, at, left, x);
+  store_piece<T, P>(static_cast<char*>(a.du) + r * a.lddu * kSize, at, left, z);
+}
+
+int launch_swiglu_grad(const SwigluGradArgs& a0, int dh_type, int type, hipStream_t s) {
+  SwigluGradArgs a = a0;
+  const int p = (dh_type == kF32 || type == kF32) ? 4 : 8;
+  const uint32_t pieces = (uint32_t)((a.k + p - 1) / p);
+  const int64_t most = ((int64_t)1 << 31) / pieces;
+  for (int64_t left = a0.m; left > 0; left -= a.m) {
+    a.m = left < most ? left : most;
+    const dim3 grid((unsigned)((a.m * pieces + 255) / 256));
+#define IQ4_GRAD(TD)                                                                                              \
+  {                                                                                                               \
+    if (type == kF32) hipLaunchKernelGGL((swiglu_grad_kernel<TD, kF32>), grid, dim3(256), 0, s, a, pieces);       \
+    else if (type == kF16) hipLaunchKernelGGL((swiglu_grad_kernel<TD, kF16>), grid, dim3(256), 0, s, a, pieces);  \
+    else hipLaunchKernelGGL((swiglu_grad_kernel<TD, kBF16>), grid, dim3(256), 0, s, a, pieces);                   \
+  }
+    if (dh_type == kF32) IQ4_GRAD(kF32)
+    else if (dh_type == kF16) IQ4_GRAD(kF16)
+    else IQ4_GRAD(kBF16)
+#undef IQ4_GRAD
+    if (int e = check_launch("swiglu_grad_kernel")) return e;
+    a.dh = static_cast<const char*>(a.dh) + a.m * a.lddh * type_bytes(dh_type);
+    a.g = static_cast<const char*>(a.g) + a.m * a.ldg * type_bytes(type);
+    a.u = static_cast<const char*>(a.u) + a.m * a.ldu * type_bytes(type);
+    a.dg = static_cast<char*>(a.dg) + a.m * a.lddg * type_bytes(type);
+    a.du = static_cast<char*>(a.du) + a.m * a.lddu * type_bytes(type);
+  }
+  return 0;
+}
+
+}  // namespace iq4

@@ -525,6 +525,129 @@ int iq4_mx_grouped_gemm(const void* packed, int32_t n_expert, int64_t n, int64_t
                         const int32_t* pairs, int32_t top_k, int64_t n_pairs, void* y, int32_t y_dtype, int64_t ldy,
                         void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * 4-bit weights with group scales: `group` consecutive weights of a row (32, 64 or 128) share
+ * a scale s and a whole zero point z, and a weight is w = s * (q - z), q one of 0 .. 15.
+ * Without zero points z is 8 everywhere.
+ */
+
+/* Size in bytes of the packed form of an n x k matrix (a multiple of 256), with zero points if
+ * zeros != 0; or -1 (n < 1, k < 1, k % 32, another group, n > 2^24, k > 2^20). */
+int64_t iq4_g4_packed_bytes(int64_t n, int64_t k, int32_t group, int32_t zeros);
+
+/*
+ * Rearrange an n x k matrix for the products below (one-time, at weight-load time).
+ *   codes   [n][ldq] bytes, ldq >= k / 2: two codes a byte, low nibble first.
+ *   scales  [n][lds] 16-bit floats (binary16 or bfloat16: the products are told which), finite,
+ *           lds >= the groups of a row, ceil(k / group) (the last may be short).
+ *   zeros   [n][ldz] bytes, a zero point (0 .. 15; the low four bits count) each, or NULL.
+ *           All three may have any alignment.
+ *   packed  iq4_g4_packed_bytes(n, k, group, zeros != NULL) bytes, 256-byte aligned, overlapping
+ *           none of them.
+ * Packed layout, KT = ceil(k / 128), KQ = ceil(k / 512), P = 512 / group: code tile (rt, kt) at
+ * (rt * KT + kt) * 1024 bytes, 64 entries of 16 bytes; word b of entry 16g + j = elements
+ * 8g .. 8g + 7 of block 4kt + b (of 32) of row 16rt + j, elements 0, 2, 4, 6, 1, 3, 5, 7 from the
+ * lowest nibble up.  After all code tiles the scales, row j's P of a tile (rt, kq) at
+ * ((rt * KQ + kq) * 16 + j) * P * 2 bytes; then the zero points in the same order, a byte each.
+ * Zero past n and k.
+ * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED.
+ */
+int iq4_g4_pack_weights(const void* codes, int64_t ldq, const void* scales, int64_t lds, const void* zeros,
+                        int64_t ldz, int64_t n, int64_t k, int32_t group, void* packed, void* stream);
+
+/*
+ * Product of few rows (a decode step's, a verify window's, a batch's) with such a matrix:
+ *   Y[i][r] = sum over the groups G of row r of s[r][G] * sum_{k in G} (q[r][k] - z[r][G]) X[i][k],
+ * i < m, r < n; the products exact, the sums in binary32, rounded once to y_dtype.
+ *   packed  iq4_g4_pack_weights, 256-byte aligned.   scale_dtype: IQ4_F16 or IQ4_BF16.
+ *   zeros   != 0 if packed with zero points.
+ *   x       [m][ldx], y [m][ldy] of their dtypes (IQ4_F32, IQ4_F16, IQ4_BF16), element aligned,
+ *           ldx >= k, ldy >= n; columns n .. ldy - 1 of y are left alone.
+ *   m >= 0 (0: no-op); meant for up to some 64 rows, any number up to 2^21 is taken.  No workspace.
+ * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED (group, k % 32, sizes; a grid of 2^32 threads).
+ */
+int iq4_g4_qmv(const void* packed, int64_t n, int64_t k, int32_t group, int32_t scale_dtype, int32_t zeros,
+               const void* x, int32_t x_dtype, int64_t ldx, int64_t m, void* y, int32_t y_dtype, int64_t ldy,
+               void* stream);
+
+/*
+ * The same product with one matrix per expert, output rows sorted by expert: Y[i] = W_e X[row(i)],
+ * offsets[e] <= i < offsets[e + 1], row(i) = pairs[i] / top_k, or i if pairs is NULL (offsets and
+ * pairs as for iq4_mx_grouped_gemm: iq4_moe_gather writes them; values out of range are clamped).
+ *   packed  n_expert packed n x k matrices, expert e at e * iq4_g4_packed_bytes(n, k, group, zeros).
+ *   x       n_rows rows.   y  [n_pairs][ldy]; rows from offsets[n_expert] on are left as they were.
+ * Errors: as iq4_g4_qmv; IQ4_E_ARG too if x has too few rows for n_pairs.
+ */
+int iq4_g4_grouped_qmv(const void* packed, int32_t n_expert, int64_t n, int64_t k, int32_t group, int32_t scale_dtype,
+                       int32_t zeros, const void* x, int32_t x_dtype, int64_t ldx, int64_t n_rows,
+                       const int32_t* offsets, const int32_t* pairs, int32_t top_k, int64_t n_pairs, void* y,
+                       int32_t y_dtype, int64_t ldy, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Tokens' rows into the experts' order and back.  Pair p = t * top_k + j is token t's slot j;
+ * slot_row[p] (iq4_moe_gather writes it) is its row among the experts' rows, or a number outside
+ * [0, n_rows) for a pair that has none (an expert that was full, another device's expert): it
+ * adds nothing and its weight's gradient is zero.  Any hidden and row strides, element alignment.
+ * 1 <= top_k <= 16, n_tok * top_k <= 2^24, n_rows <= 2^24, hidden <= 2^20; n_tok = 0 is a no-op.
+ * Buffers must not overlap but where it is said.  Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED.
+ */
+
+/*
+ * R[slot_row[p]] = w[p] * X[t] (X[t] itself if w is NULL), the binary32 product rounded once to
+ * rows_dtype.  Rows that no pair has are left as they were; a row that two pairs have gets either's.
+ * This is also the gradient of iq4_moe_combine with respect to its rows.
+ *   x  [n_tok][ldx] of x_dtype.  rows  [n_rows][ldr] of rows_dtype.  w  [n_tok][top_k] float32 or NULL.
+ */
+int iq4_moe_dispatch(const void* x, int32_t x_dtype, int64_t ldx, int64_t n_tok, int64_t hidden,
+                     const int32_t* slot_row, const float* w, int32_t top_k, int64_t n_rows, void* rows,
+                     int32_t rows_dtype, int64_t ldr, void* stream);
+
+/*
+ * O[t] = sum_j w[p] * R[slot_row[p]] (+ A[t]), added in binary32 in the order of j, A last, rounded
+ * once to out_dtype; w NULL: 1.  A token without rows gets zero (or A).  Without w and A it is the
+ * gradient of iq4_moe_dispatch.  Deterministic.
+ *   rows  [n_rows][ldr] of rows_dtype (not read if n_rows = 0).   add  [n_tok][lda] of out_dtype, or NULL
+ *   (a residual stream, a shared expert's rows).   out  [n_tok][ldo]; may be add itself (same stride).
+ */
+int iq4_moe_combine(const void* rows, int32_t rows_dtype, int64_t ldr, int64_t n_rows, const int32_t* slot_row,
+                    const float* w, int64_t n_tok, int32_t top_k, int64_t hidden, const void* add, int64_t lda,
+                    void* out, int32_t out_dtype, int64_t ldo, void* stream);
+
+/*
+ * Gradient of iq4_moe_combine, its rows' and its weights' in one pass:
+ *   dR[slot_row[p]] = w[p] * dO[t],   dw[p] = sum_h dO[t][h] * R[slot_row[p]][h]  (binary32)
+ * (A's is dO itself).  Deterministic; rows and weights of pairs as iq4_moe_dispatch has them.
+ *   dout  [n_tok][ldd] of dout_dtype.   rows  [n_rows][ldr] of rows_dtype (read only for dw).
+ *   drows [n_rows][ldg] of rows_dtype, or NULL.   dw  [n_tok][top_k] float32, or NULL (not both).
+ */
+int iq4_moe_combine_grad(const void* dout, int32_t dout_dtype, int64_t ldd, const void* rows, int32_t rows_dtype,
+                         int64_t ldr, int64_t n_rows, const int32_t* slot_row, const float* w, int64_t n_tok,
+                         int32_t top_k, int64_t hidden, void* drows, int64_t ldg, float* dw, void* stream);
+
+/*
+ * SwiGLU between a layer's two products, h = g / (1 + e^-g) * u in binary32, and the quantisation of
+ * its rows for the second product in the same pass.
+ *   g, u    [m][ldg], [m][ldu] of dtype (side by side in one buffer, or apart), element aligned.
+ *   y       [m][ldy] of y_dtype, h rounded once, element aligned; or NULL.
+ *   codes, scales  h (the float32 values) quantised as by iq4_quantize_rows, or codes NULL (fmt, ldq,
+ *           scales, lds are then ignored); k % 32 == 0 with codes.  y or codes must be given.
+ *   m >= 0 (0: no-op), m <= 2^21, k <= 2^20, m * k <= 2^34.  No output may overlap another buffer.
+ * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED.
+ */
+int iq4_swiglu(const void* g, int64_t ldg, const void* u, int64_t ldu, int32_t dtype, int64_t m, int64_t k, void* y,
+               int32_t y_dtype, int64_t ldy, int32_t fmt, void* codes, int64_t ldq, void* scales, int64_t lds,
+               void* stream);
+
+/*
+ * Gradient of iq4_swiglu, with s = 1 / (1 + e^-g):
+ *   du = dh * g * s,   dg = dh * u * s * (1 + g * (1 - s)),  in binary32, rounded once to dtype.
+ *   dh  [m][lddh] of dh_dtype; g, u, dg, du  [m][..] of dtype, any strides, element aligned.
+ * Limits and errors as iq4_swiglu.
+ */
+int iq4_swiglu_grad(const void* dh, int32_t dh_dtype, int64_t lddh, const void* g, int64_t ldg, const void* u,
+                    int64_t ldu, int32_t dtype, int64_t m, int64_t k, void* dg, int64_t lddg, void* du, int64_t lddu,
+                    void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -66,3 +66,14 @@ def packed(codes: np.ndarray, scales: np.ndarray, n: int, k: int) -> torch.Tenso
 
 def value(fmt: str, codes, scales) -> np.ndarray:
     return oracle.dequant_rows(codes, scales, fmt)
+
+
+def same_rows(fmt, k, q, d, want):
+    """Device rows hold exactly the oracle's codes and scales (a NaN scale is any NaN)."""
+    codes, scales = split_rows(fmt, k, q, d)
+    assert np.array_equal(codes, want[0])
+    if fmt == "q8_1":
+        assert np.array_equal(np.isnan(scales), np.isnan(want[1]))
+        assert np.nan_to_num(scales, nan=0).tobytes() == np.nan_to_num(want[1], nan=0).tobytes()
+    else:
+        assert np.array_equal(scales, want[1])
