@@ -1,9 +1,6 @@
-// g4.hip -- products of few rows with 4-bit weights that have a scale and a zero point per
-// group of 32, 64 or 128 weights: Y[i][r] = sum over groups G of row r of
-//   s[r][G] * sum_{k in G} (q[r][k] - z[r][G]) X[i][k],
-// for one matrix or for one matrix per expert with the rows sorted by expert.
+// g4.hip -- 4-bit weights that have a scale and a zero point per group of 32, 64 or 128: the
+// packed layout, and which kernel (g4_kernel.hpp) multiplies.
 #include "g4.hpp"
-#include "pieces.hpp"
 
 namespace iq4 {
 
@@ -57,66 +54,9 @@ int launch_g4_pack(const G4Pack& a, hipStream_t s) {
   return check_launch("g4_pack_kernel");
 }
 
-// ---- product ------------------------------------------------------------------------------
-
-template <int TYPE>
-__device__ __forceinline__ float element(const void* p, int64_t at) {
-  if constexpr (TYPE == kF32) return static_cast<const float*>(p)[at];
-  const uint16_t h = static_cast<const uint16_t*>(p)[at];
-  if constexpr (TYPE == kF16) return h2f(h);
-  return __uint_as_float((uint32_t)h << 16);
-}
-
-// One lane per output.
-template <int TX>
-__global__ void __launch_bounds__(256) g4_simple_kernel(G4Args a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = i / a.n;
-  const int64_t r = i - row * a.n;
-  if (row >= a.m) return;
-  const uint8_t* W = a.W;
-  int64_t xr = row;
-  if (a.offsets) {
-    int e = 0;
-    while (e < a.n_expert && !(a.offsets[e] <= row && row < a.offsets[e + 1])) ++e;
-    if (e == a.n_expert) return;
-    W += e * a.w_stride;
-    if (a.pairs) xr = a.pairs[row] / a.top_k;
-    xr = min(max(xr, (int64_t)0), a.n_rows - 1);
-  }
-  const int64_t rt = r >> 4;
-  const int c = (int)(r & 15), per = 512 / a.group;
-  const uint8_t* codes = W + rt * g4_k_tiles(a.k) * kG4TileBytes;
-  const uint16_t* ss = reinterpret_cast<const uint16_t*>(W + g4_code_plane(a.n, a.k));
-  const uint8_t* zs = W + g4_code_plane(a.n, a.k) + g4_scale_plane(a.n, a.k, a.group);
-  const char* x = static_cast<const char*>(a.x) + xr * a.ldx * (TX == kF32 ? 4 : 2);
-  float acc = 0.f;
-  for (int64_t k0 = 0; k0 < a.k; k0 += a.group) {
-    const int64_t at = ((rt * g4_k_quads(a.k) + k0 / 512) * 16 + c) * per + k0 % 512 / a.group;
-    const uint16_t sb = ss[at];
-    const float s = a.scale_type == kF16 ? h2f(sb) : __uint_as_float((uint32_t)sb << 16);
-    const int z = a.zeros ? zs[at] : 8;
-    float d = 0.f;
-    for (int64_t k = k0; k < min(k0 + a.group, a.k); ++k) {
-      const int b = (int)(k >> 5 & 3), g = (int)(k >> 3 & 3), e = (int)(k & 7);
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + (k >> 7) * kG4TileBytes + (16 * g + c) * 16 + 4 * b);
-      const int q = (int)(w >> (16 * (e & 1) + 4 * (e >> 1)) & 15u);
-      d = fmaf((float)(q - z), element<TX>(x, k), d);
-    }
-    acc = fmaf(s, d, acc);
-  }
-  if (a.y_type == kF32) static_cast<float*>(a.y)[row * a.ldy + r] = acc;
-  else static_cast<uint16_t*>(a.y)[row * a.ldy + r] = (uint16_t)(a.y_type == kF16 ? pack2<kF16>(acc, 0.f) : pack2<kBF16>(acc, 0.f));
-}
-
 int launch_g4_qmv(const G4Args& a, int x_type, hipStream_t s) {
-  const int64_t groups = (a.m * a.n + 255) / 256;
-  if (groups * 256 >= (int64_t)1 << 32) return set_error(-3, "iq4_g4 product: too many workgroups (n * m too large)");
-  const dim3 grid((unsigned)groups);
-  if (x_type == kF32) hipLaunchKernelGGL(g4_simple_kernel<kF32>, grid, dim3(256), 0, s, a);
-  else if (x_type == kF16) hipLaunchKernelGGL(g4_simple_kernel<kF16>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(g4_simple_kernel<kBF16>, grid, dim3(256), 0, s, a);
-  return check_launch("g4_simple_kernel");
+  if (x_type == kF32) return launch_g4_f32(a, s);
+  return x_type == kF16 ? launch_g4_f16(a, s) : launch_g4_bf16(a, s);
 }
 
 }  // namespace iq4

@@ -60,5 +60,9 @@ struct G4Args {
   int top_k;
 };
 int launch_g4_qmv(const G4Args& a, int x_type, hipStream_t s);
+// by the type of x
+int launch_g4_f32(const G4Args& a, hipStream_t s);
+int launch_g4_f16(const G4Args& a, hipStream_t s);
+int launch_g4_bf16(const G4Args& a, hipStream_t s);
 
 }  // namespace iq4

@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "experts.hpp"
 #include "mx.hpp"
 #include "rows.hpp"
 
@@ -207,17 +208,6 @@ __device__ __forceinline__ bool expert_rows(const MxArgs& a, int e0, int (&o0)[4
   clamp(0), clamp(1);
   if (upper) clamp(2), clamp(3);
   return upper;
-}
-
-// Sums of a value over lanes 0 .. own (one wave, without LDS: row shifts and broadcasts).
-__device__ __forceinline__ int scan64(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);  // row_shr:2
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);  // row_shr:4
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);  // row_shr:8
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1, 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2, 3
-  return v;
 }
 
 // The tiles of `bm` rows that the experts' rows make, found by every wave on its own from the
