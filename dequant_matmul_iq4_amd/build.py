@@ -17,7 +17,7 @@ OUT = os.path.join(PKG, "libiq4.so")
 OBJ = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.hip", "format.hip", "qmv.hip", "route.hip", "gemm.hip", "moe.hip", "xs.hip", "rows.hip", "mx.hip",
-           "g4.hip", "g4_f32.hip", "g4_f16.hip", "g4_bf16.hip", "slots.hip", "swiglu.hip"]
+           "g4.hip", "g4_32.hip", "g4_64.hip", "g4_128.hip", "slots.hip", "swiglu.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

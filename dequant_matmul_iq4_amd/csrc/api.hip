@@ -650,7 +650,7 @@ int iq4_g4_pack_weights(const void* codes, int64_t ldq, const void* scales, int6
     return set_error(IQ4_E_ARG, "%s: ldq must be >= k / 2, lds and ldz >= the groups of a row", fn);
   if (!codes || !scales || !packed) return set_error(IQ4_E_ARG, "%s: null pointer", fn);
   if (!aligned(packed, 256)) return set_error(IQ4_E_ALIGN, "%s: packed must be 256-byte aligned", fn);
-  if (g4_row_tiles(n) * g4_k_quads(k) * 64 >= ((int64_t)1 << 32) - 256)
+  if (g4_row_tiles(n) * g4_k_tiles(k) * 64 >= ((int64_t)1 << 32) - 256)
     return set_error(IQ4_E_UNSUPPORTED, "%s: n * k too large", fn);
   const uint8_t* p = static_cast<const uint8_t*>(packed);
   const uint8_t* c = static_cast<const uint8_t*>(codes);
@@ -713,12 +713,13 @@ int iq4_g4_qmv(const void* packed, int64_t n, int64_t k, int32_t group, int32_t 
   a.scale_type = scale_dtype;
   a.zeros = zeros != 0;
   a.x = x;
+  a.x_type = x_dtype;
   a.ldx = ldx;
   a.n_rows = a.m = m;
   a.y = y;
   a.y_type = y_dtype;
   a.ldy = ldy;
-  return launch_g4_qmv(a, x_dtype, as_stream(stream));
+  return launch_g4_qmv(a, as_stream(stream));
 }
 
 int iq4_g4_grouped_qmv(const void* packed, int32_t n_expert, int64_t n, int64_t k, int32_t group, int32_t scale_dtype,
@@ -747,6 +748,7 @@ int iq4_g4_grouped_qmv(const void* packed, int32_t n_expert, int64_t n, int64_t 
   a.group = group;
   a.scale_type = scale_dtype;
   a.x = x;
+  a.x_type = x_dtype;
   a.ldx = ldx;
   a.n_rows = n_rows;
   a.m = n_pairs;
@@ -757,7 +759,7 @@ int iq4_g4_grouped_qmv(const void* packed, int32_t n_expert, int64_t n, int64_t 
   a.n_expert = n_expert;
   a.pairs = pairs;
   a.top_k = top_k;
-  return launch_g4_qmv(a, x_dtype, as_stream(stream));
+  return launch_g4_qmv(a, as_stream(stream));
 }
 
 // ---- tokens' rows into the experts' order and back ------------------------------------

@@ -5,58 +5,54 @@
 namespace iq4 {
 
 // ---- pack -------------------------------------------------------------------------------
-// A lane makes the 16 bytes of one row's 32 codes: word b of lane 16 g + c of code tile
-// (rt, kt) has elements 8g .. 8g+7 of block 4 kt + b of row 16 rt + c, elements 0, 2, 4, 6 in the
-// low half's nibbles and 1, 3, 5, 7 in the high half's.  Scales and zero points keep their order
-// inside a (row tile, quad).  What lies past n or k is zero.  Run once per matrix; the source
-// is read byte by byte, which spares it any alignment.
+// A wave makes a code tile: word b of lane 16 g + c has elements 8g .. 8g+7 of block b (of 32) of
+// row 16 rt + c, elements 0, 2, 4, 6 in the low half's nibbles and 1, 3, 5, 7 in the high half's.
+// Scales and zero points keep their order inside a tile's row.  What lies past n or k is zero.  Run
+// once per matrix; the source is read byte by byte, which spares it any alignment.
 __global__ void __launch_bounds__(256) g4_pack_kernel(G4Pack a) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int lane = (int)(i & 63), g = lane >> 4, c = lane & 15;
-  const int64_t quad = i >> 6;
-  const int kt_n = g4_k_tiles(a.k), kq_n = g4_k_quads(a.k);
-  const int64_t rt = quad / kq_n;
+  const int64_t tile = i >> 6;
+  const int kt_n = g4_k_tiles(a.k);
+  const int64_t rt = tile / kt_n;
   if (rt >= g4_row_tiles(a.n)) return;
-  const int kq = (int)(quad - rt * kq_n);
+  const int kt = (int)(tile - rt * kt_n);
   const int64_t row = rt * 16 + c;
-  for (int j = 0; j < 4; ++j) {
-    const int kt = 4 * kq + j;
-    if (kt >= kt_n) break;
-    uint32_t w[4];
-    for (int b = 0; b < 4; ++b) {
-      const int64_t at = (int64_t)kt * 128 + 32 * b + 8 * g;  // the first of eight elements
-      uint32_t v = 0;
-      if (row < a.n && at < a.k)
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t two = a.codes[row * a.ldq + at / 2 + e];
-          v |= (two & 15u) << (4 * e) | (two >> 4) << (16 + 4 * e);
-        }
-      w[b] = v;
-    }
-    *reinterpret_cast<u32x4*>(a.packed + (rt * kt_n + kt) * kG4TileBytes + lane * 16) = u32x4{w[0], w[1], w[2], w[3]};
+  uint32_t w[4];
+  for (int b = 0; b < 4; ++b) {
+    const int64_t at = (int64_t)kt * 128 + 32 * b + 8 * g;  // the first of eight elements
+    uint32_t v = 0;
+    if (row < a.n && at < a.k)
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t two = a.codes[row * a.ldq + at / 2 + e];
+        v |= (two & 15u) << (4 * e) | (two >> 4) << (16 + 4 * e);
+      }
+    w[b] = v;
   }
-  const int per = 512 / a.group;  // groups of a row in a quad
-  uint16_t* s = reinterpret_cast<uint16_t*>(a.packed + g4_code_plane(a.n, a.k) + quad * g4_scale_bytes(a.group));
-  uint8_t* z = a.packed + g4_code_plane(a.n, a.k) + g4_scale_plane(a.n, a.k, a.group) + quad * g4_zero_bytes(a.group);
-  const int64_t groups = (a.k + a.group - 1) / a.group;
-  for (int e = lane; e < 16 * per; e += 64) {
-    const int64_t r = rt * 16 + e / per, q = (int64_t)kq * per + e % per;
-    const bool in = r < a.n && q < groups;
-    const uint8_t* at = reinterpret_cast<const uint8_t*>(a.scales) + 2 * (r * a.lds + q);
-    s[e] = in ? (uint16_t)(at[0] | at[1] << 8) : (uint16_t)0;
-    if (a.zeros) z[e] = in ? a.zeros[r * a.ldz + q] & 15 : 0;
-  }
+  *reinterpret_cast<u32x4*>(a.packed + tile * kG4TileBytes + lane * 16) = u32x4{w[0], w[1], w[2], w[3]};
+  const int sets = 128 / a.group;  // groups of a row in a tile: lane 16 g + c does group g of row c
+  if (g >= sets) return;
+  uint16_t* s = reinterpret_cast<uint16_t*>(a.packed + g4_code_plane(a.n, a.k)) + tile * 16 * sets;
+  uint8_t* z = a.packed + g4_code_plane(a.n, a.k) + g4_scale_plane(a.n, a.k, a.group) + tile * 16 * sets;
+  const int64_t q = (int64_t)kt * sets + g;
+  const bool in = row < a.n && q * a.group < a.k;
+  const uint8_t* at = reinterpret_cast<const uint8_t*>(a.scales) + 2 * (row * a.lds + q);
+  s[c * sets + g] = in ? (uint16_t)(at[0] | at[1] << 8) : (uint16_t)0;
+  if (a.zeros) z[c * sets + g] = in ? a.zeros[row * a.ldz + q] & 15 : 0;
 }
 
 int launch_g4_pack(const G4Pack& a, hipStream_t s) {
-  const int64_t waves = g4_row_tiles(a.n) * g4_k_quads(a.k);
+  const int64_t waves = g4_row_tiles(a.n) * g4_k_tiles(a.k);
   hipLaunchKernelGGL(g4_pack_kernel, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, s, a);
   return check_launch("g4_pack_kernel");
 }
 
-int launch_g4_qmv(const G4Args& a, int x_type, hipStream_t s) {
-  if (x_type == kF32) return launch_g4_f32(a, s);
-  return x_type == kF16 ? launch_g4_f16(a, s) : launch_g4_bf16(a, s);
+int launch_g4_qmv(const G4Args& a, hipStream_t s) {
+  // one operand of 16 rows of X (8 of binary32) or two; by expert by the rows that one has on average
+  const int64_t rows = a.offsets ? (a.m + a.n_expert - 1) / a.n_expert : a.m;
+  const int nv = rows > (a.x_type == kF32 ? 8 : 16) ? 2 : 1;
+  if (a.group == 32) return launch_g4_32(a, nv, s);
+  return a.group == 64 ? launch_g4_64(a, nv, s) : launch_g4_128(a, nv, s);
 }
 
 }  // namespace iq4

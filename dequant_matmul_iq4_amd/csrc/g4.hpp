@@ -6,24 +6,20 @@
 
 namespace iq4 {
 
-// Packed layout: a row tile is 16 rows, a code tile a row tile x 128 along k (1 KB), a quad
-// four code tiles.  Codes first, then the scales by (row tile, quad), then the zero points.
+// Packed layout: a row tile is 16 rows, a code tile a row tile x 128 along k (1 KB).  Codes first,
+// then the scales by code tile, then the zero points by code tile.
 constexpr int kG4TileBytes = 1024;
 inline __host__ __device__ int64_t g4_row_tiles(int64_t n) { return (n + 15) / 16; }
 inline __host__ __device__ int g4_k_tiles(int64_t k) { return (int)((k + 127) / 128); }
-inline __host__ __device__ int g4_k_quads(int64_t k) { return (int)((k + 511) / 512); }
 inline __host__ __device__ int64_t g4_code_plane(int64_t n, int64_t k) {
   return g4_row_tiles(n) * g4_k_tiles(k) * kG4TileBytes;
 }
-// bytes of one (row tile, quad): 16 rows x (512 / group) scales of two bytes, zeros of one
-inline __host__ __device__ int g4_scale_bytes(int group) { return 16 * (512 / group) * 2; }
-inline __host__ __device__ int g4_zero_bytes(int group) { return 16 * (512 / group); }
+// a code tile has 16 rows x (128 / group) scales of two bytes, and as many zero points of one
 inline __host__ __device__ int64_t g4_scale_plane(int64_t n, int64_t k, int group) {
-  return g4_row_tiles(n) * g4_k_quads(k) * g4_scale_bytes(group);
+  return g4_row_tiles(n) * g4_k_tiles(k) * 16 * (128 / group) * 2;
 }
 inline __host__ __device__ int64_t g4_packed_bytes(int64_t n, int64_t k, int group, bool zeros) {
-  const int64_t b = g4_code_plane(n, k) + g4_scale_plane(n, k, group) +
-                    (zeros ? g4_row_tiles(n) * g4_k_quads(k) * g4_zero_bytes(group) : 0);
+  const int64_t b = g4_code_plane(n, k) + g4_scale_plane(n, k, group) + (zeros ? g4_scale_plane(n, k, group) / 2 : 0);
   return (b + 255) / 256 * 256;  // (a bank's next matrix begins aligned)
 }
 
@@ -46,8 +42,9 @@ struct G4Args {
   int64_t n, k;
   int group;         // 32, 64 or 128
   int scale_type;    // kF16 or kBF16
-  bool zeros;
+  int zeros;         // != 0: with zero points
   const void* x;
+  int x_type;
   int64_t ldx;
   int64_t n_rows;    // rows of x
   int64_t m;         // rows of y
@@ -59,10 +56,10 @@ struct G4Args {
   const int32_t* pairs;    // or null
   int top_k;
 };
-int launch_g4_qmv(const G4Args& a, int x_type, hipStream_t s);
-// by the type of x
-int launch_g4_f32(const G4Args& a, hipStream_t s);
-int launch_g4_f16(const G4Args& a, hipStream_t s);
-int launch_g4_bf16(const G4Args& a, hipStream_t s);
+int launch_g4_qmv(const G4Args& a, hipStream_t s);
+// by group; nv: operands of 16 rows of X (8 of binary32) that a workgroup multiplies at once, 1 or 2
+int launch_g4_32(const G4Args& a, int nv, hipStream_t s);
+int launch_g4_64(const G4Args& a, int nv, hipStream_t s);
+int launch_g4_128(const G4Args& a, int nv, hipStream_t s);
 
 }  // namespace iq4

@@ -1,0 +1,11 @@
+// g4_64.hip -- products with 4-bit weights that have a scale per 64 (g4_kernel.hpp).
+#include "g4_kernel.hpp"
+
+namespace iq4 {
+
+int launch_g4_64(const G4Args& a, int nv, hipStream_t s) {
+  if (a.x_type == kF32) return launch_g4_group<kF32, 64>(a, nv, s);
+  return a.x_type == kF16 ? launch_g4_group<kF16, 64>(a, nv, s) : launch_g4_group<kBF16, 64>(a, nv, s);
+}
+
+}  // namespace iq4

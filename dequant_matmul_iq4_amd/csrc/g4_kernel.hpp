@@ -1,22 +1,27 @@
-// g4_kernel.hpp -- the product of few rows with group-scaled 4-bit weights (g4.hpp): the kernel
-// and its launch, compiled once per type of the activations (g4_f32.hip, g4_f16.hip, g4_bf16.hip).
+// g4_kernel.hpp -- the product of few rows with group-scaled 4-bit weights (g4.hpp): the kernel and
+// its launch, compiled once per group size and type of X (g4_32.hip, g4_64.hip, g4_128.hip).
 //
-// Mathematics.  With d = sum over 32 (or the whole group's) k of (q - z) x, a row's result is the
-// sum of s d over its groups.  q - z is a whole number of four bits and a sign, exact in binary16
-// and in bfloat16, so the matrix instruction's products are exact and its sums are binary32;
-// each group's d is scaled by one fused multiply-add.  No weight is rounded anywhere.
+// Mathematics.  With d = sum of (q - z) x over a group's k, a row's result is the sum of s d over
+// its groups.  A code tile's products run on the matrix cores, whose products are exact here and
+// whose sums are binary32; each group's d is scaled by one fused multiply-add.  No weight is rounded.
 //
-// Operands of v_mfma_f32_16x16x32 (lane l = 16 g + c): the activations are the first one, rows of
-// X by c; the weights the second, 16 rows of W by c, so that a lane's scale is that of the row
-// whose codes it holds; the lane receives D[4g + i][c], four rows of X times row c of W.
-//   binary16  q - z = (1024 + q) - (1024 + z), two at a time (the codes are or-ed into the bits
-//             of 1024): 11 operations for eight weights.
-//   bfloat16  q - z = (128 + q) - (128 + z) by a two-term dot product with (1, 0) or (0, 1) into
-//             binary32, then rounded (exactly) in pairs: 19 operations.
-//   binary32  an activation is the sum of three bfloat16 numbers, its leading, middle and last
-//             eight bits (cut, not rounded: exact, and no part overflows).  Up to four rows:
-//             row 4 p + t of the first operand is part p of row t, one instruction for all parts;
-//             more rows: three instructions.
+//   binary16 X  q - z as a binary16 number, (1024 + q) - (1024 + z): the codes are or-ed into the
+//               bits of 1024, two at a time.  11 operations for eight weights.
+//   bfloat16 X  no packed instruction makes q - z a bfloat16 number (19 operations from a dot
+//               product with (1, 0) and (0, 1)), so the weight is 8 + q / 2, or-ed into the bits of 8, and
+//               the group's sums of X, made once for all rows of W, are multiplied by -(8 + z / 2) and begin
+//               d: 8 operations.  The sums are then some five times those of q - z, and so
+//               are their roundings, 2^-24 of them each.  An infinity leaves a NaN (infinity
+//               minus infinity): a result that is not finite is made again, one by one, without this.
+//   binary32 X  two binary16 numbers, the value rounded to eleven bits and what is left, rounded
+//               likewise; a wave has a slice of k, and there a row's values are multiplied by the power
+//               of two that brings the largest to 2^14 .. 2^15, and its sums divided by it.  Within half
+//               a step of binary32 (2^-24) of the value, or 2^-40 of the slice's largest.  Each of
+//               the two is a row of the operand; their sums are joined before they are divided.
+//
+// Operands of v_mfma_f32_16x16x32 (lane l = 16 g + c): the activations are the first one, rows by c;
+// the weights the second, 16 rows of W by c, so that a lane's scale is that of the row whose codes
+// it holds; the lane receives D[4g + i][c], four rows of X times row c of W.
 #pragma once
 #include "experts.hpp"
 #include "g4.hpp"
@@ -24,323 +29,502 @@
 
 namespace iq4 {
 
-enum G4Mode {
-  kG4Half,     // binary16 activations, 16 rows a tile
-  kG4Brain,    // bfloat16, 16 rows a tile
-  kG4Parts4,   // binary32, four rows a tile: the parts are rows of the operand
-  kG4Parts16,  // binary32, 16 rows a tile: one instruction per part
-};
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
-// Eight weights, q - z, as matrix-core operand; `z` is the zero point's byte of a word.
-__device__ __forceinline__ u32x4 g4_half(uint32_t w, uint32_t bias) {
+// An instruction takes one constant from a scalar register, the other has to come from a vector one.
+struct G4Consts {
+  uint32_t lo, hi, top;
+};
+template <bool BRAIN>
+__device__ __forceinline__ G4Consts g4_consts() {
+  G4Consts k = {BRAIN ? 0x00780078u : 0x000F000Fu, 0x00F000F0u, BRAIN ? 0x41004100u : 0x64006400u};
+  asm("" : "+s"(k.lo), "+s"(k.hi), "+v"(k.top));  // opaque: not literals
+  return k;
+}
+// Eight weights of a word: q - z in binary16 (bias 1024 + z twice; the second pair is 16 q in the bits of
+// 1024, brought down by a multiply-add with bias16, -(64 + z) twice).
+// (SHIFT: brought down by a shift instead, where bias16 would serve for eight weights only.)
+template <bool SHIFT>
+__device__ __forceinline__ u32x4 g4_half(const G4Consts& k, uint32_t w, f16x2 bias, f16x2 bias16) {
+  const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
   u32x4 r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u;
-    const f16x2 d = __builtin_bit_cast(f16x2, v) - __builtin_bit_cast(f16x2, bias);
-    r[i] = __builtin_bit_cast(uint32_t, d);
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t v = h ? w >> 8 : w;
+    const f16x2 a = __builtin_bit_cast(f16x2, (v & k.lo) | k.top) - bias;
+    f16x2 b;
+    if constexpr (SHIFT) b = __builtin_bit_cast(f16x2, ((w >> (8 * h + 4)) & k.lo) | k.top) - bias;
+    else b = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (v & k.hi) | k.top), sixteenth, bias16);
+    r[2 * h] = __builtin_bit_cast(uint32_t, a);
+    r[2 * h + 1] = __builtin_bit_cast(uint32_t, b);
   }
   return r;
 }
-__device__ __forceinline__ u32x4 g4_brain(uint32_t w, float bias, uint32_t one_lo, uint32_t one_hi) {
-  u32x4 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bf16x2 v = __builtin_bit_cast(bf16x2, ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u);
-    const bf16x2 d = {(__bf16)__builtin_amdgcn_fdot2_f32_bf16(v, __builtin_bit_cast(bf16x2, one_lo), bias, false),
-                      (__bf16)__builtin_amdgcn_fdot2_f32_bf16(v, __builtin_bit_cast(bf16x2, one_hi), bias, false)};
-    r[i] = __builtin_bit_cast(uint32_t, d);
-  }
-  return r;
+// 8 + q / 2 in bfloat16.
+__device__ __forceinline__ u32x4 g4_brain(const G4Consts& k, uint32_t w) {
+  return u32x4{((w << 3) & k.lo) | k.top, ((w >> 1) & k.lo) | k.top, ((w >> 5) & k.lo) | k.top, ((w >> 9) & k.lo) | k.top};
 }
 
-// The three parts of eight binary32 numbers.  An infinity's rest counts as zero (infinity minus
-// itself would make a NaN of it).
-struct G4Parts {
-  u32x4 p[3];
-};
-__device__ __forceinline__ G4Parts g4_parts(const u32x4 (&x)[2]) {
-  G4Parts r;
-  float v[8], top = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x[i >> 2][i & 3]);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
-  const bool inf = __ballot(top == __builtin_inff()) != 0;
-#pragma unroll
-  for (int q = 0; q < 3; ++q) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r.p[q][i] = __builtin_amdgcn_perm(__float_as_uint(v[2 * i + 1]), __float_as_uint(v[2 * i]), 0x07060302u);
-    if (q == 2) break;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float rest = v[i] - __uint_as_float(__float_as_uint(v[i]) & 0xFFFF0000u);
-      if (inf) rest = fabsf(v[i]) == __builtin_inff() ? 0.f : rest;
-      v[i] = rest;
+// Largest value over the 16 lanes of a row.
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = max(v, (uint32_t)lane_move<0xB1>((int)v));   // lane ^ 1
+  v = max(v, (uint32_t)lane_move<0x4E>((int)v));   // lane ^ 2
+  v = max(v, (uint32_t)lane_move<0x141>((int)v));  // half rows mirrored
+  return max(v, (uint32_t)lane_move<0x140>((int)v));  // rows mirrored
+}
+// x less the binary16 number in the low or high half of h, exact: one mixed instruction each.
+__device__ __forceinline__ float less_lo(float x, uint32_t h) {
+  float r;
+  asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r) : "v"(h), "v"(x));
+  return r;
+}
+__device__ __forceinline__ float less_hi(float x, uint32_t h) {
+  float r;
+  asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r) : "v"(h), "v"(x));
+  return r;
+}
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// One result by itself, from the definition.
+template <int XT>
+__device__ float g4_single(const G4Args& a, const uint8_t* W, int64_t x_row, int64_t r) {
+  const int64_t rt = r >> 4, kt_n = g4_k_tiles(a.k);
+  const int c = (int)(r & 15), sets = 128 / a.group;
+  const uint16_t* ss = reinterpret_cast<const uint16_t*>(W + g4_code_plane(a.n, a.k));
+  const uint8_t* zs = W + g4_code_plane(a.n, a.k) + g4_scale_plane(a.n, a.k, a.group);
+  float acc = 0.f;
+#pragma nounroll
+  for (int64_t k0 = 0; k0 < a.k; k0 += a.group) {
+    const int64_t tile = rt * kt_n + (k0 >> 7), at = (tile * 16 + c) * sets + (k0 & 127) / a.group;
+    const float s = a.scale_type == kF16 ? h2f(ss[at]) : __uint_as_float((uint32_t)ss[at] << 16);
+    const int z = a.zeros ? zs[at] : 8;
+    float d = 0.f;
+#pragma nounroll
+    for (int64_t k = k0; k < min(k0 + a.group, a.k); ++k) {
+      const int b = (int)(k >> 5 & 3), g = (int)(k >> 3 & 3), e = (int)(k & 7);
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(W + tile * kG4TileBytes + (16 * g + c) * 16 + 4 * b);
+      const uint16_t h = static_cast<const uint16_t*>(a.x)[x_row * a.ldx + k];
+      d = fmaf((float)((int)(w >> (16 * (e & 1) + 4 * (e >> 1)) & 15u) - z), __uint_as_float((uint32_t)h << 16), d);
     }
+    acc = fmaf(s, d, acc);
   }
-  return r;
+  return acc;
 }
 
-// A workgroup of KS waves: RT row tiles of W against one tile of NT x 16 (kG4Parts4: 4) rows of
-// X, k split over the waves (wave s takes the code tiles s, s + KS, ...), whose sums are added
-// through LDS in the waves' order.  Every operand goes from memory straight into registers, D
-// tiles of 128 along k ahead of its products.
-template <int XM, int NT, int RT, int G, int D>
-__global__ void __launch_bounds__(512) g4_kernel(G4Args a, uint32_t row_groups, uint32_t cols) {
-  constexpr int kTok = XM == kG4Parts4 ? 4 : 16, kBM = kTok * NT, kMaxWaves = 8;
-  constexpr int kXs = XM == kG4Parts4 ? 2 : XM == kG4Parts16 ? 8 : 4;  // 16-byte words of a row tile's x a lane
-  constexpr int kSets = 128 / G, kSteps = G / 32;                     // groups of a code tile, steps of a group
-  constexpr int kElem = XM == kG4Half || XM == kG4Brain ? 2 : 4;
-  constexpr int kStageRow = 128 * 2 + 16;  // a part's row of 128, 16 bytes on: 16 rows begin in different banks
-  __shared__ f32x4 part[kMaxWaves * RT * NT * 64];
-  __shared__ uint8_t stage[XM == kG4Parts4 ? kMaxWaves * 12 * kStageRow : 16];
+// How a call's work is dealt out (set by the launcher).
+struct G4Plan {
+  int cols;    // tiles of rows of X
+  int y;       // those along the grid's y (the rest along z)
+  int ks;      // waves a workgroup
+  int kt_n, rt_n;  // code tiles along k, row tiles
+  int per;     // row tiles of W a workgroup
+  int rb;      // row tiles between two joins of the waves' sums: all, or a multiple of four
+  int chunks;  // slices of k one after another (the activations of one are in registers)
+};
+constexpr int kG4StageRow = 128 * 2 + 16;  // a row of 128 binary16 numbers; 16 bytes on, so that rows begin in different banks
+// A wave's LDS before its sums: the way of its operands; binary32, the powers of two; bfloat16, the groups'
+// sums of X.
+constexpr int g4_x_lds(int xt, int nv, int sx, int group) {
+  return 16 * kG4StageRow + (xt == kF32 ? nv * 64 : xt == kBF16 ? sx * (128 / group) * nv * 64 : 0);
+}
+
+// A workgroup of KS waves: `per` row tiles of W against one tile of rows of X (NV operands of 16
+// rows; a binary32 row is two of them), k dealt out to the waves in slices of SX code tiles.  A wave
+// keeps its slice of X as operands in registers and runs over the row tiles, whose codes go from
+// memory straight into registers, a row tile ahead.  The waves' sums are joined through LDS in
+// the waves' order.
+template <int XT, int NV, int SX, int G, bool CHUNKS>
+__global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
+  // all arguments at once: loaded where they are used, one would wait for memory after the other
+  asm volatile("" ::"s"(a.W), "s"(a.n), "s"(a.k), "s"(a.scale_type), "s"(a.zeros), "s"(a.x), "s"(a.ldx), "s"(a.m));
+  asm volatile("" ::"s"(a.y), "s"(a.y_type), "s"(a.ldy), "s"(a.offsets), "s"(plan.cols), "s"(plan.y), "s"(plan.ks));
+  asm volatile("" ::"s"(plan.kt_n), "s"(plan.rt_n), "s"(plan.per), "s"(plan.rb), "s"(plan.chunks));
+  constexpr bool f32 = XT == kF32;
+  constexpr int kBM = f32 ? 8 * NV : 16 * NV;
+  constexpr int kSets = 128 / G, kSteps = G / 32;  // groups of a code tile, steps of a group
+  constexpr int kFours = f32 ? 2 : 4;              // groups of four rows of X in an operand
+  constexpr int kXLds = g4_x_lds(XT, NV, SX, G);
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const int slice = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), KS = blockDim.x >> 6;
-  // workgroups go round-robin to eight XCDs: the column tiles that share rows of W go to one
-  const uint32_t in = blockIdx.x / 8, rg = in / cols * 8 + blockIdx.x % 8;
-  const int col = (int)(in % cols);
-  if (rg >= row_groups) return;
+  const int slice = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), KS = plan.ks;
+  const int col = (int)blockIdx.z * plan.y + (int)blockIdx.y;
+  if (col >= plan.cols) return;
   const uint8_t* W = a.W;
-  int row0 = col * kBM, rows;
-  if (a.offsets) {
+  int row0 = col * kBM, rows = min(kBM, (int)a.m - row0);
+  if (__builtin_expect(a.offsets != nullptr, 0)) {
     int e;
     if (!expert_tile(a.offsets, a.n_expert, (int)a.m, kBM, col, e, row0, rows)) return;
     W += e * a.w_stride;
-  } else {
-    rows = (int)min((int64_t)kBM, a.m - row0);
   }
-  const int kt_n = g4_k_tiles(a.k), kq_n = g4_k_quads(a.k), K = (int)a.k;
-  const int64_t rt_n = g4_row_tiles(a.n), rt0 = (int64_t)rg * RT;
-  const uint8_t* wq[RT];
-  const uint8_t* ws[RT];
-  const uint8_t* wz[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {  // row tiles past the last repeat it and are not stored
-    const int64_t rt = min(rt0 + r, rt_n - 1);
-    wq[r] = W + rt * kt_n * kG4TileBytes + lane * 16;
-    ws[r] = W + g4_code_plane(a.n, a.k) + (rt * kq_n * 16 + c) * (512 / G) * 2;
-    wz[r] = W + g4_code_plane(a.n, a.k) + g4_scale_plane(a.n, a.k, G) + (rt * kq_n * 16 + c) * (512 / G);
-  }
+  const int kt_n = plan.kt_n, rt_n = plan.rt_n, K = (int)a.k;
+  const int first = (int)blockIdx.x * plan.per, last = min(first + plan.per, rt_n);
+  const int wave_lds = kXLds + plan.rb * NV * 1024;
+  uint8_t* mine = lds + slice * wave_lds;
+  int* exps = reinterpret_cast<int*>(mine + 16 * kG4StageRow);  // binary32
+  uint8_t* sums = mine + 16 * kG4StageRow;                       // bfloat16
+  f32x4* part = reinterpret_cast<f32x4*>(mine + kXLds);
+
+  // ---- codes, scales and zero points of a row tile's slice ------------------------------------------
   struct WTile {
-    u32x4 q[RT];
-    uint32_t s[RT][G == 32 ? 2 : 1], z[RT];
+    u32x4 q;
+    uint32_t s[G == 32 ? 2 : 1], z;
   };
-  struct XTile {
-    u32x4 x[NT][kXs];
-  };
-  auto load_w = [&](int j, WTile& o) {
-    const int at = (j >> 2) * 16 * (512 / G) + (j & 3) * kSets;  // in scales
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      o.q[r] = *reinterpret_cast<const u32x4*>(wq[r] + (int64_t)j * kG4TileBytes);
-      if constexpr (G == 32) {
-        const u32x2 s = *reinterpret_cast<const u32x2*>(ws[r] + 2 * at);
-        o.s[r][0] = s[0], o.s[r][1] = s[1];
-      } else if constexpr (G == 64) {
-        o.s[r][0] = *reinterpret_cast<const uint32_t*>(ws[r] + 2 * at);
-      } else {
-        o.s[r][0] = *reinterpret_cast<const uint16_t*>(ws[r] + 2 * at);
-      }
-      o.z[r] = 0x08080808u;
-      if (a.zeros) {
-        if constexpr (G == 32) o.z[r] = *reinterpret_cast<const uint32_t*>(wz[r] + at);
-        else if constexpr (G == 64) o.z[r] = *reinterpret_cast<const uint16_t*>(wz[r] + at);
-        else o.z[r] = *(wz[r] + at);
-      }
+  const int64_t tiles_n = (int64_t)rt_n * kt_n;
+  const uint8_t* S = W + tiles_n * kG4TileBytes;
+  const uint8_t* Z = S + tiles_n * (16 * kSets * 2);
+  auto load_w = [&](int64_t tile, WTile& o) {  // tile: rt * kt_n + kt, the same in all lanes
+    o.q = *reinterpret_cast<const u32x4*>(W + tile * kG4TileBytes + (uint32_t)(lane * 16));
+    const uint8_t* s = S + tile * (16 * kSets * 2) + (uint32_t)(c * kSets * 2);
+    if constexpr (G == 32) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(s);
+      o.s[0] = v[0], o.s[1] = v[1];
+    } else if constexpr (G == 64) {
+      o.s[0] = *reinterpret_cast<const uint32_t*>(s);
+    } else {
+      o.s[0] = *reinterpret_cast<const uint16_t*>(s);
+    }
+    o.z = 0x08080808u;
+    if (a.zeros) {
+      const uint8_t* z = Z + tile * (16 * kSets) + (uint32_t)(c * kSets);
+      if constexpr (G == 32) o.z = *reinterpret_cast<const uint32_t*>(z);
+      else if constexpr (G == 64) o.z = *reinterpret_cast<const uint16_t*>(z);
+      else o.z = *z;
     }
   };
-  // this lane's rows of X: row 16 i + c of the tile (rows past the last repeat it and are not
-  // stored), from element 8 g on; kG4Parts4: row g, from element 8 c on
-  const uint8_t* xp[NT];
+  // A slice's code tiles [base, base + SX).  Where the slice would pass the last code tile it begins
+  // earlier, and the tiles that are not its own (below `own`) get activations of zero.
+  auto slice_of = [&](int chunk, int& base, int& own) {
+    own = (chunk * KS + slice) * SX;
+    base = min(own, kt_n - SX);
+  };
+
+  // ---- the activations of a slice, as operands in registers ------------------------------------------
+  // First as in memory, whole rows of a code tile: lane (g, c) has elements 8 c .. 8 c + 7 of row 4 p + g in
+  // word p, binary32 in words 2 p and 2 p + 1.  (As the instruction takes them, neighbouring lanes would
+  // load of different rows, 64 cache lines an instruction, which takes four times as long: 16 rows of
+  // 14336 x 4096 so 14.1 us, and 4.2 of them until the loads are under way.)  Then through LDS.
+  u32x4 xf[SX][NV][4];
+  auto x_row = [&](int i) {  // row i of the tile (one past the last repeats that, and is not stored)
+    int r = row0 + min(i, rows - 1);
+    if (__builtin_expect(a.offsets != nullptr, 0)) {
+      if (a.pairs) r = a.pairs[r] / a.top_k;
+      r = min(max(r, 0), (int)a.n_rows - 1);
+    }
+    return (int64_t)r;
+  };
+  auto load_x = [&](int chunk) {
+    int base, own;
+    slice_of(chunk, base, own);
+    const bool whole = base == own && (base + SX) * 128 <= K;  // the same in all lanes
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    int64_t r = row0 + min(XM == kG4Parts4 ? g : 16 * i + c, rows - 1);
-    if (a.pairs) r = a.pairs[r] / a.top_k;
-    if (a.offsets) r = min(max(r, (int64_t)0), a.n_rows - 1);
-    xp[i] = static_cast<const uint8_t*>(a.x) + (r * a.ldx + 8 * (XM == kG4Parts4 ? c : g)) * kElem;
-  }
-  auto load_x = [&](int j, XTile& o) {
-    if constexpr (XM == kG4Parts4) {
-      const uint8_t* p = xp[0] + (int64_t)j * 128 * 4;
-      o.x[0][0] = o.x[0][1] = u32x4{0u, 0u, 0u, 0u};
-      if (128 * j + 8 * c < K) o.x[0][0] = get16<false>(p), o.x[0][1] = get16<false>(p + 16);
-    } else {
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
+      for (int p = 0; p < kFours; ++p) {
+        if (4 * (kFours * v + p) >= rows) continue;  // (no result comes of what LDS then holds)
+        const int i = 4 * (kFours * v + p) + g;
+        const bool here = i < rows;
+        const char* x = static_cast<const char*>(a.x) + (x_row(i) * a.ldx + 128 * (int64_t)base + 8 * c) * (f32 ? 4 : 2);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const uint8_t* p = xp[i] + ((int64_t)j * 128 + 32 * s) * kElem;
-          const bool is = 128 * j + 32 * s < K;  // the same in all lanes
-          if constexpr (XM == kG4Parts16) {
-            o.x[i][2 * s] = o.x[i][2 * s + 1] = u32x4{0u, 0u, 0u, 0u};
-            if (is) o.x[i][2 * s] = get16<false>(p), o.x[i][2 * s + 1] = get16<false>(p + 16);
-          } else {
-            o.x[i][s] = u32x4{0u, 0u, 0u, 0u};
-            if (is) o.x[i][s] = get16<false>(p);
+        for (int t = 0; t < SX; ++t) {
+          u32x4 lo = {0u, 0u, 0u, 0u}, hi = {0u, 0u, 0u, 0u};
+          if (here && (whole || (base + t >= own && 128 * (base + t) + 8 * c < K))) {
+            lo = get16<false>(x + 128 * t * (f32 ? 4 : 2));
+            if constexpr (f32) hi = get16<false>(x + 128 * t * 4 + 16);
           }
+          if constexpr (f32) xf[t][v][2 * p] = lo, xf[t][v][2 * p + 1] = hi;
+          else xf[t][v][p] = lo;
         }
       }
+  };
+  auto make_operands = [&]() {
+    if constexpr (!f32) {
+#pragma unroll
+      for (int t = 0; t < SX; ++t)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            if (16 * v + 4 * p < rows) *reinterpret_cast<u32x4*>(mine + (4 * p + g) * kG4StageRow + 16 * c) = xf[t][v][p];
+          wave_fence();
+#pragma unroll
+          for (int s = 0; s < 4; ++s) xf[t][v][s] = *reinterpret_cast<const u32x4*>(mine + c * kG4StageRow + 64 * s + 16 * g);
+          wave_fence();
+        }
+    }
+    if constexpr (XT == kBF16) {  // the groups' sums of each row
+      const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll
+      for (int t = 0; t < SX; ++t)
+#pragma unroll
+        for (int b = 0; b < kSets; ++b)
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) d = mfma_bf16(xf[t][v][b * kSteps + s], ones, d);
+            if (c == 0) *reinterpret_cast<f32x4*>(sums + ((t * kSets + b) * NV + v) * 64 + 16 * g) = d;
+          }
+      wave_fence();
+    }
+    if constexpr (f32) {
+      uint32_t scale[NV][2];  // bits of the power of two
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          if (8 * v + 4 * p >= rows) continue;
+          float top = 0.f;  // (a NaN is passed over: it makes its own results NaN whatever the scale is)
+#pragma unroll
+          for (int t = 0; t < SX; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              top = fmaxf(fmaxf(top, fabsf(__uint_as_float(xf[t][v][2 * p][i]))), fabsf(__uint_as_float(xf[t][v][2 * p + 1][i])));
+          // 2^(141 - E) for a largest value of exponent field E, at most 2^126
+          const uint32_t f = min(268u - (row_max(__float_as_uint(top)) >> 23), 253u);
+          scale[v][p] = f << 23;
+          if (c == 0) exps[16 * v + 4 * p + g] = 127 - (int)f;
+        }
+#pragma unroll
+      for (int t = 0; t < SX; ++t)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            if (8 * v + 4 * p >= rows) continue;
+            const float s = __uint_as_float(scale[v][p]);
+            float x[8], rest[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[i] = __uint_as_float(xf[t][v][2 * p][i]) * s;
+              x[4 + i] = __uint_as_float(xf[t][v][2 * p + 1][i]) * s;
+            }
+            u32x4 h, m;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              asm("" : "+v"(x[2 * i]), "+v"(x[2 * i + 1]));  // (one packed conversion, not two mixed products)
+              h[i] = pack2<kF16>(x[2 * i], x[2 * i + 1]);
+              rest[2 * i] = less_lo(x[2 * i], h[i]);
+              rest[2 * i + 1] = less_hi(x[2 * i + 1], h[i]);
+            }
+            if (__builtin_expect(__ballot(s == 0x1p-114f) != 0, 0)) {  // a row holds an infinity: it has no rest
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (fabsf(x[i]) == __builtin_inff()) rest[i] = 0.f;
+                asm volatile("" : "+v"(rest[i]));  // (keeps this a branch: as selects it costs every call)
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = pack2<kF16>(rest[2 * i], rest[2 * i + 1]);
+            uint8_t* to = mine + (4 * p + g) * kG4StageRow + 16 * c;
+            *reinterpret_cast<u32x4*>(to) = h;
+            *reinterpret_cast<u32x4*>(to + 8 * kG4StageRow) = m;
+          }
+          wave_fence();
+#pragma unroll
+          for (int s = 0; s < 4; ++s) xf[t][v][s] = *reinterpret_cast<const u32x4*>(mine + c * kG4StageRow + 64 * s + 16 * g);
+          wave_fence();
+        }
     }
   };
-  f32x4 acc[RT][NT];
+
+  // ---- products ---------------------------------------------------------------------------------------
+  const G4Consts consts = g4_consts<XT == kBF16>();
+  const bool scale_f16 = a.scale_type == kF16;
+  f32x4 acc[NV];
+  auto multiply = [&](int t, const WTile& w) {
+    float sc[kSets];
+    if (scale_f16) {
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
+      for (int b = 0; b < kSets; ++b) sc[b] = h2f((uint16_t)(w.s[b >> 1] >> (16 * (b & 1))));
+    } else {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  uint32_t one_lo = 0x00003F80u, one_hi = 0x3F800000u;  // (1, 0) and (0, 1) as bfloat16 pairs
-  asm("" : "+s"(one_lo), "+s"(one_hi));                   // opaque: kept in registers
-  uint8_t* mine = stage + (XM == kG4Parts4 ? slice * 12 * kStageRow : 0);
-  auto multiply = [&](const WTile& w, const XTile& x) {
-    u32x4 xf[4];  // kG4Parts4: the four steps' operands
-    if constexpr (XM == kG4Parts4) {
-      // from row g, elements 8 c .. 8 c + 7 to the parts' rows; the wave's own LDS, in order
-      const G4Parts p = g4_parts(x.x[0]);
-#pragma unroll
-      for (int q = 0; q < 3; ++q) *reinterpret_cast<u32x4*>(mine + (4 * q + g) * kStageRow + 16 * c) = p.p[q];
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      const uint8_t* row = mine + (c < 12 ? c : c - 12) * kStageRow + 16 * g;  // (rows 12 .. 15 of the result are not used)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) xf[s] = *reinterpret_cast<const u32x4*>(row + 64 * s);
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      for (int b = 0; b < kSets; ++b) sc[b] = __uint_as_float((b & 1) ? w.s[b >> 1] & 0xFFFF0000u : w.s[b >> 1] << 16);
     }
 #pragma unroll
     for (int b = 0; b < kSets; ++b) {
-      f32x4 d[RT][NT];
+      f32x4 d[NV];
+      if constexpr (XT == kBF16) {
+        const float corr = fmaf((float)((w.z >> (8 * b)) & 0xFFu), -0.5f, -8.0f);
+        sc[b] = sc[b] + sc[b];
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+        for (int v = 0; v < NV; ++v) {
+          const f32x4 sum = *reinterpret_cast<const f32x4*>(sums + ((t * kSets + b) * NV + v) * 64 + 16 * g);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) d[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int t = 0; t < kSteps; ++t) {
-        const int s = b * kSteps + t;
-        u32x4 wf[RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          if constexpr (XM == kG4Half) {
-            // 1024 + z twice: the zero point's byte under the byte 0x64
-            const uint32_t bias = __builtin_amdgcn_perm(0x64646464u, w.z[r], 0x04000400u + 0x00010001u * b);
-            wf[r] = g4_half(w.q[r][s], bias);
-          } else {
-            wf[r] = g4_brain(w.q[r][s], -128.0f - (float)((w.z[r] >> (8 * b)) & 0xFFu), one_lo, one_hi);
-          }
+          for (int e = 0; e < 4; ++e) d[v][e] = corr * sum[e];
         }
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          if constexpr (XM == kG4Half) {
+        for (int s = 0; s < kSteps; ++s) {
+          const u32x4 wf = g4_brain(consts, w.q[b * kSteps + s]);
 #pragma unroll
-            for (int r = 0; r < RT; ++r) d[r][i] = mfma_f16(x.x[i][s], wf[r], d[r][i]);
-          } else if constexpr (XM == kG4Brain) {
+          for (int v = 0; v < NV; ++v) d[v] = mfma_bf16(xf[t][v][b * kSteps + s], wf, d[v]);
+        }
+      } else {
+        // 1024 + z twice: the zero point's byte under the byte 0x64
+        const uint32_t bias = __builtin_amdgcn_perm(0x64646464u, w.z, 0x04000400u + 0x00010001u * b);
+        const uint32_t bias16 = ((bias << 4) & 0x00F000F0u) | 0xD400D400u;  // -(64 + z) twice
 #pragma unroll
-            for (int r = 0; r < RT; ++r) d[r][i] = mfma_bf16(x.x[i][s], wf[r], d[r][i]);
-          } else if constexpr (XM == kG4Parts4) {
+        for (int s = 0; s < kSteps; ++s) {
+          const u32x4 wf = g4_half<G == 32>(consts, w.q[b * kSteps + s], __builtin_bit_cast(f16x2, bias), __builtin_bit_cast(f16x2, bias16));
 #pragma unroll
-            for (int r = 0; r < RT; ++r) d[r][i] = mfma_bf16(xf[s], wf[r], d[r][i]);
-          } else {
-            const u32x4 two[2] = {x.x[i][2 * s], x.x[i][2 * s + 1]};
-            const G4Parts p = g4_parts(two);
-#pragma unroll
-            for (int q = 2; q >= 0; --q)
-#pragma unroll
-              for (int r = 0; r < RT; ++r) d[r][i] = mfma_bf16(p.p[q], wf[r], d[r][i]);
-          }
+          for (int v = 0; v < NV; ++v) d[v] = mfma_f16(xf[t][v][b * kSteps + s], wf, s ? d[v] : f32x4{0.f, 0.f, 0.f, 0.f});
         }
       }
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const uint32_t bits = w.s[r][b >> 1] >> (16 * (b & 1)) & 0xFFFFu;
-        const float sc = a.scale_type == kF16 ? h2f((uint16_t)bits) : __uint_as_float(bits << 16);
+      for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int e = 0; e < 4; ++e) acc[v][e] = fmaf(d[v][e], sc[b], acc[v][e]);
+    }
+    // (opaque: or the compiler scales all tiles' sums behind the last one, and holds them until then)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[r][i][e] = fmaf(d[r][i][e], sc, acc[r][i][e]);
+    for (int v = 0; v < NV; ++v) asm volatile("" : "+v"(acc[v]));
+  };
+  // the sums of a row tile and a slice of k, divided by the rows' powers of two, into LDS (or added there)
+  auto keep = [&](int rb, bool add) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      f32x4 s = acc[v];
+      if constexpr (f32) {  // rows 8 .. 15 have what rows 0 .. 7 left
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = __builtin_amdgcn_ldexpf(s[e] + __shfl_xor(s[e], 32), exps[16 * v + 4 * (g & 1) + e]);
       }
+      f32x4* to = part + (rb * NV + v) * 64 + lane;
+      if (add) {
+        const f32x4 o = *to;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = o[e] + s[e];
+      }
+      *to = s;
     }
   };
-  const int n = (kt_n - slice + KS - 1) / KS;
-  WTile w[D];
-  XTile x[D];
-#pragma unroll
-  for (int v = 0; v < D; ++v)
-    if (v < n) {
-      load_w(slice + v * KS, w[v]);
-      load_x(slice + v * KS, x[v]);
-    }
-  for (int i0 = 0; i0 < n; i0 += D) {
-#pragma unroll
-    for (int v = 0; v < D; ++v) {
-      const int i = i0 + v;
-      if (i >= n) break;
-      multiply(w[v], x[v]);
-      if (i + D < n) {
-        load_w(slice + (i + D) * KS, w[v]);
-        load_x(slice + (i + D) * KS, x[v]);
-      }
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int i = 0; i < NT; ++i) part[((slice * RT + r) * NT + i) * 64 + lane] = acc[r][i];
-  __syncthreads();
   auto store = [&](int t, int64_t at, float v) {  // row t of the tile, column `at`
     if (t >= rows || at >= a.n) return;
+    if constexpr (XT == kBF16) {
+      if (__builtin_expect(!(fabsf(v) < __builtin_inff()), 0)) v = g4_single<XT>(a, W, x_row(t), at);
+    }
     const int64_t o = (int64_t)(row0 + t) * a.ldy + at;
     if (a.y_type == kF32) static_cast<float*>(a.y)[o] = v;
     else static_cast<uint16_t*>(a.y)[o] = (uint16_t)(a.y_type == kF16 ? pack2<kF16>(v, 0.f) : pack2<kBF16>(v, 0.f));
   };
-  for (int q = slice; q < RT * NT; q += KS) {
-    const int r = q / NT, i = q % NT;
-    if (rt0 + r >= rt_n) continue;
-    const int64_t at = (rt0 + r) * 16 + c;
-    if constexpr (XM == kG4Parts4) {  // lane (g, c): row g, the sum over its three parts
-      float s = 0.f;
-      for (int v = 0; v < KS; ++v)
+
+  constexpr int kAhead = SX == 1 ? 4 : SX <= 3 ? 2 : 1;  // row tiles, some 4 KB a wave
+  int base, own;
+  slice_of(0, base, own);
+  load_x(0);
+  WTile w[kAhead][SX];
 #pragma unroll
-        for (int p = 0; p < 3; ++p) s = s + part[(v * RT + r) * 64 + 16 * p + c][g];
-      store(g, at, s);
-    } else {
-      f32x4 s = part[q * 64 + lane];
+  for (int d = 0; d < kAhead; ++d)
+    if (first + d < last)
+#pragma unroll
+      for (int t = 0; t < SX; ++t) load_w((int64_t)(first + d) * kt_n + base + t, w[d][t]);
+  for (int b = first; b < last; b += plan.rb) {
+    const int tiles = min(plan.rb, last - b);
+    for (int chunk = 0; chunk < (CHUNKS ? plan.chunks : 1); ++chunk) {
+      const bool begin = b == first && chunk == 0;
+      if (begin || CHUNKS) {
+        if (!begin) load_x(chunk);
+        make_operands();
+      }
+      for (int rb = 0; rb < tiles; rb += kAhead) {
+        // the kAhead row tiles that come after these
+        int nr = b + rb + kAhead, nc = chunk;
+        if (rb + kAhead >= tiles) {
+          nr = b, nc = chunk + 1;
+          if (!CHUNKS || nc == plan.chunks) nr = b + plan.rb, nc = 0;
+        }
+        slice_of(nc, base, own);
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+          if (rb + d < tiles) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+          }
+#pragma unroll
+          for (int t = 0; t < SX; ++t) {
+            if (rb + d < tiles) multiply(t, w[d][t]);
+            if (nr + d < last) load_w((int64_t)(nr + d) * kt_n + base + t, w[d][t]);
+            __builtin_amdgcn_sched_barrier(0);  // (the tiles' operands, mixed, would not fit the registers)
+          }
+          if (rb + d < tiles) keep(rb + d, chunk > 0);
+        }
+      }
+    }
+    lds_barrier();
+    for (int q = slice; q < tiles * NV; q += KS) {
+      const uint8_t* p = lds + kXLds + (q * 64 + lane) * 16;
+      f32x4 s = *reinterpret_cast<const f32x4*>(p);
       for (int v = 1; v < KS; ++v) {
-        const f32x4 o = part[(v * RT * NT + q) * 64 + lane];
+        const f32x4 o = *reinterpret_cast<const f32x4*>(p + v * wave_lds);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[e] = s[e] + o[e];
       }
+      const int v = q % NV;
+      const int64_t at = (int64_t)(b + q / NV) * 16 + c;
+      if (!f32 || g < 2) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) store(16 * i + 4 * g + e, at, s[e]);
+        for (int e = 0; e < 4; ++e) store((f32 ? 8 : 16) * v + 4 * g + e, at, s[e]);
+      }
     }
+    if (b + plan.rb < last) lds_barrier();  // the sums are read before the next ones are written
   }
 }
 
-template <int XM, int NT, int RT, int G, int D>
-static int launch_g4_tile(const G4Args& a, hipStream_t s) {
-  constexpr int kBM = (XM == kG4Parts4 ? 4 : 16) * NT;
-  const int64_t row_groups = (g4_row_tiles(a.n) + RT - 1) / RT;
-  int64_t cols = (a.m + kBM - 1) / kBM;
-  // by expert: each expert's last tile may be partial
-  if (a.offsets) cols = a.m / kBM + a.n_expert < a.m ? a.m / kBM + a.n_expert : a.m;
-  const int kt_n = g4_k_tiles(a.k);
-  int ks = kt_n < 8 ? kt_n : 8;
-  const int each = (kt_n + ks - 1) / ks;
-  ks = (kt_n + each - 1) / each;
-  const int64_t groups = (row_groups + 7) / 8 * 8 * cols;
-  if (groups * 64 * ks >= (int64_t)1 << 32)
-    return set_error(-3, "iq4_g4 product: too many workgroups (n * m too large)");
-  hipLaunchKernelGGL((g4_kernel<XM, NT, RT, G, D>), dim3((unsigned)groups), dim3(64 * ks), 0, s, a, (uint32_t)row_groups,
-                     (uint32_t)cols);
+template <int XT, int NV, int SX, int G, bool CHUNKS = false>
+static int launch_g4_kernel(const G4Args& a, G4Plan p, hipStream_t s) {
+  // (at most 512 workgroups or one a tile of X, 2^21: far from a grid's 2^32 threads)
+  p.kt_n = g4_k_tiles(a.k);
+  p.rt_n = (int)g4_row_tiles(a.n);
+  p.y = p.cols < 32768 ? p.cols : 32768;
+  p.chunks = (p.kt_n + p.ks * SX - 1) / (p.ks * SX);
+  const dim3 grid((unsigned)((p.rt_n + p.per - 1) / p.per), (unsigned)p.y, (unsigned)((p.cols + p.y - 1) / p.y));
+  const int lds = p.ks * (g4_x_lds(XT, NV, SX, G) + p.rb * NV * 1024);
+  hipLaunchKernelGGL((g4_kernel<XT, NV, SX, G, CHUNKS>), grid, dim3(64 * p.ks), lds, s, a, p);
   return check_launch("g4_kernel");
 }
 
-template <int XM, int NT, int RT, int D>
-static int launch_g4_group(const G4Args& a, hipStream_t s) {
-  if (a.group == 32) return launch_g4_tile<XM, NT, RT, 32, D>(a, s);
-  if (a.group == 64) return launch_g4_tile<XM, NT, RT, 64, D>(a, s);
-  return launch_g4_tile<XM, NT, RT, 128, D>(a, s);
+// k over up to eight waves, sx code tiles of each in registers (as many as those hold; where that is
+// not all of k, one slice after another).
+template <int XT, int G>
+static int launch_g4_group(const G4Args& a, int nv, hipStream_t s) {
+  const int bm = XT == kF32 ? 8 * nv : 16 * nv;
+  int64_t cols = (a.m + bm - 1) / bm;
+  // by expert: each expert's last tile may be partial
+  if (a.offsets) cols = a.m / bm + a.n_expert < a.m ? a.m / bm + a.n_expert : a.m;
+  const int64_t rt_n = g4_row_tiles(a.n);
+  const int kt_n = g4_k_tiles(a.k), most = nv == 1 ? 6 : 4;
+  int sx = (kt_n + 7) / 8;
+  // short rows: two tiles a wave where there is work for twice the device's waves all the same (128 experts
+  // of 2048 x 768, 488 rows: 23.4 us for 29.6)
+  if (sx == 1 && kt_n > 1 && rt_n * cols * ((kt_n + 1) / 2) >= 8192) sx = 2;
+  if (sx == 5) sx = 6;
+  if (sx == 3 && nv == 2) sx = 4;
+  const bool chunks = sx > most;
+  if (chunks) sx = most;
+  G4Plan p{};
+  p.ks = (kt_n + sx - 1) / sx;
+  if (p.ks > 8) p.ks = 8;
+  p.cols = (int)cols;
+  // row tiles a workgroup: as many as leave the device 8 waves a CU, 16 where their registers allow or
+  // the way of X is short.  14336 x 4096, 16 rows: 12.1 us with 8, 15.8 with 16; one row 9.5 and 8.9; 40000 x
+  // 4096, one row 18.9 and 17.0; 128 experts of 1536 x 2048, 32 rows: 16.0 with 32, 14.4 with 16.
+  const int64_t waves = nv * sx >= 4 && a.m > 4 ? 2048 : 4096;
+  int64_t per = (rt_n * cols * p.ks + waves - 1) / waves;
+  p.per = (int)(per > rt_n ? rt_n : per);
+  p.rb = p.per < 4 ? p.per : 4;  // (a multiple of the row tiles that a wave loads ahead, or all)
+  if (chunks) return nv == 1 ? launch_g4_kernel<XT, 1, 6, G, true>(a, p, s) : launch_g4_kernel<XT, 2, 4, G, true>(a, p, s);
+  switch (10 * nv + sx) {
+    case 11: return launch_g4_kernel<XT, 1, 1, G>(a, p, s);
+    case 12: return launch_g4_kernel<XT, 1, 2, G>(a, p, s);
+    case 13: return launch_g4_kernel<XT, 1, 3, G>(a, p, s);
+    case 14: return launch_g4_kernel<XT, 1, 4, G>(a, p, s);
+    case 16: return launch_g4_kernel<XT, 1, 6, G>(a, p, s);
+    case 21: return launch_g4_kernel<XT, 2, 1, G>(a, p, s);
+    case 22: return launch_g4_kernel<XT, 2, 2, G>(a, p, s);
+    default: return launch_g4_kernel<XT, 2, 4, G>(a, p, s);
+  }
 }
 
 }  // namespace iq4

@@ -544,11 +544,10 @@ int64_t iq4_g4_packed_bytes(int64_t n, int64_t k, int32_t group, int32_t zeros);
  *           All three may have any alignment.
  *   packed  iq4_g4_packed_bytes(n, k, group, zeros != NULL) bytes, 256-byte aligned, overlapping
  *           none of them.
- * Packed layout, KT = ceil(k / 128), KQ = ceil(k / 512), P = 512 / group: code tile (rt, kt) at
- * (rt * KT + kt) * 1024 bytes, 64 entries of 16 bytes; word b of entry 16g + j = elements
- * 8g .. 8g + 7 of block 4kt + b (of 32) of row 16rt + j, elements 0, 2, 4, 6, 1, 3, 5, 7 from the
- * lowest nibble up.  After all code tiles the scales, row j's P of a tile (rt, kq) at
- * ((rt * KQ + kq) * 16 + j) * P * 2 bytes; then the zero points in the same order, a byte each.
+ * Packed layout, KT = ceil(k / 128), P = 128 / group: code tile (rt, kt) at (rt * KT + kt) * 1024 bytes,
+ * 64 entries of 16 bytes; word b of entry 16g + j = elements 8g .. 8g + 7 of block 4kt + b (of 32) of row
+ * 16rt + j, elements 0, 2, 4, 6, 1, 3, 5, 7 from the lowest nibble up.  After all code tiles the scales, row
+ * j's P of a tile at ((rt * KT + kt) * 16 + j) * P * 2 bytes; then the zero points in the same order, a byte each.
  * Zero past n and k.
  * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED.
  */
@@ -564,7 +563,7 @@ int iq4_g4_pack_weights(const void* codes, int64_t ldq, const void* scales, int6
  *   x       [m][ldx], y [m][ldy] of their dtypes (IQ4_F32, IQ4_F16, IQ4_BF16), element aligned,
  *           ldx >= k, ldy >= n; columns n .. ldy - 1 of y are left alone.
  *   m >= 0 (0: no-op); meant for up to some 64 rows, any number up to 2^21 is taken.  No workspace.
- * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED (group, k % 32, sizes; a grid of 2^32 threads).
+ * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED (group, k % 32, sizes).
  */
 int iq4_g4_qmv(const void* packed, int64_t n, int64_t k, int32_t group, int32_t scale_dtype, int32_t zeros,
                const void* x, int32_t x_dtype, int64_t ldx, int64_t m, void* y, int32_t y_dtype, int64_t ldy,

@@ -56,15 +56,15 @@ def product(p, n, k, group, zeros, scale, x, t, y_t, ldx=None, ldy=None):
 def unpacked(p, n, k, group, zeros):
     """Codes, scale bytes and zero points read back out of the documented layout."""
     b = host(p)
-    kt, kq, rt, per = -(-k // 128), -(-k // 512), -(-n // 16), 512 // group
+    kt, rt, per = -(-k // 128), -(-n // 16), 128 // group
     w = b[: rt * kt * 1024].view(np.uint32).reshape(rt, kt, 4, 16, 4)  # row tile, code tile, g, row, block
     q = np.empty((rt, 16, kt, 4, 4, 8), dtype=np.uint8)  # row, code tile, block, g, element
     for nib, e in enumerate((0, 2, 4, 6, 1, 3, 5, 7)):
         q[..., e] = (w >> np.uint32(4 * nib) & np.uint32(15)).transpose(0, 3, 1, 4, 2)
     at = rt * kt * 1024
-    s = b[at: at + rt * kq * 16 * per * 2].view(np.uint16).reshape(rt, kq, 16, per).transpose(0, 2, 1, 3).reshape(rt * 16, -1)
-    at += rt * kq * 16 * per * 2
-    z = b[at: at + rt * kq * 16 * per].reshape(rt, kq, 16, per).transpose(0, 2, 1, 3).reshape(rt * 16, -1) if zeros else None
+    s = b[at: at + rt * kt * 16 * per * 2].view(np.uint16).reshape(rt, kt, 16, per).transpose(0, 2, 1, 3).reshape(rt * 16, -1)
+    at += rt * kt * 16 * per * 2
+    z = b[at: at + rt * kt * 16 * per].reshape(rt, kt, 16, per).transpose(0, 2, 1, 3).reshape(rt * 16, -1) if zeros else None
     return q.reshape(rt * 16, -1), s, z
 
 
@@ -95,7 +95,8 @@ def test_pack_takes_any_alignment_and_strides():
     zz[:, :4] = dev(z) | 0xF0  # the low four bits count
     p = torch.full_like(want, 0xEE)
     iq4.iq4_g4_pack_weights(c, 200, d.data_ptr() + 1, 7, zz, 9, n, k, group, p)
-    assert torch.equal(p[: 2 * 2 * 1024 + 2 * 256 + 2 * 128], want[: 2 * 2 * 1024 + 2 * 256 + 2 * 128])
+    size = 2 * 2 * (1024 + 16 * 2 * 3)  # two row tiles, two code tiles
+    assert torch.equal(p[:size], want[:size])
 
 
 SHAPES = [(1, 32, 32), (16, 128, 128), (17, 160, 32), (5, 544, 64), (48, 672, 128), (100, 2592, 32), (33, 6144, 128), (130, 4096, 64),
