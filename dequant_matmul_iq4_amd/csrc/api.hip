@@ -12,6 +12,7 @@
 #include "moe.hpp"
 #include "g4.hpp"
 #include "mx.hpp"
+#include "pieces.hpp"
 #include "rows.hpp"
 #include "slots.hpp"
 #include "swiglu.hpp"
@@ -783,6 +784,28 @@ static int check_any(const char* fn, const char* what, const void* p, int32_t ty
   return IQ4_OK;
 }
 
+// Rows of `width` bytes every `pitch` bytes.
+struct Span {
+  const char* p;
+  int64_t rows, pitch, width;
+};
+static Span span(const void* p, int64_t rows, int64_t k, int64_t ld, int32_t type) {
+  return Span{static_cast<const char*>(p), rows, ld * type_bytes(type), k * type_bytes(type)};
+}
+// Two buffers whose rows share memory.  Rows of one pitch may lie between each other's (two halves of a
+// buffer's rows).
+static bool meet(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
+  if (a.p + (a.rows - 1) * a.pitch + a.width <= b.p || b.p + (b.rows - 1) * b.pitch + b.width <= a.p) return false;
+  if (a.pitch != b.pitch) return true;
+  const int64_t d = ((b.p - a.p) % a.pitch + a.pitch) % a.pitch;
+  return d < a.width || a.pitch - d < b.width;
+}
+static int check_apart(const char* fn, const char* out, const Span& o, const char* in, const Span& i) {
+  if (meet(o, i)) return set_error(IQ4_E_ARG, "%s: %s overlaps %s", fn, out, in);
+  return IQ4_OK;
+}
+
 static int check_slot_lists(const char* fn, const int32_t* slot_row, const float* w, const float* dw) {
   if (!slot_row) return set_error(IQ4_E_ARG, "%s: null pointer (slot_row)", fn);
   if (!aligned(slot_row, 4) || !aligned(w, 4) || !aligned(dw, 4))
@@ -800,6 +823,9 @@ int iq4_moe_dispatch(const void* x, int32_t x_dtype, int64_t ldx, int64_t n_tok,
   if (int e = check_any(fn, "x", x, x_dtype, hidden, ldx)) return e;
   if (int e = check_any(fn, "rows", rows, rows_dtype, hidden, ldr)) return e;
   if (int e = check_slot_lists(fn, slot_row, w, nullptr)) return e;
+  if (int e = check_apart(fn, "rows", span(rows, n_rows, hidden, ldr, rows_dtype), "x",
+                          span(x, n_tok, hidden, ldx, x_dtype)))
+    return e;
   SlotArgs a{};
   a.slot_row = slot_row;
   a.w = w;
@@ -830,6 +856,10 @@ int iq4_moe_combine(const void* rows, int32_t rows_dtype, int64_t ldr, int64_t n
     if (add == out && lda != ldo) return set_error(IQ4_E_ARG, "%s: out stored over add needs the same row stride", fn);
   }
   if (int e = check_slot_lists(fn, slot_row, w, nullptr)) return e;
+  const Span o = span(out, n_tok, hidden, ldo, out_dtype);
+  if (add != out)
+    if (int e = check_apart(fn, "out", o, "add", span(add, n_tok, hidden, lda, out_dtype))) return e;
+  if (int e = check_apart(fn, "out", o, "rows", span(rows, n_rows, hidden, ldr, rows_dtype))) return e;
   SlotArgs a{};
   a.slot_row = slot_row;
   a.w = w;
@@ -860,6 +890,10 @@ int iq4_moe_combine_grad(const void* dout, int32_t dout_dtype, int64_t ldd, cons
   if (n_rows > 0 && drows)
     if (int e = check_any(fn, "drows", drows, rows_dtype, hidden, ldg)) return e;
   if (int e = check_slot_lists(fn, slot_row, w, dw)) return e;
+  const Span o = span(drows, n_rows, hidden, ldg, rows_dtype);
+  if (int e = check_apart(fn, "drows", o, "dout", span(dout, n_tok, hidden, ldd, dout_dtype))) return e;
+  if (dw)
+    if (int e = check_apart(fn, "drows", o, "rows", span(rows, n_rows, hidden, ldr, rows_dtype))) return e;
   SlotArgs a{};
   a.slot_row = slot_row;
   a.w = w;
@@ -904,6 +938,11 @@ int iq4_swiglu(const void* g, int64_t ldg, const void* u, int64_t ldu, int32_t d
     if (int e = check_any(fn, "y", y, y_dtype, k, ldy)) return e;
   if (codes)
     if (int e = check_rows(fn, fmt, k, codes, ldq, scales, lds)) return e;
+  if (y) {
+    const Span o = span(y, m, k, ldy, y_dtype);
+    if (int e = check_apart(fn, "y", o, "g", span(g, m, k, ldg, dtype))) return e;
+    if (int e = check_apart(fn, "y", o, "u", span(u, m, k, ldu, dtype))) return e;
+  }
   SwigluArgs a{};
   a.g = g;
   a.u = u;
@@ -931,6 +970,14 @@ int iq4_swiglu_grad(const void* dh, int32_t dh_dtype, int64_t lddh, const void* 
   if (int e = check_any(fn, "u", u, dtype, k, ldu)) return e;
   if (int e = check_any(fn, "dg", dg, dtype, k, lddg)) return e;
   if (int e = check_any(fn, "du", du, dtype, k, lddu)) return e;
+  const Span os[2] = {span(dg, m, k, lddg, dtype), span(du, m, k, lddu, dtype)};
+  const char* names[2] = {"dg", "du"};
+  for (int i = 0; i < 2; ++i) {
+    if (int e = check_apart(fn, names[i], os[i], "dh", span(dh, m, k, lddh, dh_dtype))) return e;
+    if (int e = check_apart(fn, names[i], os[i], "g", span(g, m, k, ldg, dtype))) return e;
+    if (int e = check_apart(fn, names[i], os[i], "u", span(u, m, k, ldu, dtype))) return e;
+  }
+  if (int e = check_apart(fn, "dg", os[0], "du", os[1])) return e;
   SwigluGradArgs a{};
   a.dh = dh;
   a.g = g;

@@ -15,8 +15,8 @@
 //               minus infinity): a result that is not finite is made again, one by one, without this.
 //   binary32 X  two binary16 numbers, the value rounded to eleven bits and what is left, rounded
 //               likewise; a wave has a slice of k, and there a row's values are multiplied by the power
-//               of two that brings the largest to 2^14 .. 2^15, and its sums divided by it.  Within half
-//               a step of binary32 (2^-24) of the value, or 2^-40 of the slice's largest.  Each of
+//               of two that brings the largest to 2^14 .. 2^15, and its sums divided by it.  Within 2^-23
+//               of the value (a tie of what is left), or 2^-39 of the slice's largest (half a step of the smallest).  Each of
 //               the two is a row of the operand; their sums are joined before they are divided.
 //
 // Operands of v_mfma_f32_16x16x32 (lane l = 16 g + c): the activations are the first one, rows by c;

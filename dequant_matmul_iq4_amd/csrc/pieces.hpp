@@ -1,7 +1,8 @@
 // pieces.hpp -- rows of floats of any length and element alignment, read and written in
 // pieces of P consecutive elements a lane.  A whole piece is one wide access (the device
-// takes them at any element's address); the last piece of a row that is no multiple of P
-// goes element by element.
+// takes them at any element's address).  The last piece of a row that is no multiple of P begins
+// earlier, over elements of the piece before it; only a row shorter than a piece goes element by
+// element.
 #pragma once
 #include "common.hpp"
 #include "rows.hpp"
@@ -9,6 +10,10 @@
 namespace iq4 {
 
 inline int type_bytes(int t) { return t == kF32 ? 4 : 2; }
+
+// Rows of more bytes than this are read and written past the L2 (non-temporal): each is used once, and
+// they would only push each other out of it and of the memory-side cache behind it.
+constexpr int64_t kStreamBytes = 64 << 20;
 
 #ifdef __HIPCC__
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
@@ -34,6 +39,19 @@ template <bool STREAM>
 __device__ __forceinline__ void put8(void* p, u32x2 v) {
   if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<u32x2_any*>(p));
   else *static_cast<u32x2_any*>(p) = v;
+}
+
+// Piece q of a row of n elements: the first element, how many there are (P unless the row is shorter), and
+// how many of them are the piece's before it too.
+struct Piece {
+  int64_t at;
+  int left, twice;
+};
+template <int P>
+__device__ __forceinline__ Piece piece_of(uint32_t q, int64_t n) {
+  const int64_t at = (int64_t)q * P;
+  const int over = (int)max<int64_t>(at + P - n, 0);
+  return over == 0 || n < P ? Piece{at, P - over, 0} : Piece{at - over, P, over};
 }
 
 // Elements at .. at + P - 1 of a row, `left` of which exist (the others are zero), as binary32.

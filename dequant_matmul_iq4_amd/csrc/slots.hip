@@ -25,89 +25,259 @@ __device__ __forceinline__ float scaled(float w, float v) {
   return p;
 }
 
-template <int TX, int TR>
+// What a token's slots j0 .. j0 + N - 1 point at: row numbers (-1: none) and weights.
+template <int N>
+struct Slots {
+  int r[N];
+  float w[N];
+};
+template <int N>
+__device__ __forceinline__ Slots<N> slots_of(const SlotArgs& a, int64_t t, int j0) {
+  Slots<N> s;
+  const int64_t p = t * a.top_k + j0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) s.r[i] = j0 + i < a.top_k ? a.slot_row[p + i] : -1;
+#pragma unroll
+  for (int i = 0; i < N; ++i) s.w[i] = a.w && j0 + i < a.top_k ? a.w[p + i] : 1.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if ((uint32_t)s.r[i] >= a.n_rows) s.r[i] = -1;
+  return s;
+}
+// The same where all lanes have one token: lane j loads slot j's, and they are read from there into
+// scalar registers, as are the addresses made of them.
+struct TokenSlots {
+  int r;
+  float w;
+  __device__ __forceinline__ TokenSlots(const SlotArgs& a, int64_t t) : r(-1), w(1.0f) {
+    const int lane = threadIdx.x & 63;
+    if (lane < a.top_k) {
+      r = a.slot_row[t * a.top_k + lane];
+      if (a.w) w = a.w[t * a.top_k + lane];
+    }
+    if ((uint32_t)r >= a.n_rows) r = -1;
+  }
+  __device__ __forceinline__ int row(int j) const { return __builtin_amdgcn_readlane(r, j); }
+  __device__ __forceinline__ float weight(int j) const {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), j));
+  }
+};
+template <int T>
+__device__ __forceinline__ const char* row_of(const void* rows, int64_t r, int64_t ld) {
+  return static_cast<const char*>(rows) + r * ld * (T == kF32 ? 4 : 2);
+}
+template <int T>
+__device__ __forceinline__ char* row_of(void* rows, int64_t r, int64_t ld) {
+  return static_cast<char*>(rows) + r * ld * (T == kF32 ? 4 : 2);
+}
+
+template <int T>
+__device__ __forceinline__ void store_one(char* row, int64_t at, float v) {
+  if constexpr (T == kF32) reinterpret_cast<float*>(row)[at] = v;
+  else reinterpret_cast<uint16_t*>(row)[at] = (uint16_t)pack2<T>(v, 0.f);
+}
+
+// A lane per piece, whatever token it belongs to; four slots at a time.  The written rows bound it: 3256
+// tokens of 2048 numbers of 16 bits to 8 rows each 22 us (5.4 TB/s), of 2047 28, of float32 42.
+template <int TX, int TR, bool STREAM>
 __global__ void __launch_bounds__(256) dispatch_kernel(SlotArgs a, uint32_t pieces) {
   constexpr int P = kPiece<TX, TR>;
   const uint32_t i = blockIdx.x * 256 + threadIdx.x;
   const uint32_t t = i / pieces;
   if (t >= a.n_tok) return;
-  const int64_t at = (int64_t)(i - t * pieces) * P;
-  const int left = (int)min<int64_t>(a.hidden - at, P);
+  const Piece c = piece_of<P>(i - t * pieces, a.hidden);
   float v[P];
-  load_piece<TX, P>(static_cast<const char*>(a.tok) + t * a.ldt * (TX == kF32 ? 4 : 2), at, left, v);
-  for (int j = 0; j < a.top_k; ++j) {
-    const int64_t p = (int64_t)t * a.top_k + j;
-    const int r = a.slot_row[p];
-    if ((uint32_t)r >= a.n_rows) continue;
-    float o[P];
-    const float w = a.w ? a.w[p] : 1.0f;
+  load_piece<TX, P>(row_of<TX>(a.tok, t, a.ldt), c.at, c.left, v);
+  for (int j0 = 0; j0 < a.top_k; j0 += 4) {
+    const Slots<4> s = slots_of<4>(a, t, j0);
 #pragma unroll
-    for (int e = 0; e < P; ++e) o[e] = a.w ? scaled(w, v[e]) : v[e];
-    store_piece<TR, P>(static_cast<char*>(a.out) + r * a.ldo * (TR == kF32 ? 4 : 2), at, left, o);
+    for (int j = 0; j < 4; ++j) {
+      if (s.r[j] < 0) continue;
+      float o[P];
+#pragma unroll
+      for (int e = 0; e < P; ++e) o[e] = a.w ? scaled(s.w[j], v[e]) : v[e];
+      // (what two pieces have is written twice, the same)
+      store_piece<TR, P, STREAM>(row_of<TR>(a.out, s.r[j], a.ldo), c.at, c.left, o);
+    }
   }
 }
 
-template <int TR, int TO>
+// The same way; the rows of four slots are under way at once.  The rows read bound it: 3256 tokens of
+// 2048, eight rows of 16 bits each, 26 us (4.6 TB/s), of 2047 29, of float32 44; four tokens 3.3.  (Eight, 16-bit rows: the prompt's 31.9 us
+// for 26.1; a workgroup per token, its slots in scalar registers: 28.2, and 52 for rows of 700.)
+template <int TR, int TO, bool STREAM>
 __global__ void __launch_bounds__(256) combine_rows_kernel(SlotArgs a, uint32_t pieces) {
   constexpr int P = kPiece<TR, TO>;
   const uint32_t i = blockIdx.x * 256 + threadIdx.x;
   const uint32_t t = i / pieces;
   if (t >= a.n_tok) return;
-  const int64_t at = (int64_t)(i - t * pieces) * P;
-  const int left = (int)min<int64_t>(a.hidden - at, P);
+  const Piece c = piece_of<P>(i - t * pieces, a.hidden);
   float acc[P];
 #pragma unroll
   for (int e = 0; e < P; ++e) acc[e] = 0.f;
-  for (int j = 0; j < a.top_k; ++j) {
-    const int64_t p = (int64_t)t * a.top_k + j;
-    const int r = a.slot_row[p];
-    if ((uint32_t)r >= a.n_rows) continue;
-    const float w = a.w ? a.w[p] : 1.0f;
-    float v[P];
-    load_piece<TR, P>(static_cast<const char*>(a.rows) + r * a.ldr * (TR == kF32 ? 4 : 2), at, left, v);
+  for (int j0 = 0; j0 < a.top_k; j0 += 4) {
+    const Slots<4> s = slots_of<4>(a, t, j0);
+    float v[4][P];
 #pragma unroll
-    for (int e = 0; e < P; ++e) acc[e] = acc[e] + w * v[e];
+    for (int j = 0; j < 4; ++j)
+      if (s.r[j] >= 0) load_piece<TR, P, STREAM>(row_of<TR>(a.rows, s.r[j], a.ldr), c.at, c.left, v[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (s.r[j] >= 0) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) acc[e] = acc[e] + s.w[j] * v[j][e];
+      }
   }
   if (a.tok) {
     float v[P];
-    load_piece<TO, P>(static_cast<const char*>(a.tok) + t * a.ldt * (TO == kF32 ? 4 : 2), at, left, v);
+    load_piece<TO, P>(row_of<TO>(a.tok, t, a.ldt), c.at, c.left, v);
 #pragma unroll
     for (int e = 0; e < P; ++e) acc[e] = acc[e] + v[e];
   }
-  store_piece<TO, P>(static_cast<char*>(a.out) + t * a.ldo * (TO == kF32 ? 4 : 2), at, left, acc);
+  char* out = row_of<TO>(a.out, t, a.ldo);
+  if (c.twice == 0) {
+    store_piece<TO, P>(out, c.at, c.left, acc);
+  } else {
+    // out may be the addend: what the piece before has it may have stored already, and the sum here is
+    // then wrong; only the others are stored
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      if (e >= c.twice) store_one<TO>(out, c.at + e, acc[e]);
+    }
+  }
 }
 
-// One wave per token.
-template <int TD, int TR>
-__global__ void __launch_bounds__(64) combine_grad_kernel(SlotArgs a, uint32_t pieces) {
+// The wave's sum in every lane: within 16 lanes by DPP, across them by two exchanges.
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+  return __int_as_float(lane_move<CTRL>(__float_as_int(v)));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += moved<0xB1>(v);   // lane ^ 1
+  v += moved<0x4E>(v);   // lane ^ 2
+  v += moved<0x141>(v);  // half rows mirrored
+  v += moved<0x140>(v);  // rows mirrored
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// (Rows both read and written bound it: 3256 tokens of 2048, eight rows of 16 bits each, 47 us, 4.8 TB/s.)
+// A workgroup of WAVES per token: a lane takes every WAVES * 64th piece of the row, its part of dO
+// from memory once and the rows of eight slots at once; the slots' dots are summed over the
+// lanes in a fixed order.
+template <int TD, int TR, int WAVES, bool STREAM>
+__global__ void __launch_bounds__(WAVES * 64) combine_grad_kernel(SlotArgs a, uint32_t pieces) {
   constexpr int P = kPiece<TD, TR>;
+  __shared__ float part[WAVES][16];
   const int64_t t = blockIdx.x;
-  for (int j = 0; j < a.top_k; ++j) {
-    const int64_t p = t * a.top_k + j;
-    const int r = a.slot_row[p];
-    float dot = 0.f;
-    if ((uint32_t)r < a.n_rows) {
-      const float w = a.w ? a.w[p] : 1.0f;
-      for (uint32_t q = threadIdx.x; q < pieces; q += 64) {
-        const int64_t at = (int64_t)q * P;
-        const int left = (int)min<int64_t>(a.hidden - at, P);
-        float d[P], v[P], o[P];
-        load_piece<TD, P>(static_cast<const char*>(a.tok) + t * a.ldt * (TD == kF32 ? 4 : 2), at, left, d);
-        if (a.dw) {
-          load_piece<TR, P>(static_cast<const char*>(a.rows) + r * a.ldr * (TR == kF32 ? 4 : 2), at, left, v);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const TokenSlots s(a, t);
+  const char* dout = row_of<TD>(a.tok, t, a.ldt);
+  for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+    float dot[8];
 #pragma unroll
-          for (int e = 0; e < P; ++e) dot = fmaf(d[e], v[e], dot);
+    for (int j = 0; j < 8; ++j) dot[j] = 0.f;
+    for (uint32_t q = threadIdx.x; q < pieces; q += WAVES * 64) {
+      const Piece c = piece_of<P>(q, a.hidden);
+      float d[P], v[8][P];
+      load_piece<TD, P>(dout, c.at, c.left, d);
+      if (a.dw) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = s.row(j0 + j);
+          if (r >= 0) load_piece<TR, P, STREAM>(row_of<TR>(a.rows, r, a.ldr), c.at, c.left, v[j]);
         }
-        if (a.out) {
+      }
+      if (a.out) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = s.row(j0 + j);
+          if (r < 0) continue;
+          const float w = s.weight(j0 + j);
+          float o[P];
 #pragma unroll
           for (int e = 0; e < P; ++e) o[e] = scaled(w, d[e]);
-          store_piece<TR, P>(static_cast<char*>(a.out) + r * a.ldo * (TR == kF32 ? 4 : 2), at, left, o);
+          // (what two pieces have is written twice, the same)
+          store_piece<TR, P, STREAM>(row_of<TR>(a.out, r, a.ldo), c.at, c.left, o);
         }
+      }
+      if (a.dw) {
+        if (c.twice) {  // and counted once
+#pragma unroll
+          for (int e = 0; e < P; ++e) d[e] = e < c.twice ? 0.f : d[e];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (s.row(j0 + j) >= 0) {
+#pragma unroll
+            for (int e = 0; e < P; ++e) dot[j] = fmaf(d[e], v[j][e], dot[j]);
+          }
       }
     }
     if (a.dw) {
-      for (int m = 32; m > 0; m >>= 1) dot += __shfl_xor(dot, m);
-      if (threadIdx.x == 0) a.dw[p] = dot;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float sum = wave_sum(dot[j]);
+        if (lane == 0) part[wave][j0 + j] = sum;
+      }
+    }
+  }
+  if (!a.dw) return;
+  if constexpr (WAVES > 1) __syncthreads();
+  else {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+  if ((int)threadIdx.x < a.top_k) {
+    float s = part[0][threadIdx.x];
+#pragma unroll
+    for (int v = 1; v < WAVES; ++v) s = s + part[v][threadIdx.x];
+    a.dw[t * a.top_k + threadIdx.x] = s;
+  }
+}
+
+// Rows of at most 16 pieces: sixteen lanes a token (10000 tokens of 128, two rows each: 6.2 us; a wave a
+// token 14).
+template <int TD, int TR>
+__global__ void __launch_bounds__(256) combine_grad_short_kernel(SlotArgs a, uint32_t pieces) {
+  constexpr int P = kPiece<TD, TR>;
+  const int64_t t = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const uint32_t q = threadIdx.x & 15;
+  const bool live = t < a.n_tok && q < pieces;  // (the others take part in the sums)
+  const Piece c = piece_of<P>(live ? q : 0, a.hidden);
+  float d[P], once[P];
+#pragma unroll
+  for (int e = 0; e < P; ++e) d[e] = 0.f;
+  if (live) load_piece<TD, P>(row_of<TD>(a.tok, t, a.ldt), c.at, c.left, d);
+#pragma unroll
+  for (int e = 0; e < P; ++e) once[e] = e < c.twice ? 0.f : d[e];
+  for (int j0 = 0; j0 < a.top_k; j0 += 4) {
+    Slots<4> s = slots_of<4>(a, t < a.n_tok ? t : 0, j0);
+    float v[4][P];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (live && a.dw && s.r[j] >= 0) load_piece<TR, P>(row_of<TR>(a.rows, s.r[j], a.ldr), c.at, c.left, v[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float dot = 0.f;
+      if (live && s.r[j] >= 0) {
+        if (a.out) {
+          float o[P];
+#pragma unroll
+          for (int e = 0; e < P; ++e) o[e] = scaled(s.w[j], d[e]);
+          store_piece<TR, P>(row_of<TR>(a.out, s.r[j], a.ldo), c.at, c.left, o);
+        }
+        if (a.dw) {
+#pragma unroll
+          for (int e = 0; e < P; ++e) dot = fmaf(once[e], v[j][e], dot);
+        }
+      }
+      dot += moved<0xB1>(dot);
+      dot += moved<0x4E>(dot);
+      dot += moved<0x141>(dot);
+      dot += moved<0x140>(dot);
+      if (a.dw && q == 0 && t < a.n_tok && j0 + j < a.top_k) a.dw[t * a.top_k + j0 + j] = dot;
     }
   }
 }
@@ -149,11 +319,21 @@ static uint32_t pieces_of(int64_t hidden, int t1, int t2) {
   return (uint32_t)((hidden + p - 1) / p);
 }
 
+// The experts' rows pass the caches where they are too many for them (kStreamBytes): each is used once.
+// The prompt's dispatch 22.0 us for 23.9, its gradient 47 for 54; 42 for 47 of float32 rows.
+static bool streams(const SlotArgs& a, int rows_type) {
+  return a.n_tok * a.top_k * a.hidden * type_bytes(rows_type) > kStreamBytes;
+}
+
 int launch_dispatch(const SlotArgs& a, int x_type, int rows_type, hipStream_t s) {
   const uint32_t pieces = pieces_of(a.hidden, x_type, rows_type);
+  // (written rows that do not begin on 16 bytes leave in parts: 2047 numbers of 16 bits 31 us for 27)
+  const bool st = streams(a, rows_type) && aligned(a.out, 16) && a.ldo * type_bytes(rows_type) % 16 == 0;
   return by_tokens(a, pieces, x_type, rows_type, false, [&](const SlotArgs& b) {
     const dim3 grid((unsigned)((b.n_tok * pieces + 255) / 256));
-#define IQ4_CALL(T1, T2) hipLaunchKernelGGL((dispatch_kernel<T1, T2>), grid, dim3(256), 0, s, b, pieces)
+#define IQ4_CALL(T1, T2)                                                                                 \
+  if (st) hipLaunchKernelGGL((dispatch_kernel<T1, T2, true>), grid, dim3(256), 0, s, b, pieces);         \
+  else hipLaunchKernelGGL((dispatch_kernel<T1, T2, false>), grid, dim3(256), 0, s, b, pieces)
     IQ4_TYPES(x_type, rows_type, IQ4_CALL)
 #undef IQ4_CALL
     return check_launch("dispatch_kernel");
@@ -162,24 +342,47 @@ int launch_dispatch(const SlotArgs& a, int x_type, int rows_type, hipStream_t s)
 
 int launch_combine_rows(const SlotArgs& a, int rows_type, int out_type, hipStream_t s) {
   const uint32_t pieces = pieces_of(a.hidden, rows_type, out_type);
+  const bool st = streams(a, rows_type);
   return by_tokens(a, pieces, out_type, out_type, true, [&](const SlotArgs& b) {
     const dim3 grid((unsigned)((b.n_tok * pieces + 255) / 256));
-#define IQ4_CALL(T1, T2) hipLaunchKernelGGL((combine_rows_kernel<T1, T2>), grid, dim3(256), 0, s, b, pieces)
+#define IQ4_CALL(T1, T2)                                                                                 \
+  if (st) hipLaunchKernelGGL((combine_rows_kernel<T1, T2, true>), grid, dim3(256), 0, s, b, pieces);     \
+  else hipLaunchKernelGGL((combine_rows_kernel<T1, T2, false>), grid, dim3(256), 0, s, b, pieces)
     IQ4_TYPES(rows_type, out_type, IQ4_CALL)
 #undef IQ4_CALL
     return check_launch("combine_rows_kernel");
   });
 }
 
-int launch_combine_grad(const SlotArgs& a, int dout_type, int rows_type, hipStream_t s) {
-  const uint32_t pieces = pieces_of(a.hidden, dout_type, rows_type);
-  return by_tokens(a, 64, dout_type, rows_type, false, [&](const SlotArgs& b) {
+template <int WAVES, bool STREAM>
+static int launch_grad_waves(const SlotArgs& a, int dout_type, int rows_type, uint32_t pieces, hipStream_t s) {
+  return by_tokens(a, 64 * WAVES, dout_type, rows_type, false, [&](const SlotArgs& b) {
     const dim3 grid((unsigned)b.n_tok);
-#define IQ4_CALL(T1, T2) hipLaunchKernelGGL((combine_grad_kernel<T1, T2>), grid, dim3(64), 0, s, b, pieces)
+#define IQ4_CALL(T1, T2) \
+  hipLaunchKernelGGL((combine_grad_kernel<T1, T2, WAVES, STREAM>), grid, dim3(64 * WAVES), 0, s, b, pieces)
     IQ4_TYPES(dout_type, rows_type, IQ4_CALL)
 #undef IQ4_CALL
     return check_launch("combine_grad_kernel");
   });
+}
+
+int launch_combine_grad(const SlotArgs& a, int dout_type, int rows_type, hipStream_t s) {
+  const uint32_t pieces = pieces_of(a.hidden, dout_type, rows_type);
+  if (pieces <= 16)
+    return by_tokens(a, 16, dout_type, rows_type, false, [&](const SlotArgs& b) {
+      const dim3 grid((unsigned)((b.n_tok + 15) / 16));
+#define IQ4_CALL(T1, T2) hipLaunchKernelGGL((combine_grad_short_kernel<T1, T2>), grid, dim3(256), 0, s, b, pieces)
+      IQ4_TYPES(dout_type, rows_type, IQ4_CALL)
+#undef IQ4_CALL
+      return check_launch("combine_grad_kernel");
+    });
+  // waves a token: one a 64 pieces, up to four; sixteen where the tokens alone would not fill the device
+  // (four tokens of 8192: 7.9 us)
+  if (pieces <= 64) return launch_grad_waves<1, false>(a, dout_type, rows_type, pieces, s);
+  if (pieces > 256 && a.n_tok <= 256) return launch_grad_waves<16, false>(a, dout_type, rows_type, pieces, s);
+  if (pieces <= 128) return launch_grad_waves<2, false>(a, dout_type, rows_type, pieces, s);
+  return streams(a, rows_type) ? launch_grad_waves<4, true>(a, dout_type, rows_type, pieces, s)
+            : launch_grad_waves<4, false>(a, dout_type, rows_type, pieces, s);
 }
 
 }  // namespace iq4

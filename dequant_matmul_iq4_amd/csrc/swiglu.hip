@@ -18,25 +18,29 @@ __device__ __forceinline__ float sigmoid(float g) {
   return g < -88.f ? 0.f : s;
 }
 
+// Eight elements a lane, whatever row they belong to.  Memory bounds it: 26048 rows of 768 in binary16
+// 23 us with y alone (5.2 TB/s), 3 of the few rows of a step.  Past the caches it is no faster.
 template <int T>
 __global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a, uint32_t octs) {
   const uint32_t i = blockIdx.x * 256 + threadIdx.x;
   const uint32_t r = i / octs;
   const int oct = (int)(i - r * octs);
   const bool live = r < a.m;
-  const int left = (int)min<int64_t>(a.k - 8 * (int64_t)oct, 8);
+  // (a row that is quantised has whole pieces; behind them, up to its padding, there are none)
+  const Piece c = piece_of<8>(oct, a.k);
+  const bool here = live && 8 * (int64_t)oct < a.k;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (live && left > 0) {
+  if (here) {
     float g[8], u[8];
-    load_piece<T, 8>(static_cast<const char*>(a.g) + r * a.ldg * (T == kF32 ? 4 : 2), 8 * (int64_t)oct, left, g);
-    load_piece<T, 8>(static_cast<const char*>(a.u) + r * a.ldu * (T == kF32 ? 4 : 2), 8 * (int64_t)oct, left, u);
+    load_piece<T, 8>(static_cast<const char*>(a.g) + r * a.ldg * (T == kF32 ? 4 : 2), c.at, c.left, g);
+    load_piece<T, 8>(static_cast<const char*>(a.u) + r * a.ldu * (T == kF32 ? 4 : 2), c.at, c.left, u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = (g[e] * sigmoid(g[e])) * u[e];
     if (a.y) {
       char* y = static_cast<char*>(a.y) + r * a.ldy * (a.y_type == kF32 ? 4 : 2);
-      if (a.y_type == kF32) store_piece<kF32, 8>(y, 8 * (int64_t)oct, left, v);
-      else if (a.y_type == kF16) store_piece<kF16, 8>(y, 8 * (int64_t)oct, left, v);
-      else store_piece<kBF16, 8>(y, 8 * (int64_t)oct, left, v);
+      if (a.y_type == kF32) store_piece<kF32, 8>(y, c.at, c.left, v);
+      else if (a.y_type == kF16) store_piece<kF16, 8>(y, c.at, c.left, v);
+      else store_piece<kBF16, 8>(y, c.at, c.left, v);
     }
   }
   if (a.fmt < 0) return;
@@ -66,26 +70,27 @@ int launch_swiglu(const SwigluArgs& a0, int type, hipStream_t s) {
   return 0;
 }
 
-template <int TD, int T>
+// 16 bytes of the wider type a lane; five rows of memory a row, which bound it: 3256 rows of 14336 in
+// bfloat16 74 us (6.3 TB/s), 500 rows 12.
+template <int TD, int T, bool STREAM>
 __global__ void __launch_bounds__(256) swiglu_grad_kernel(SwigluGradArgs a, uint32_t pieces) {
   constexpr int P = (TD == kF32 || T == kF32) ? 4 : 8, kSize = T == kF32 ? 4 : 2;
   const uint32_t i = blockIdx.x * 256 + threadIdx.x;
   const uint32_t r = i / pieces;
   if (r >= a.m) return;
-  const int64_t at = (int64_t)(i - r * pieces) * P;
-  const int left = (int)min<int64_t>(a.k - at, P);
+  const Piece c = piece_of<P>(i - r * pieces, a.k);  // (what two pieces have is written twice, the same)
   float d[P], g[P], u[P], x[P], z[P];
-  load_piece<TD, P>(static_cast<const char*>(a.dh) + r * a.lddh * (TD == kF32 ? 4 : 2), at, left, d);
-  load_piece<T, P>(static_cast<const char*>(a.g) + r * a.ldg * kSize, at, left, g);
-  load_piece<T, P>(static_cast<const char*>(a.u) + r * a.ldu * kSize, at, left, u);
+  load_piece<TD, P, STREAM>(static_cast<const char*>(a.dh) + r * a.lddh * (TD == kF32 ? 4 : 2), c.at, c.left, d);
+  load_piece<T, P, STREAM>(static_cast<const char*>(a.g) + r * a.ldg * kSize, c.at, c.left, g);
+  load_piece<T, P, STREAM>(static_cast<const char*>(a.u) + r * a.ldu * kSize, c.at, c.left, u);
 #pragma unroll
   for (int e = 0; e < P; ++e) {
     const float s = sigmoid(g[e]);
     z[e] = d[e] * (g[e] * s);
     x[e] = (d[e] * u[e]) * (s * fmaf(g[e], 1.0f - s, 1.0f));
   }
-  store_piece<T, P>(static_cast<char*>(a.dg) + r * a.lddg * kSize, at, left, x);
-  store_piece<T, P>(static_cast<char*>(a.du) + r * a.lddu * kSize, at, left, z);
+  store_piece<T, P, STREAM>(static_cast<char*>(a.dg) + r * a.lddg * kSize, c.at, c.left, x);
+  store_piece<T, P, STREAM>(static_cast<char*>(a.du) + r * a.lddu * kSize, c.at, c.left, z);
 }
 
 int launch_swiglu_grad(const SwigluGradArgs& a0, int dh_type, int type, hipStream_t s) {
@@ -93,19 +98,28 @@ int launch_swiglu_grad(const SwigluGradArgs& a0, int dh_type, int type, hipStrea
   const int p = (dh_type == kF32 || type == kF32) ? 4 : 8;
   const uint32_t pieces = (uint32_t)((a.k + p - 1) / p);
   const int64_t most = ((int64_t)1 << 31) / pieces;
+  // (3256 rows of 14336 in bfloat16 74 us for 82; written rows off 16 bytes would leave in parts)
+  const bool st = a.m * a.k * type_bytes(type) > kStreamBytes && aligned(a.dg, 16) && aligned(a.du, 16) &&
+                  ((a.lddg | a.lddu) * type_bytes(type)) % 16 == 0;
   for (int64_t left = a0.m; left > 0; left -= a.m) {
     a.m = left < most ? left : most;
     const dim3 grid((unsigned)((a.m * pieces + 255) / 256));
-#define IQ4_GRAD(TD)                                                                                              \
-  {                                                                                                               \
-    if (type == kF32) hipLaunchKernelGGL((swiglu_grad_kernel<TD, kF32>), grid, dim3(256), 0, s, a, pieces);       \
-    else if (type == kF16) hipLaunchKernelGGL((swiglu_grad_kernel<TD, kF16>), grid, dim3(256), 0, s, a, pieces);  \
-    else hipLaunchKernelGGL((swiglu_grad_kernel<TD, kBF16>), grid, dim3(256), 0, s, a, pieces);                   \
+#define IQ4_GRAD2(TD, T)                                                                                        \
+  {                                                                                                             \
+    if (st) hipLaunchKernelGGL((swiglu_grad_kernel<TD, T, true>), grid, dim3(256), 0, s, a, pieces);            \
+    else hipLaunchKernelGGL((swiglu_grad_kernel<TD, T, false>), grid, dim3(256), 0, s, a, pieces);              \
+  }
+#define IQ4_GRAD(TD)                                 \
+  {                                                  \
+    if (type == kF32) IQ4_GRAD2(TD, kF32)            \
+    else if (type == kF16) IQ4_GRAD2(TD, kF16)       \
+    else IQ4_GRAD2(TD, kBF16)                        \
   }
     if (dh_type == kF32) IQ4_GRAD(kF32)
     else if (dh_type == kF16) IQ4_GRAD(kF16)
     else IQ4_GRAD(kBF16)
 #undef IQ4_GRAD
+#undef IQ4_GRAD2
     if (int e = check_launch("swiglu_grad_kernel")) return e;
     a.dh = static_cast<const char*>(a.dh) + a.m * a.lddh * type_bytes(dh_type);
     a.g = static_cast<const char*>(a.g) + a.m * a.ldg * type_bytes(type);

@@ -557,7 +557,14 @@ int iq4_g4_pack_weights(const void* codes, int64_t ldq, const void* scales, int6
 /*
  * Product of few rows (a decode step's, a verify window's, a batch's) with such a matrix:
  *   Y[i][r] = sum over the groups G of row r of s[r][G] * sum_{k in G} (q[r][k] - z[r][G]) X[i][k],
- * i < m, r < n; the products exact, the sums in binary32, rounded once to y_dtype.
+ * i < m, r < n; summed in binary32 and rounded once to y_dtype.  The products enter the sums exactly, with
+ * two things to know:
+ *   x binary32   an element enters as two binary16 numbers after its row's slice of k (512 or 768 consecutive
+ *                elements, less where k is short) is scaled by a power of two: off by at most 2^-23 of
+ *                itself or 2^-39 of the largest magnitude in the slice, whichever is more.
+ *   x bfloat16   a group's sum is made as sum (8 + q / 2) X - (8 + z / 2) sum X (times 2 s): it rounds as sums of
+ *                terms of up to 31 |s X| do.
+ * An infinity or a NaN of X makes what it makes in the formula, in its own row's results alone.
  *   packed  iq4_g4_pack_weights, 256-byte aligned.   scale_dtype: IQ4_F16 or IQ4_BF16.
  *   zeros   != 0 if packed with zero points.
  *   x       [m][ldx], y [m][ldy] of their dtypes (IQ4_F32, IQ4_F16, IQ4_BF16), element aligned,
@@ -593,7 +600,7 @@ int iq4_g4_grouped_qmv(const void* packed, int32_t n_expert, int64_t n, int64_t 
 
 /*
  * R[slot_row[p]] = w[p] * X[t] (X[t] itself if w is NULL), the binary32 product rounded once to
- * rows_dtype.  Rows that no pair has are left as they were; a row that two pairs have gets either's.
+ * rows_dtype.  Rows that no pair has are left as they were; a row that two pairs have is unspecified.
  * This is also the gradient of iq4_moe_combine with respect to its rows.
  *   x  [n_tok][ldx] of x_dtype.  rows  [n_rows][ldr] of rows_dtype.  w  [n_tok][top_k] float32 or NULL.
  */
@@ -602,8 +609,8 @@ int iq4_moe_dispatch(const void* x, int32_t x_dtype, int64_t ldx, int64_t n_tok,
                      int32_t rows_dtype, int64_t ldr, void* stream);
 
 /*
- * O[t] = sum_j w[p] * R[slot_row[p]] (+ A[t]), added in binary32 in the order of j, A last, rounded
- * once to out_dtype; w NULL: 1.  A token without rows gets zero (or A).  Without w and A it is the
+ * O[t] = sum_j w[p] * R[slot_row[p]] (+ A[t]), in binary32 (a product rounded, then added) in the order of
+ * j, A last, rounded once to out_dtype; w NULL: 1.  Pairs may share a row.  A token without rows gets zero (or A).  Without w and A it is the
  * gradient of iq4_moe_dispatch.  Deterministic.
  *   rows  [n_rows][ldr] of rows_dtype (not read if n_rows = 0).   add  [n_tok][lda] of out_dtype, or NULL
  *   (a residual stream, a shared expert's rows).   out  [n_tok][ldo]; may be add itself (same stride).

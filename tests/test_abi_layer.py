@@ -77,6 +77,8 @@ def test_slots_refusals():
     assert disp(n=0, x=None, r=None) == iq4.IQ4_OK
     assert comb(o=None) == A and comb(ldo=63) == A and comb(lda=63) == A and comb(add=FAKE + 2) == AL and comb(o=far + 2) == AL
     assert comb(add=far, lda=128) == A  # over the addend, but not row for row
+    assert disp(r=FAKE + 64) == A and comb(o=FAKE + 64) == A and grad(dr=FAKE + 64) == A  # overlaps
+    assert comb(add=far + 128, o=far) == A and comb(add=far, lda=64, o=far, ldo=128) == A
     assert grad(dr=None, dw=None) == A and grad(ldg=63) == A and grad(dr=far + 1) == AL and grad(dw=far + 2) == AL
 
 
@@ -94,6 +96,9 @@ def test_swiglu_refusals():
     assert fwd(yt=3) == A and fwd(y=None, q=None) == A and fwd(ldy=127) == A and fwd(y=FAKE * 3 + 2) == AL and fwd(k=100) == U
     assert fwd(fmt=7) == A and fwd(d=None) == A and fwd(ldq=64) == A and fwd(q=FAKE + 8) == AL and fwd(fmt=MX4, lds=24) == AL
     assert fwd(fmt=Q8, lds=6) == A
+    assert fwd(y=FAKE) == A and fwd(g=FAKE * 3 + 64) == A and fwd(u=FAKE * 3 - 64) == A  # overlaps
+    assert grad(dg=FAKE) == A and grad(du=FAKE * 3) == A and grad(dh=FAKE * 4 + 64, dt=1) == A
+    assert grad(dg=FAKE * 3, lddg=256, du=FAKE * 3 + 256, lddu=256) == A  # halves of a buffer's rows, too narrow
     assert grad(dt=3) == A and grad(dh=None) == A and grad(dg=None) == A and grad(du=None) == A
     assert grad(lddh=127) == A and grad(lddg=127) == A and grad(lddu=127) == A and grad(dg=FAKE * 3 + 1) == AL
 
