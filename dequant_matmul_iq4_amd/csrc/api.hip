@@ -689,13 +689,38 @@ static int check_g4_args(const char* fn, int64_t n, int64_t k, int32_t group, in
   return IQ4_OK;
 }
 
-static int check_g4_buffers(const char* fn, const void* packed, int64_t n, int64_t k, const void* x, int32_t x_dtype,
-                            int64_t ldx, const void* y, int32_t y_dtype, int64_t ldy) {
+// Rows of `width` bytes every `pitch` bytes.
+struct Span {
+  const char* p;
+  int64_t rows, pitch, width;
+};
+static Span span(const void* p, int64_t rows, int64_t k, int64_t ld, int32_t type) {
+  return Span{static_cast<const char*>(p), rows, ld * type_bytes(type), k * type_bytes(type)};
+}
+// Two buffers whose rows share memory.  Rows of one pitch may lie between each other's (two halves of a
+// buffer's rows).
+static bool meet(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
+  if (a.p + (a.rows - 1) * a.pitch + a.width <= b.p || b.p + (b.rows - 1) * b.pitch + b.width <= a.p) return false;
+  if (a.pitch != b.pitch) return true;
+  const int64_t d = ((b.p - a.p) % a.pitch + a.pitch) % a.pitch;
+  return d < a.width || a.pitch - d < b.width;
+}
+static int check_apart(const char* fn, const char* out, const Span& o, const char* in, const Span& i) {
+  if (meet(o, i)) return set_error(IQ4_E_ARG, "%s: %s overlaps %s", fn, out, in);
+  return IQ4_OK;
+}
+
+static int check_g4_buffers(const char* fn, const void* packed, int64_t packed_bytes, int64_t n, int64_t k,
+                            const void* x, int32_t x_dtype, int64_t ldx, int64_t n_rows, const void* y, int32_t y_dtype,
+                            int64_t ldy, int64_t m) {
   if (ldx < k || ldy < n) return set_error(IQ4_E_ARG, "%s: ldx must be >= k and ldy >= n", fn);
   if (!packed || !x || !y) return set_error(IQ4_E_ARG, "%s: null pointer", fn);
   if (!aligned(packed, 256) || !elem_aligned(x, x_dtype) || !elem_aligned(y, y_dtype))
     return set_error(IQ4_E_ALIGN, "%s: packed must be 256-byte, x and y element aligned", fn);
-  return IQ4_OK;
+  const Span o = span(y, m, n, ldy, y_dtype);
+  if (int e = check_apart(fn, "y", o, "x", span(x, n_rows, k, ldx, x_dtype))) return e;
+  return check_apart(fn, "y", o, "packed", Span{static_cast<const char*>(packed), 1, packed_bytes, packed_bytes});
 }
 
 int iq4_g4_qmv(const void* packed, int64_t n, int64_t k, int32_t group, int32_t scale_dtype, int32_t zeros,
@@ -705,7 +730,8 @@ int iq4_g4_qmv(const void* packed, int64_t n, int64_t k, int32_t group, int32_t 
   clear_error();
   if (int e = check_g4_args(fn, n, k, group, scale_dtype, x_dtype, y_dtype, m)) return e;
   if (m == 0) return IQ4_OK;
-  if (int e = check_g4_buffers(fn, packed, n, k, x, x_dtype, ldx, y, y_dtype, ldy)) return e;
+  const int64_t bytes = g4_packed_bytes(n, k, group, zeros != 0);
+  if (int e = check_g4_buffers(fn, packed, bytes, n, k, x, x_dtype, ldx, m, y, y_dtype, ldy, m)) return e;
   G4Args a{};
   a.W = static_cast<const uint8_t*>(packed);
   a.n = n;
@@ -739,11 +765,13 @@ int iq4_g4_grouped_qmv(const void* packed, int32_t n_expert, int64_t n, int64_t 
   if (!offsets) return set_error(IQ4_E_ARG, "%s: null pointer", fn);
   if (!aligned(offsets, 4) || !aligned(pairs, 4))
     return set_error(IQ4_E_ALIGN, "%s: offsets and pairs must be 4-byte aligned", fn);
-  if (int e = check_g4_buffers(fn, packed, n, k, x, x_dtype, ldx, y, y_dtype, ldy)) return e;
+  const int64_t stride = g4_packed_bytes(n, k, group, zeros != 0);
+  if (int e = check_g4_buffers(fn, packed, stride * n_expert, n, k, x, x_dtype, ldx, n_rows, y, y_dtype, ldy, n_pairs))
+    return e;
   G4Args a{};
   a.W = static_cast<const uint8_t*>(packed);
   a.zeros = zeros != 0;
-  a.w_stride = g4_packed_bytes(n, k, group, a.zeros);
+  a.w_stride = stride;
   a.n = n;
   a.k = k;
   a.group = group;
@@ -781,28 +809,6 @@ static int check_any(const char* fn, const char* what, const void* p, int32_t ty
   if (ld < k) return set_error(IQ4_E_ARG, "%s: the row stride of %s must hold a row", fn, what);
   if (!p) return set_error(IQ4_E_ARG, "%s: null pointer (%s)", fn, what);
   if (!elem_aligned(p, type)) return set_error(IQ4_E_ALIGN, "%s: %s must be element aligned", fn, what);
-  return IQ4_OK;
-}
-
-// Rows of `width` bytes every `pitch` bytes.
-struct Span {
-  const char* p;
-  int64_t rows, pitch, width;
-};
-static Span span(const void* p, int64_t rows, int64_t k, int64_t ld, int32_t type) {
-  return Span{static_cast<const char*>(p), rows, ld * type_bytes(type), k * type_bytes(type)};
-}
-// Two buffers whose rows share memory.  Rows of one pitch may lie between each other's (two halves of a
-// buffer's rows).
-static bool meet(const Span& a, const Span& b) {
-  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
-  if (a.p + (a.rows - 1) * a.pitch + a.width <= b.p || b.p + (b.rows - 1) * b.pitch + b.width <= a.p) return false;
-  if (a.pitch != b.pitch) return true;
-  const int64_t d = ((b.p - a.p) % a.pitch + a.pitch) % a.pitch;
-  return d < a.width || a.pitch - d < b.width;
-}
-static int check_apart(const char* fn, const char* out, const Span& o, const char* in, const Span& i) {
-  if (meet(o, i)) return set_error(IQ4_E_ARG, "%s: %s overlaps %s", fn, out, in);
   return IQ4_OK;
 }
 

@@ -570,6 +570,7 @@ int iq4_g4_pack_weights(const void* codes, int64_t ldq, const void* scales, int6
  *   x       [m][ldx], y [m][ldy] of their dtypes (IQ4_F32, IQ4_F16, IQ4_BF16), element aligned,
  *           ldx >= k, ldy >= n; columns n .. ldy - 1 of y are left alone.
  *   m >= 0 (0: no-op); meant for up to some 64 rows, any number up to 2^21 is taken.  No workspace.
+ *   y overlaps neither x nor packed.
  * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED (group, k % 32, sizes).
  */
 int iq4_g4_qmv(const void* packed, int64_t n, int64_t k, int32_t group, int32_t scale_dtype, int32_t zeros,

@@ -48,6 +48,7 @@ def test_g4_product_refusals():
         assert f(g=48) == U and f(st=0) == A and f(st=3) == A and f(xt=3) == A and f(yt=-1) == A and f(ldx=127) == A and f(ldy=15) == A
         assert f(p=None) == A and f(x=None) == A and f(y=None) == A
         assert f(p=FAKE + 16) == AL and f(x=FAKE + 2) == AL and f(y=FAKE + 2) == AL and f(xt=1, x=FAKE + 1) == AL and f(yt=2, y=FAKE + 1) == AL
+        assert f(x=FAKE * 4, y=FAKE * 4) == A and f(p=FAKE * 4, x=FAKE * 8, y=FAKE * 4 + 256) == A  # overlaps
     assert dense(m=0, p=None, x=None, y=None) == iq4.IQ4_OK and grouped(m=0, p=None, off=None, y=None) == iq4.IQ4_OK
     assert grouped(e=0) == A and grouped(e=1025) == A and grouped(top=0) == A and grouped(off=None) == A
     assert grouped(off=FAKE + 2) == AL and grouped(pairs=FAKE + 1) == AL

@@ -8,7 +8,10 @@ Where the inputs are real, the bound is by the number of additions: a result is 
 products (and of each group's sum times its scale), and each addition is off by at most a whole
 step of the magnitudes' sum M (2^-23 M; a matrix instruction may truncate), each group's scaling
 by half a step: (k + 2 k / 32 + 64) 2^-23 M, and half a step of y's type of the result itself.
-An activation of binary32 enters as three parts, whose magnitudes sum to at most 1.01 of its own.
+An activation of binary32 enters as two parts (at most 1.001 of its own magnitude), which miss 2^-23 of it
+(half a step of what the first leaves, 2^-11 of the value at most) or, of a slice's smallest, 2^-39 of the
+slice's largest magnitude: 2^-23 M + 2^-39 max |x| sum |w|.  One of bfloat16 counts in M with the weights
+that the sums are made of: 2 |s| (8 + q / 2) in the products, 2 |s| (8 + z / 2) in what is taken off.
 """
 import numpy as np
 import pytest
@@ -137,7 +140,15 @@ def test_real_inputs(group, t):
             want, mags = oracle.g4_product(w, x), oracle.g4_product(abs(w), abs(x))
             y_t = "f32" if m != 7 else t
             got = product(pack(codes, s, z, group, scale), n, k, group, z, scale, x, t, y_t)
-            bound = (1.01 * (k + 2 * k / 32) + 64) * 2.0**-23 * mags + HALF_STEP[y_t] * abs(want) * (y_t != "f32")
+            own = 0
+            if t == "f32":
+                own = 2.0**-23 * mags + 2.0**-39 * abs(x).max(1, keepdims=True) * abs(w).sum(1)
+            if t == "bf16":
+                q = np.stack((codes & 15, codes >> 4), 2).reshape(n, k)
+                wide = lambda v: np.repeat(v, group, axis=1)  # noqa: E731
+                mags = oracle.g4_product(2 * abs(wide(s)) * (16 + q / 2 + (wide(z) / 2 if zeros else 4)), abs(x))
+            err = (1.001 * (k + 2 * k / 32) + 64) * 2.0**-23 * mags + own
+            bound = err + (HALF_STEP[y_t] * (abs(want) + err) if y_t != "f32" else 0)
             assert np.all(abs(got - want) <= bound)
             # what such a bound would hide, the norm of all errors shows: they are of either sign
             if y_t == "f32":
@@ -146,7 +157,7 @@ def test_real_inputs(group, t):
 
 def test_every_bit_of_an_activation_counts():
     """One activation a row that is not zero, at every place: its product with each code, 29 bits
-    of it at most, is off by the roundings of two additions of parts."""
+    of it at most, is off by what its two parts miss (2^-23) and the rounding of their sum (2^-24)."""
     note("g4: single activations over all of binary32")
     n, k, group = 16, 256, 32
     codes, s, z = weights(5, n, k, group, True, "f16", True)
