@@ -132,19 +132,22 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_raw_stream = None  # torch's lookup of a device's current stream as an integer
+# torch's lookups of the current device and of a device's current stream, as integers
+_device = _raw_stream = None
 
 
 def _stream(stream):
     if stream is None:
         # torch.cuda.current_stream() builds a Stream object (some 3 us, as long as a small
         # kernel); the integer alone is a tenth of that
-        global _raw_stream
-        import torch
+        global _device, _raw_stream
         if _raw_stream is None:
+            import torch
+            torch.cuda.current_device()  # initialises the device; the lookup below it does not
+            _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
             _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
                 lambda device: torch.cuda.current_stream(device).cuda_stream)
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
