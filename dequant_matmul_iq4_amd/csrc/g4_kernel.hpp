@@ -8,8 +8,8 @@
 //   binary16 X  q - z as a binary16 number, (1024 + q) - (1024 + z): the codes are or-ed into the
 //               bits of 1024, two at a time.  11 operations for eight weights.
 //   bfloat16 X  no packed instruction makes q - z a bfloat16 number (19 operations from a dot
-//               product with (1, 0) and (0, 1)), so the weight is 8 + q / 2, or-ed into the bits of 8, and
-//               the group's sums of X, made once for all rows of W, are multiplied by -(8 + z / 2) and begin
+//               product with (1, 0) and (0, 1)), so the weight is 16 + q, or-ed into the bits of 16, and
+//               the group's sums of X, made once for all rows of W, are multiplied by -(16 + z) and begin
 //               d: 8 operations.  The sums are then some five times those of q - z, and so
 //               are their roundings, 2^-24 of them each.  An infinity leaves a NaN (infinity
 //               minus infinity): a result that is not finite is made again, one by one, without this.
@@ -27,6 +27,10 @@
 #include "g4.hpp"
 #include "pieces.hpp"
 
+#include <math.h>
+
+#include <type_traits>
+
 namespace iq4 {
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
@@ -37,7 +41,7 @@ struct G4Consts {
 };
 template <bool BRAIN>
 __device__ __forceinline__ G4Consts g4_consts() {
-  G4Consts k = {BRAIN ? 0x00780078u : 0x000F000Fu, 0x00F000F0u, BRAIN ? 0x41004100u : 0x64006400u};
+  G4Consts k = {BRAIN ? 0x00780078u : 0x000F000Fu, 0x00F000F0u, BRAIN ? 0x41804180u : 0x64006400u};
   asm("" : "+s"(k.lo), "+s"(k.hi), "+v"(k.top));  // opaque: not literals
   return k;
 }
@@ -60,7 +64,7 @@ __device__ __forceinline__ u32x4 g4_half(const G4Consts& k, uint32_t w, f16x2 bi
   }
   return r;
 }
-// 8 + q / 2 in bfloat16.
+// 16 + q in bfloat16.
 __device__ __forceinline__ u32x4 g4_brain(const G4Consts& k, uint32_t w) {
   return u32x4{((w << 3) & k.lo) | k.top, ((w >> 1) & k.lo) | k.top, ((w >> 5) & k.lo) | k.top, ((w >> 9) & k.lo) | k.top};
 }
@@ -175,7 +179,9 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
   };
   const int64_t tiles_n = (int64_t)rt_n * kt_n;
   const uint8_t* S = W + tiles_n * kG4TileBytes;
-  const uint8_t* Z = S + tiles_n * (16 * kSets * 2);
+  // (without zero points bytes of the scales are loaded, and not looked at: a branch around the load would
+  // make every wait one for all loads)
+  const uint8_t* Z = a.zeros ? S + tiles_n * (16 * kSets * 2) : S;
   auto load_w = [&](int64_t tile, WTile& o) {  // tile: rt * kt_n + kt, the same in all lanes
     o.q = *reinterpret_cast<const u32x4*>(W + tile * kG4TileBytes + (uint32_t)(lane * 16));
     const uint8_t* s = S + tile * (16 * kSets * 2) + (uint32_t)(c * kSets * 2);
@@ -187,13 +193,10 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
     } else {
       o.s[0] = *reinterpret_cast<const uint16_t*>(s);
     }
-    o.z = 0x08080808u;
-    if (a.zeros) {
-      const uint8_t* z = Z + tile * (16 * kSets) + (uint32_t)(c * kSets);
-      if constexpr (G == 32) o.z = *reinterpret_cast<const uint32_t*>(z);
-      else if constexpr (G == 64) o.z = *reinterpret_cast<const uint16_t*>(z);
-      else o.z = *z;
-    }
+    const uint8_t* z = Z + tile * (16 * kSets) + (uint32_t)(c * kSets);
+    if constexpr (G == 32) o.z = *reinterpret_cast<const uint32_t*>(z);
+    else if constexpr (G == 64) o.z = *reinterpret_cast<const uint16_t*>(z);
+    else o.z = *z;
   };
   // A slice's code tiles [base, base + SX).  Where the slice would pass the last code tile it begins
   // earlier, and the tiles that are not its own (below `own`) get activations of zero.
@@ -201,6 +204,8 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
     own = (chunk * KS + slice) * SX;
     base = min(own, kt_n - SX);
   };
+  int base, own;
+  slice_of(0, base, own);
 
   // ---- the activations of a slice, as operands in registers ------------------------------------------
   // First as in memory, whole rows of a code tile: lane (g, c) has elements 8 c .. 8 c + 7 of row 4 p + g in
@@ -240,7 +245,24 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
         }
       }
   };
-  auto make_operands = [&]() {
+  // The same where the slice is whole and all four loads of each operand have rows: without a branch, the code tiles one
+  // after another, so that the first one's way through LDS begins while the others are under way (20.5
+  // us to 19.7 for 47 rows of 14336 x 4096).  (Rows past the last are that one again.)
+  auto load_whole = [&]() {
+    const char* x[NV][4];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        x[v][p] = static_cast<const char*>(a.x) + (x_row(16 * v + 4 * p + g) * a.ldx + 128 * (int64_t)base + 8 * c) * 2;
+#pragma unroll
+    for (int t = 0; t < SX; ++t)
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) xf[t][v][p] = get16<false>(x[v][p] + 256 * t);
+  };
+  auto make_operands = [&](auto all) {
     if constexpr (!f32) {
 #pragma unroll
       for (int t = 0; t < SX; ++t)
@@ -248,7 +270,7 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
         for (int v = 0; v < NV; ++v) {
 #pragma unroll
           for (int p = 0; p < 4; ++p)
-            if (16 * v + 4 * p < rows) *reinterpret_cast<u32x4*>(mine + (4 * p + g) * kG4StageRow + 16 * c) = xf[t][v][p];
+            if (all || 16 * v + 4 * p < rows) *reinterpret_cast<u32x4*>(mine + (4 * p + g) * kG4StageRow + 16 * c) = xf[t][v][p];
           wave_fence();
 #pragma unroll
           for (int s = 0; s < 4; ++s) xf[t][v][s] = *reinterpret_cast<const u32x4*>(mine + c * kG4StageRow + 64 * s + 16 * g);
@@ -336,6 +358,7 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
   const bool scale_f16 = a.scale_type == kF16;
   f32x4 acc[NV];
   auto multiply = [&](int t, const WTile& w) {
+    const uint32_t zeros = a.zeros ? w.z : 0x08080808u;
     float sc[kSets];
     if (scale_f16) {
 #pragma unroll
@@ -348,8 +371,7 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
     for (int b = 0; b < kSets; ++b) {
       f32x4 d[NV];
       if constexpr (XT == kBF16) {
-        const float corr = fmaf((float)((w.z >> (8 * b)) & 0xFFu), -0.5f, -8.0f);
-        sc[b] = sc[b] + sc[b];
+        const float corr = -16.0f - (float)((zeros >> (8 * b)) & 0xFFu);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           const f32x4 sum = *reinterpret_cast<const f32x4*>(sums + ((t * kSets + b) * NV + v) * 64 + 16 * g);
@@ -364,7 +386,7 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
         }
       } else {
         // 1024 + z twice: the zero point's byte under the byte 0x64
-        const uint32_t bias = __builtin_amdgcn_perm(0x64646464u, w.z, 0x04000400u + 0x00010001u * b);
+        const uint32_t bias = __builtin_amdgcn_perm(0x64646464u, zeros, 0x04000400u + 0x00010001u * b);
         const uint32_t bias16 = ((bias << 4) & 0x00F000F0u) | 0xD400D400u;  // -(64 + z) twice
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
@@ -411,22 +433,35 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
   };
 
   constexpr int kAhead = SX == 1 ? 4 : SX <= 3 ? 2 : 1;  // row tiles, some 4 KB a wave
-  int base, own;
-  slice_of(0, base, own);
-  load_x(0);
   WTile w[kAhead][SX];
+  auto first_w = [&]() {
+    // (one row tile without a branch, so that a wait for the activations is not one for these too: one row of
+    // 4096 x 4096 5.4 us for 5.9; with more, past the last it would load for nothing: 17.6 us for 16.8 for 32
+    // rows of 128 experts)
 #pragma unroll
-  for (int d = 0; d < kAhead; ++d)
-    if (first + d < last)
+    for (int d = 0; d < kAhead; ++d)
 #pragma unroll
-      for (int t = 0; t < SX; ++t) load_w((int64_t)(first + d) * kt_n + base + t, w[d][t]);
+      for (int t = 0; t < SX; ++t)
+        if (kAhead == 1 || first + d < last) load_w((int64_t)(first + d) * kt_n + base + t, w[d][t]);
+  };
+  // Many activations take longer than the weights, which then come first (47 rows of 14336 x 4096 22.0 us for
+  // 24.8; one row the other way round 9.7 for 10.4).
+  if (!f32 && rows > 16 * NV - 4 && base == own && (base + SX) * 128 <= K) {
+    first_w();
+    load_whole();
+    make_operands(std::true_type());
+  } else {
+    if constexpr (NV == 2) first_w();
+    load_x(0);
+    if constexpr (NV == 1) first_w();
+    make_operands(std::false_type());
+  }
   for (int b = first; b < last; b += plan.rb) {
     const int tiles = min(plan.rb, last - b);
     for (int chunk = 0; chunk < (CHUNKS ? plan.chunks : 1); ++chunk) {
-      const bool begin = b == first && chunk == 0;
-      if (begin || CHUNKS) {
-        if (!begin) load_x(chunk);
-        make_operands();
+      if (CHUNKS && (b != first || chunk != 0)) {
+        load_x(chunk);
+        make_operands(std::false_type());
       }
       for (int rb = 0; rb < tiles; rb += kAhead) {
         // the kAhead row tiles that come after these
@@ -490,15 +525,19 @@ static int launch_g4_kernel(const G4Args& a, G4Plan p, hipStream_t s) {
 template <int XT, int G>
 static int launch_g4_group(const G4Args& a, int nv, hipStream_t s) {
   const int bm = XT == kF32 ? 8 * nv : 16 * nv;
-  int64_t cols = (a.m + bm - 1) / bm;
-  // by expert: each expert's last tile may be partial
-  if (a.offsets) cols = a.m / bm + a.n_expert < a.m ? a.m / bm + a.n_expert : a.m;
+  int64_t cols = (a.m + bm - 1) / bm, busy = cols;
+  if (a.offsets) {
+    // each expert's last tile may be partial; as many have any if the rows choose at random
+    cols = a.m / bm + a.n_expert < a.m ? a.m / bm + a.n_expert : a.m;
+    busy = (int64_t)(a.n_expert * -expm1(-(double)a.m / a.n_expert)) + a.m / (a.n_expert * bm) * a.n_expert + 1;
+    if (busy > cols) busy = cols;
+  }
   const int64_t rt_n = g4_row_tiles(a.n);
   const int kt_n = g4_k_tiles(a.k), most = nv == 1 ? 6 : 4;
   int sx = (kt_n + 7) / 8;
   // short rows: two tiles a wave where there is work for twice the device's waves all the same (128 experts
   // of 2048 x 768, 488 rows: 23.4 us for 29.6)
-  if (sx == 1 && kt_n > 1 && rt_n * cols * ((kt_n + 1) / 2) >= 8192) sx = 2;
+  if (sx == 1 && kt_n > 1 && rt_n * busy * ((kt_n + 1) / 2) >= 8192) sx = 2;
   if (sx == 5) sx = 6;
   if (sx == 3 && nv == 2) sx = 4;
   const bool chunks = sx > most;
@@ -507,11 +546,13 @@ static int launch_g4_group(const G4Args& a, int nv, hipStream_t s) {
   p.ks = (kt_n + sx - 1) / sx;
   if (p.ks > 8) p.ks = 8;
   p.cols = (int)cols;
-  // row tiles a workgroup: as many as leave the device 8 waves a CU, 16 where their registers allow or
-  // the way of X is short.  14336 x 4096, 16 rows: 12.1 us with 8, 15.8 with 16; one row 9.5 and 8.9; 40000 x
-  // 4096, one row 18.9 and 17.0; 128 experts of 1536 x 2048, 32 rows: 16.0 with 32, 14.4 with 16.
-  const int64_t waves = nv * sx >= 4 && a.m > 4 ? 2048 : 4096;
-  int64_t per = (rt_n * cols * p.ks + waves - 1) / waves;
+  // row tiles a workgroup: as many as leave the device the 8 waves a CU that its registers hold, or 16 where
+  // a wave's activations are few or soon made operands.  14336 x 4096 in bfloat16, 16 rows: 12.4 us with 8,
+  // 16.4 with 16; one row 9.7 and 11.6, in binary16 11.1 and 10.0, four rows 11.2 and 12.2; 128 experts of 1536 x 2048, 32 rows: 16.0 with 32, 14.8 with 16.  One workgroup more than
+  // there is room for costs as much as all (128 experts of 2048 x 768, 488 rows: 21.5 us, 26.0 with one row
+  // tile less each), so by expert the columns that have rows count, not the grid's.
+  const int64_t waves = nv * sx >= 4 && (XT != kF16 || a.m > 1) ? 2048 : 4096;
+  const int64_t per = (rt_n * busy * p.ks + waves - 1) / waves;
   p.per = (int)(per > rt_n ? rt_n : per);
   p.rb = p.per < 4 ? p.per : 4;  // (a multiple of the row tiles that a wave loads ahead, or all)
   if (chunks) return nv == 1 ? launch_g4_kernel<XT, 1, 6, G, true>(a, p, s) : launch_g4_kernel<XT, 2, 4, G, true>(a, p, s);

@@ -562,8 +562,8 @@ int iq4_g4_pack_weights(const void* codes, int64_t ldq, const void* scales, int6
  *   x binary32   an element enters as two binary16 numbers after its row's slice of k (512 or 768 consecutive
  *                elements, less where k is short) is scaled by a power of two: off by at most 2^-23 of
  *                itself or 2^-39 of the largest magnitude in the slice, whichever is more.
- *   x bfloat16   a group's sum is made as sum (8 + q / 2) X - (8 + z / 2) sum X (times 2 s): it rounds as sums of
- *                terms of up to 31 |s X| do.
+ *   x bfloat16   a group's sum is made as sum (16 + q) X - (16 + z) sum X: it rounds as sums of terms of up to
+ *                31 |s X| do.
  * An infinity or a NaN of X makes what it makes in the formula, in its own row's results alone.
  *   packed  iq4_g4_pack_weights, 256-byte aligned.   scale_dtype: IQ4_F16 or IQ4_BF16.
  *   zeros   != 0 if packed with zero points.

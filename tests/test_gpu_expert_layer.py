@@ -75,7 +75,7 @@ class Layer:
         bound = (2.0**-20 + HALF_STEP[t]) * abs(want) + 2.0**-125 * abs(gu[:, :I] * gu[:, I:]) + small
         assert fine.all() and np.all(abs(h - want) <= bound)
         want = np.stack([oracle.g4_product(self.w_down[e], v[None])[0] for e, v in zip(of, h)])
-        # bfloat16: terms of up to 31 |s h| (8 + q / 2 and 8 + z / 2, twice); s is at most 2.  What binary32's two
+        # bfloat16: terms of up to 31 |s h| (16 + q and 16 + z); s is at most 2.  What binary32's two
         # parts miss, 2^-23 |w h| and 2^-39 of the largest h, is far less than that allows
         mags = abs(h).sum(1, keepdims=True) * 2 * 31
         assert np.all(abs(rows - want) <= (I + 2 * I / 32 + 64) * 2.0**-23 * mags)

@@ -11,7 +11,7 @@ by half a step: (k + 2 k / 32 + 64) 2^-23 M, and half a step of y's type of the 
 An activation of binary32 enters as two parts (at most 1.001 of its own magnitude), which miss 2^-23 of it
 (half a step of what the first leaves, 2^-11 of the value at most) or, of a slice's smallest, 2^-39 of the
 slice's largest magnitude: 2^-23 M + 2^-39 max |x| sum |w|.  One of bfloat16 counts in M with the weights
-that the sums are made of: 2 |s| (8 + q / 2) in the products, 2 |s| (8 + z / 2) in what is taken off.
+that the sums are made of: |s| (16 + q) in the products, |s| (16 + z) in what is taken off.
 """
 import numpy as np
 import pytest
@@ -146,7 +146,7 @@ def test_real_inputs(group, t):
             if t == "bf16":
                 q = np.stack((codes & 15, codes >> 4), 2).reshape(n, k)
                 wide = lambda v: np.repeat(v, group, axis=1)  # noqa: E731
-                mags = oracle.g4_product(2 * abs(wide(s)) * (16 + q / 2 + (wide(z) / 2 if zeros else 4)), abs(x))
+                mags = oracle.g4_product(abs(wide(s)) * (32 + q + (wide(z) if zeros else 8)), abs(x))
             err = (1.001 * (k + 2 * k / 32) + 64) * 2.0**-23 * mags + own
             bound = err + (HALF_STEP[y_t] * (abs(want) + err) if y_t != "f32" else 0)
             assert np.all(abs(got - want) <= bound)

@@ -101,7 +101,7 @@ def test_activations_off_their_natural_address(m, t):
 @pytest.mark.parametrize("m", [2, 20])
 def test_one_large_activation_among_small_ones(m, t):
     """What is said of an activation's precision: of binary32, 2^-23 of itself or 2^-39 of the largest of its slice,
-    and sums of terms of |w x|; of bfloat16, sums of terms of |2 s (8 + q / 2) x| and |2 s (8 + z / 2) x|."""
+    and sums of terms of |w x|; of bfloat16, sums of terms of |s (16 + q) x| and |s (16 + z) x|."""
     note(f"edges: one large activation, {m} rows, {t}")
     n, k, group = 64, 2048, 64
     codes, s, z = weights(6, n, k, group, True, "bf16", False)
@@ -120,7 +120,7 @@ def test_one_large_activation_among_small_ones(m, t):
     else:
         q = np.stack((codes & 15, codes >> 4), 2).reshape(n, k)
         wide = lambda v: np.repeat(v, group, axis=1)  # noqa: E731
-        mags = oracle.g4_product(2 * abs(wide(s)) * (16 + q / 2 + wide(z) / 2), abs(x))
+        mags = oracle.g4_product(abs(wide(s)) * (32 + q + wide(z)), abs(x))
         own = 0
     assert np.all(abs(got - want) <= (1.001 * (k + 2 * k / 32) + 64) * 2.0**-23 * mags + own)
 
