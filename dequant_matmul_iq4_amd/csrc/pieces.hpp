@@ -15,6 +15,21 @@ inline int type_bytes(int t) { return t == kF32 ? 4 : 2; }
 // they would only push each other out of it and of the memory-side cache behind it.
 constexpr int64_t kStreamBytes = 64 << 20;
 
+// Division of n < 2^31 by a fixed number d, the pieces of a row (1 .. 2^30): with 2^l >= d and m = floor(2^(31 + l) / d) + 1
+// (below 2^32), m d - 2^(31 + l) is at most 2^l, so that floor(n m / 2^(31 + l)) is n / d.
+struct Pieces {
+  uint32_t n, m, l;
+  explicit Pieces(uint32_t d) : n(d), l(0) {
+    while (((uint64_t)1 << l) < d) ++l;
+    m = (uint32_t)(((uint64_t)1 << (31 + l)) / d) + 1;
+  }
+#ifdef __HIPCC__
+  __device__ __forceinline__ uint32_t row(uint32_t i) const { return __umulhi(i << 1, m) >> l; }
+#endif
+};
+// Rows of a launch: below 2^31 threads, those of the last workgroup included.
+inline int64_t rows_a_launch(const Pieces& p) { return (((int64_t)1 << 31) - 256) / p.n; }
+
 #ifdef __HIPCC__
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(2)));

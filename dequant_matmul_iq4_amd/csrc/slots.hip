@@ -80,12 +80,12 @@ __device__ __forceinline__ void store_one(char* row, int64_t at, float v) {
 // A lane per piece, whatever token it belongs to; four slots at a time.  The written rows bound it: 3256
 // tokens of 2048 numbers of 16 bits to 8 rows each 22 us (5.4 TB/s), of 2047 28, of float32 42.
 template <int TX, int TR, bool STREAM>
-__global__ void __launch_bounds__(256) dispatch_kernel(SlotArgs a, uint32_t pieces) {
+__global__ void __launch_bounds__(256) dispatch_kernel(SlotArgs a, Pieces pieces) {
   constexpr int P = kPiece<TX, TR>;
   const uint32_t i = blockIdx.x * 256 + threadIdx.x;
-  const uint32_t t = i / pieces;
+  const uint32_t t = pieces.row(i);
   if (t >= a.n_tok) return;
-  const Piece c = piece_of<P>(i - t * pieces, a.hidden);
+  const Piece c = piece_of<P>(i - t * pieces.n, a.hidden);
   float v[P];
   load_piece<TX, P>(row_of<TX>(a.tok, t, a.ldt), c.at, c.left, v);
   for (int j0 = 0; j0 < a.top_k; j0 += 4) {
@@ -106,12 +106,12 @@ __global__ void __launch_bounds__(256) dispatch_kernel(SlotArgs a, uint32_t piec
 // 2048, eight rows of 16 bits each, 26 us (4.6 TB/s), of 2047 29, of float32 44; four tokens 3.3.  (Eight, 16-bit rows: the prompt's 31.9 us
 // for 26.1; a workgroup per token, its slots in scalar registers: 28.2, and 52 for rows of 700.)
 template <int TR, int TO, bool STREAM>
-__global__ void __launch_bounds__(256) combine_rows_kernel(SlotArgs a, uint32_t pieces) {
+__global__ void __launch_bounds__(256) combine_rows_kernel(SlotArgs a, Pieces pieces) {
   constexpr int P = kPiece<TR, TO>;
   const uint32_t i = blockIdx.x * 256 + threadIdx.x;
-  const uint32_t t = i / pieces;
+  const uint32_t t = pieces.row(i);
   if (t >= a.n_tok) return;
-  const Piece c = piece_of<P>(i - t * pieces, a.hidden);
+  const Piece c = piece_of<P>(i - t * pieces.n, a.hidden);
   float acc[P];
 #pragma unroll
   for (int e = 0; e < P; ++e) acc[e] = 0.f;
@@ -282,10 +282,9 @@ __global__ void __launch_bounds__(256) combine_grad_short_kernel(SlotArgs a, uin
   }
 }
 
-// A launch has fewer than 2^32 threads: tokens go in as many launches as that takes.
+// Tokens go in as many launches of at most `most` as that takes.
 template <typename F>
-static int by_tokens(SlotArgs a, int64_t threads_per_token, int in_type, int out_type, bool out_by_token, F launch) {
-  const int64_t most = ((int64_t)1 << 31) / threads_per_token;
+static int by_tokens(SlotArgs a, int64_t most, int in_type, int out_type, bool out_by_token, F launch) {
   while (a.n_tok > 0) {
     SlotArgs part = a;
     part.n_tok = a.n_tok < most ? a.n_tok : most;
@@ -326,11 +325,11 @@ static bool streams(const SlotArgs& a, int rows_type) {
 }
 
 int launch_dispatch(const SlotArgs& a, int x_type, int rows_type, hipStream_t s) {
-  const uint32_t pieces = pieces_of(a.hidden, x_type, rows_type);
+  const Pieces pieces(pieces_of(a.hidden, x_type, rows_type));
   // (written rows that do not begin on 16 bytes leave in parts: 2047 numbers of 16 bits 31 us for 27)
   const bool st = streams(a, rows_type) && aligned(a.out, 16) && a.ldo * type_bytes(rows_type) % 16 == 0;
-  return by_tokens(a, pieces, x_type, rows_type, false, [&](const SlotArgs& b) {
-    const dim3 grid((unsigned)((b.n_tok * pieces + 255) / 256));
+  return by_tokens(a, rows_a_launch(pieces), x_type, rows_type, false, [&](const SlotArgs& b) {
+    const dim3 grid((unsigned)((b.n_tok * pieces.n + 255) / 256));
 #define IQ4_CALL(T1, T2)                                                                                 \
   if (st) hipLaunchKernelGGL((dispatch_kernel<T1, T2, true>), grid, dim3(256), 0, s, b, pieces);         \
   else hipLaunchKernelGGL((dispatch_kernel<T1, T2, false>), grid, dim3(256), 0, s, b, pieces)
@@ -341,10 +340,10 @@ int launch_dispatch(const SlotArgs& a, int x_type, int rows_type, hipStream_t s)
 }
 
 int launch_combine_rows(const SlotArgs& a, int rows_type, int out_type, hipStream_t s) {
-  const uint32_t pieces = pieces_of(a.hidden, rows_type, out_type);
+  const Pieces pieces(pieces_of(a.hidden, rows_type, out_type));
   const bool st = streams(a, rows_type);
-  return by_tokens(a, pieces, out_type, out_type, true, [&](const SlotArgs& b) {
-    const dim3 grid((unsigned)((b.n_tok * pieces + 255) / 256));
+  return by_tokens(a, rows_a_launch(pieces), out_type, out_type, true, [&](const SlotArgs& b) {
+    const dim3 grid((unsigned)((b.n_tok * pieces.n + 255) / 256));
 #define IQ4_CALL(T1, T2)                                                                                 \
   if (st) hipLaunchKernelGGL((combine_rows_kernel<T1, T2, true>), grid, dim3(256), 0, s, b, pieces);     \
   else hipLaunchKernelGGL((combine_rows_kernel<T1, T2, false>), grid, dim3(256), 0, s, b, pieces)
@@ -356,7 +355,7 @@ int launch_combine_rows(const SlotArgs& a, int rows_type, int out_type, hipStrea
 
 template <int WAVES, bool STREAM>
 static int launch_grad_waves(const SlotArgs& a, int dout_type, int rows_type, uint32_t pieces, hipStream_t s) {
-  return by_tokens(a, 64 * WAVES, dout_type, rows_type, false, [&](const SlotArgs& b) {
+  return by_tokens(a, ((int64_t)1 << 31) / (64 * WAVES), dout_type, rows_type, false, [&](const SlotArgs& b) {
     const dim3 grid((unsigned)b.n_tok);
 #define IQ4_CALL(T1, T2) \
   hipLaunchKernelGGL((combine_grad_kernel<T1, T2, WAVES, STREAM>), grid, dim3(64 * WAVES), 0, s, b, pieces)
@@ -369,7 +368,7 @@ static int launch_grad_waves(const SlotArgs& a, int dout_type, int rows_type, ui
 int launch_combine_grad(const SlotArgs& a, int dout_type, int rows_type, hipStream_t s) {
   const uint32_t pieces = pieces_of(a.hidden, dout_type, rows_type);
   if (pieces <= 16)
-    return by_tokens(a, 16, dout_type, rows_type, false, [&](const SlotArgs& b) {
+    return by_tokens(a, ((int64_t)1 << 31) / 16, dout_type, rows_type, false, [&](const SlotArgs& b) {
       const dim3 grid((unsigned)((b.n_tok + 15) / 16));
 #define IQ4_CALL(T1, T2) hipLaunchKernelGGL((combine_grad_short_kernel<T1, T2>), grid, dim3(256), 0, s, b, pieces)
       IQ4_TYPES(dout_type, rows_type, IQ4_CALL)
