@@ -59,19 +59,17 @@ __device__ __forceinline__ void put8(void* p, u32x2 v) {
 // Piece q of a row of n elements: the first element, how many there are (P unless the row is shorter), and
 // how many of them are the piece's before it too.
 struct Piece {
-  int64_t at;
-  int left, twice;
+  int at, left, twice;
 };
 template <int P>
-__device__ __forceinline__ Piece piece_of(uint32_t q, int64_t n) {
-  const int64_t at = (int64_t)q * P;
-  const int over = (int)max<int64_t>(at + P - n, 0);
+__device__ __forceinline__ Piece piece_of(uint32_t q, int64_t n) {  // n <= 2^20
+  const int at = (int)q * P, end = at + P - (int)n, over = end > 0 ? end : 0;
   return over == 0 || n < P ? Piece{at, P - over, 0} : Piece{at - over, P, over};
 }
 
 // Elements at .. at + P - 1 of a row, `left` of which exist (the others are zero), as binary32.
 template <int TYPE, int P, bool STREAM = false>
-__device__ __forceinline__ void load_piece(const void* row, int64_t at, int left, float (&v)[P]) {
+__device__ __forceinline__ void load_piece(const void* row, int at, int left, float (&v)[P]) {
   if constexpr (TYPE == kF32) {
     const float* p = static_cast<const float*>(row) + at;
     if (left >= P) {
@@ -119,7 +117,7 @@ __device__ __forceinline__ void load_piece(const void* row, int64_t at, int left
 
 // The same elements rounded (once, to nearest even) to TYPE and written.
 template <int TYPE, int P, bool STREAM = false>
-__device__ __forceinline__ void store_piece(void* row, int64_t at, int left, const float (&v)[P]) {
+__device__ __forceinline__ void store_piece(void* row, int at, int left, const float (&v)[P]) {
   if constexpr (TYPE == kF32) {
     float* p = static_cast<float*>(row) + at;
     if (left >= P) {
