@@ -944,10 +944,15 @@ int iq4_swiglu(const void* g, int64_t ldg, const void* u, int64_t ldu, int32_t d
     if (int e = check_any(fn, "y", y, y_dtype, k, ldy)) return e;
   if (codes)
     if (int e = check_rows(fn, fmt, k, codes, ldq, scales, lds)) return e;
-  if (y) {
-    const Span o = span(y, m, k, ldy, y_dtype);
-    if (int e = check_apart(fn, "y", o, "g", span(g, m, k, ldg, dtype))) return e;
-    if (int e = check_apart(fn, "y", o, "u", span(u, m, k, ldu, dtype))) return e;
+  const Span outs[3] = {span(y, m, k, ldy, y_dtype),
+                        codes ? Span{static_cast<const char*>(codes), m, ldq, rows_code_bytes(fmt, k)} : Span{},
+                        codes ? Span{static_cast<const char*>(scales), m, lds, rows_scale_bytes(fmt, k)} : Span{}};
+  const char* names[3] = {"y", "codes", "scales"};
+  for (int i = 0; i < 3; ++i) {
+    if (int e = check_apart(fn, names[i], outs[i], "g", span(g, m, k, ldg, dtype))) return e;
+    if (int e = check_apart(fn, names[i], outs[i], "u", span(u, m, k, ldu, dtype))) return e;
+    for (int j = 0; j < i; ++j)
+      if (int e = check_apart(fn, names[i], outs[i], names[j], outs[j])) return e;
   }
   SwigluArgs a{};
   a.g = g;

@@ -97,6 +97,7 @@ def test_swiglu_refusals():
     assert fwd(yt=3) == A and fwd(y=None, q=None) == A and fwd(ldy=127) == A and fwd(y=FAKE * 3 + 2) == AL and fwd(k=100) == U
     assert fwd(fmt=7) == A and fwd(d=None) == A and fwd(ldq=64) == A and fwd(q=FAKE + 8) == AL and fwd(fmt=MX4, lds=24) == AL
     assert fwd(fmt=Q8, lds=6) == A
+    assert fwd(q=FAKE + 256) == A and fwd(d=FAKE - 16) == A and fwd(q=FAKE * 3 + 512) == A and fwd(d=FAKE * 4 + 128) == A  # overlaps
     assert fwd(y=FAKE) == A and fwd(g=FAKE * 3 + 64) == A and fwd(u=FAKE * 3 - 64) == A  # overlaps
     assert grad(dg=FAKE) == A and grad(du=FAKE * 3) == A and grad(dh=FAKE * 4 + 64, dt=1) == A
     assert grad(dg=FAKE * 3, lddg=256, du=FAKE * 3 + 256, lddu=256) == A  # halves of a buffer's rows, too narrow

@@ -189,3 +189,54 @@ def test_many_elements():
     dw = torch.zeros(T, top, device="cuda")
     iq4.iq4_moe_combine_grad(x, HALF, H, rows, HALF, H, T * top, slot, None, T, top, H, None, 0, dw)
     assert torch.equal(dw, (x.float() ** 2).sum(1, keepdim=True).expand(T, top))
+
+
+def test_more_rows_than_a_launch_takes():
+    """2^24 tokens of 129 pieces of 16 bytes are more than 2^31 lanes: the calls go in parts."""
+    note("edges: 2^24 tokens of 1032")
+    T, H = 1 << 24, 1032
+    value = (torch.arange(T, device="cuda") % 31).half()
+    x = torch.empty(T, H, dtype=torch.float16, device="cuda")
+    x.copy_(value[:, None].expand(T, H))
+    x[-1] = torch.arange(H, device="cuda") % 29
+    slot = torch.arange(T - 1, -1, -1, dtype=torch.int32, device="cuda")
+    rows = torch.zeros(T, H, dtype=torch.float16, device="cuda")
+    iq4.iq4_moe_dispatch(x, HALF, H, T, H, slot, None, 1, T, rows, HALF, H)
+    last = x[-1].clone()
+    dw = torch.zeros(T, 1, device="cuda")
+    iq4.iq4_moe_combine_grad(x, HALF, H, rows, HALF, H, T, slot, None, T, 1, H, None, 0, dw)
+    want = H * value.float() ** 2
+    want[-1] = (last.float() ** 2).sum()
+    assert torch.equal(dw[:, 0], want)
+    x.zero_()
+    iq4.iq4_moe_combine(rows, HALF, H, T, slot, None, T, 1, H, None, 0, x, HALF, H)
+    assert torch.equal(x[-1], last) and torch.equal(rows[0], last)
+    for at in (0, 1, H // 2, H - 1):
+        assert torch.equal(x[:-1, at], value[:-1]) and torch.equal(rows[1:, at].flip(0), value[:-1])
+    rows.zero_()
+    iq4.iq4_moe_combine_grad(x, HALF, H, None, HALF, H, T, slot, None, T, 1, H, rows, H, None)
+    assert torch.equal(rows[0], last) and torch.equal(rows[1:, H - 1].flip(0), value[:-1])
+    del x, rows
+    torch.cuda.empty_cache()
+
+
+def test_the_largest_swiglu():
+    """2^34 elements, 2^31 lanes: in two parts, the second of one row."""
+    note("edges: SwiGLU of 16384 x 2^20")
+    m, k, bf = 1 << 14, 1 << 20, iq4.IQ4_BF16
+    row = torch.randn(k, device="cuda").bfloat16()
+    g = torch.empty(m, k, dtype=torch.bfloat16, device="cuda")
+    g.copy_(row.expand(m, k))
+    g[-1].neg_()
+    one = torch.zeros(2, k, dtype=torch.bfloat16, device="cuda")
+    two = torch.zeros_like(one)
+    y, z = torch.zeros_like(g), torch.zeros_like(g)
+    iq4.iq4_swiglu(g, k, g, k, bf, m, k, y, bf, k)
+    iq4.iq4_swiglu(g[-2:], k, g[-2:], k, bf, 2, k, one, bf, k)
+    assert torch.equal(y[-2:], one) and torch.equal(y[0], one[0]) and torch.equal(y[:, -1], one[0, -1:].expand(m).where(torch.arange(m, device="cuda") < m - 1, one[1, -1]))
+    iq4.iq4_swiglu_grad(g, bf, k, g, k, g, k, bf, m, k, y, k, z, k)
+    iq4.iq4_swiglu_grad(g[-2:], bf, k, g[-2:], k, g[-2:], k, bf, 2, k, one, k, two, k)
+    for big, small in ((y, one), (z, two)):
+        assert torch.equal(big[-2:], small) and torch.equal(big[0], small[0]) and torch.equal(big[m // 2], small[0])
+    del g, y, z
+    torch.cuda.empty_cache()
