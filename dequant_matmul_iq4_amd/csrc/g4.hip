@@ -48,11 +48,8 @@ int launch_g4_pack(const G4Pack& a, hipStream_t s) {
 }
 
 int launch_g4_qmv(const G4Args& a, hipStream_t s) {
-  // one operand of 16 rows of X (8 of binary32) or two; by expert by the rows that one has on average
-  const int64_t rows = a.offsets ? (a.m + a.n_expert - 1) / a.n_expert : a.m;
-  const int nv = rows > (a.x_type == kF32 ? 8 : 16) ? 2 : 1;
-  if (a.group == 32) return launch_g4_32(a, nv, s);
-  return a.group == 64 ? launch_g4_64(a, nv, s) : launch_g4_128(a, nv, s);
+  if (a.group == 32) return launch_g4_32(a, s);
+  return a.group == 64 ? launch_g4_64(a, s) : launch_g4_128(a, s);
 }
 
 }  // namespace iq4

@@ -3,9 +3,9 @@
 
 namespace iq4 {
 
-int launch_g4_64(const G4Args& a, int nv, hipStream_t s) {
-  if (a.x_type == kF32) return launch_g4_group<kF32, 64>(a, nv, s);
-  return a.x_type == kF16 ? launch_g4_group<kF16, 64>(a, nv, s) : launch_g4_group<kBF16, 64>(a, nv, s);
+int launch_g4_64(const G4Args& a, hipStream_t s) {
+  if (a.x_type == kF32) return launch_g4_group<kF32, 64>(a, s);
+  return a.x_type == kF16 ? launch_g4_group<kF16, 64>(a, s) : launch_g4_group<kBF16, 64>(a, s);
 }
 
 }  // namespace iq4

@@ -1,5 +1,5 @@
 // g4_kernel.hpp -- the product of few rows with group-scaled 4-bit weights (g4.hpp): the kernel and
-// its launch, compiled once per group size and type of X (g4_32.hip, g4_64.hip, g4_128.hip).
+// its launch, compiled once per group size (g4_32.hip, g4_64.hip, g4_128.hip).
 //
 // Mathematics.  With d = sum of (q - z) x over a group's k, a row's result is the sum of s d over
 // its groups.  A code tile's products run on the matrix cores, whose products are exact here and
@@ -523,39 +523,55 @@ static int launch_g4_kernel(const G4Args& a, G4Plan p, hipStream_t s) {
 // k over up to eight waves, sx code tiles of each in registers (as many as those hold; where that is
 // not all of k, one slice after another).
 template <int XT, int G>
-static int launch_g4_group(const G4Args& a, int nv, hipStream_t s) {
-  const int bm = XT == kF32 ? 8 * nv : 16 * nv;
-  int64_t cols = (a.m + bm - 1) / bm, busy = cols;
-  if (a.offsets) {
+static int launch_g4_group(const G4Args& a, hipStream_t s) {
+  const int64_t rt_n = g4_row_tiles(a.n);
+  const int kt_n = g4_k_tiles(a.k);
+  int64_t cols, busy;  // tiles of rows of X: the grid's, and those that have rows
+  auto columns = [&](int nv) {
+    const int bm = XT == kF32 ? 8 * nv : 16 * nv;
+    busy = cols = (a.m + bm - 1) / bm;
+    if (!a.offsets) return;
     // each expert's last tile may be partial; as many have any if the rows choose at random
     cols = a.m / bm + a.n_expert < a.m ? a.m / bm + a.n_expert : a.m;
     busy = (int64_t)(a.n_expert * -expm1(-(double)a.m / a.n_expert)) + a.m / (a.n_expert * bm) * a.n_expert + 1;
     if (busy > cols) busy = cols;
-  }
-  const int64_t rt_n = g4_row_tiles(a.n);
-  const int kt_n = g4_k_tiles(a.k), most = nv == 1 ? 6 : 4;
+  };
+  // Two operands of rows of X where there are rows for them (an expert's on average), all of k fits the
+  // registers with them, and they leave every CU a workgroup.  bfloat16, 64 rows of 2048 x 4096: 9.9 us with two,
+  // 8.5 with one; 33 rows of 4096 x 4096 11.9 and 13.6; 47 rows of 14336 x 6144 37.3 and 29.3.
+  const int64_t rows = a.offsets ? (a.m + a.n_expert - 1) / a.n_expert : a.m;
+  int nv = rows > (XT == kF32 ? 8 : 16) && kt_n <= 32 ? 2 : 1;
+  columns(nv);
+  if (nv == 2 && rt_n * busy * (kt_n < 8 ? kt_n : 8) <= 2048) columns(nv = 1);
   int sx = (kt_n + 7) / 8;
   // short rows: two tiles a wave where there is work for twice the device's waves all the same (128 experts
   // of 2048 x 768, 488 rows: 23.4 us for 29.6)
   if (sx == 1 && kt_n > 1 && rt_n * busy * ((kt_n + 1) / 2) >= 8192) sx = 2;
   if (sx == 5) sx = 6;
   if (sx == 3 && nv == 2) sx = 4;
-  const bool chunks = sx > most;
-  if (chunks) sx = most;
+  // longer rows in slices of six tiles or four, whichever fill their last round better (one row of
+  // 4096 x 14336: 14.7 us with six, 12.8 with four)
+  const bool chunks = sx > 6;
+  if (chunks) sx = (kt_n + 47) / 48 * 6 <= (kt_n + 31) / 32 * 4 ? 6 : 4;
   G4Plan p{};
   p.ks = (kt_n + sx - 1) / sx;
   if (p.ks > 8) p.ks = 8;
   p.cols = (int)cols;
   // row tiles a workgroup: as many as leave the device the 8 waves a CU that its registers hold, or 16 where
   // a wave's activations are few or soon made operands.  14336 x 4096 in bfloat16, 16 rows: 12.4 us with 8,
-  // 16.4 with 16; one row 9.7 and 11.6, in binary16 11.1 and 10.0, four rows 11.2 and 12.2; 128 experts of 1536 x 2048, 32 rows: 16.0 with 32, 14.8 with 16.  One workgroup more than
-  // there is room for costs as much as all (128 experts of 2048 x 768, 488 rows: 21.5 us, 26.0 with one row
-  // tile less each), so by expert the columns that have rows count, not the grid's.
+  // 16.4 with 16; one row 9.7 and 11.6, in binary16 11.1 and 10.0, four rows 11.2 and 12.2; 128 experts of
+  // 1536 x 2048, 32 rows: 16.0 with 32, 14.8 with 16.  One workgroup more than there is room for costs as much
+  // as all (128 experts of 2048 x 768, 488 rows: 21.5 us, 26.0 with one row tile less each), so by
+  // expert the columns that have rows count, not the grid's.
   const int64_t waves = nv * sx >= 4 && (XT != kF16 || a.m > 1) ? 2048 : 4096;
   const int64_t per = (rt_n * busy * p.ks + waves - 1) / waves;
   p.per = (int)(per > rt_n ? rt_n : per);
-  p.rb = p.per < 4 ? p.per : 4;  // (a multiple of the row tiles that a wave loads ahead, or all)
-  if (chunks) return nv == 1 ? launch_g4_kernel<XT, 1, 6, G, true>(a, p, s) : launch_g4_kernel<XT, 2, 4, G, true>(a, p, s);
+  // joins: every four row tiles (a multiple of those that a wave loads ahead), or, where each would load X again,
+  // as many as the CU's LDS holds (57 rows of 6097 x 8768, six row tiles each: 49.5 us with two joins, 40.9 with one)
+  const int room = (160 * 1024 / 8 - g4_x_lds(XT, 1, 6, G)) / 1024;
+  const int rb = chunks ? room : 4;
+  p.rb = p.per < rb ? p.per : rb;
+  if (chunks) return sx == 6 ? launch_g4_kernel<XT, 1, 6, G, true>(a, p, s) : launch_g4_kernel<XT, 1, 4, G, true>(a, p, s);
   switch (10 * nv + sx) {
     case 11: return launch_g4_kernel<XT, 1, 1, G>(a, p, s);
     case 12: return launch_g4_kernel<XT, 1, 2, G>(a, p, s);

@@ -125,6 +125,21 @@ def test_whole_numbers_are_exact(n, k, group, zeros, t):
 
 
 @pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("n,k,group", [(4100, 160, 32), (4100, 640, 128), (4100, 1056, 32), (2100, 2048, 64), (2100, 3584, 128), (2100, 4096, 32),
+                                       (20, 6400, 64), (1030, 6400, 128), (600, 8768, 32)])
+def test_more_columns_and_longer_rows(n, k, group, t):
+    # |sum| <= 8768 * 15 * 2 * 4 < 2^21 in steps of 1/2
+    codes, s, z = weights(n * k, n, k, group, True, "f16", True)
+    p = pack(codes, s, z, group, "f16")
+    w = oracle.g4_weights(codes, s, z, group)
+    rng = np.random.default_rng(k)
+    for m in (1, 12, 17, 33, 47, 64, 130):
+        note(f"g4: exact {m} x {n} x {k} by {group}, {t}")
+        x = rng.integers(-4, 5, (m, k)).astype(np.float64)
+        assert np.array_equal(product(p, n, k, group, z, "f16", x, t, "f32", ldx=k + m % 2), oracle.g4_product(w, x)), m
+
+
+@pytest.mark.parametrize("t", list(TYPES))
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_real_inputs(group, t):
     n, k = 96, 2560
