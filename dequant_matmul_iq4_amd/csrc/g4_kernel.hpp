@@ -531,18 +531,22 @@ static int launch_g4_group(const G4Args& a, hipStream_t s) {
     const int bm = XT == kF32 ? 8 * nv : 16 * nv;
     busy = cols = (a.m + bm - 1) / bm;
     if (!a.offsets) return;
-    // each expert's last tile may be partial; as many have any if the rows choose at random
+    // each expert's last tile may be partial, on average half of one; if the rows choose at random, as many
+    // experts as `some` have any
     cols = a.m / bm + a.n_expert < a.m ? a.m / bm + a.n_expert : a.m;
-    busy = (int64_t)(a.n_expert * -expm1(-(double)a.m / a.n_expert)) + a.m / (a.n_expert * bm) * a.n_expert + 1;
+    const double some = a.n_expert * -expm1(-(double)a.m / a.n_expert), tiles = (double)a.m / bm + some / 2;
+    busy = (int64_t)ceil(tiles > some ? tiles : some);
     if (busy > cols) busy = cols;
   };
-  // Two operands of rows of X where there are rows for them (an expert's on average), all of k fits the
-  // registers with them, and they leave every CU a workgroup.  bfloat16, 64 rows of 2048 x 4096: 9.9 us with two,
-  // 8.5 with one; 33 rows of 4096 x 4096 11.9 and 13.6; 47 rows of 14336 x 6144 37.3 and 29.3.
+  // Two operands of rows of X where there are rows for them (an expert's on average), all of k fits the registers
+  // with them, and they leave every CU a workgroup; by expert, where many tiles are not full, sixteen.
+  // bfloat16, 64 rows of 2048 x 4096: 9.9 us with two, 8.5 with one; 33 rows of 4096 x 4096 11.9 and 13.6; 47 rows of
+  // 14336 x 6144 37.3 and 29.3; 9 experts of 1991 x 1312 with 32 rows each 17.7 and 14.9; 128 of 2048 x 768 with 19
+  // each 47 and 49.
   const int64_t rows = a.offsets ? (a.m + a.n_expert - 1) / a.n_expert : a.m;
   int nv = rows > (XT == kF32 ? 8 : 16) && kt_n <= 32 ? 2 : 1;
   columns(nv);
-  if (nv == 2 && rt_n * busy * (kt_n < 8 ? kt_n : 8) <= 2048) columns(nv = 1);
+  if (nv == 2 && rt_n * busy * (kt_n < 8 ? kt_n : 8) <= (a.offsets ? 16 : 1) * 2048) columns(nv = 1);
   int sx = (kt_n + 7) / 8;
   // short rows: two tiles a wave where there is work for twice the device's waves all the same (128 experts
   // of 2048 x 768, 488 rows: 23.4 us for 29.6)
@@ -557,15 +561,19 @@ static int launch_g4_group(const G4Args& a, hipStream_t s) {
   p.ks = (kt_n + sx - 1) / sx;
   if (p.ks > 8) p.ks = 8;
   p.cols = (int)cols;
-  // row tiles a workgroup: as many as leave the device the 8 waves a CU that its registers hold, or 16 where
-  // a wave's activations are few or soon made operands.  14336 x 4096 in bfloat16, 16 rows: 12.4 us with 8,
-  // 16.4 with 16; one row 9.7 and 11.6, in binary16 11.1 and 10.0, four rows 11.2 and 12.2; 128 experts of
-  // 1536 x 2048, 32 rows: 16.0 with 32, 14.8 with 16.  One workgroup more than there is room for costs as much
-  // as all (128 experts of 2048 x 768, 488 rows: 21.5 us, 26.0 with one row tile less each), so by
-  // expert the columns that have rows count, not the grid's.
-  const int64_t waves = nv * sx >= 4 && (XT != kF16 || a.m > 1) ? 2048 : 4096;
-  const int64_t per = (rt_n * busy * p.ks + waves - 1) / waves;
-  p.per = (int)(per > rt_n ? rt_n : per);
+  // Row tiles a workgroup: as few as let the device hold all workgroups at once.  Its registers hold 8 waves a CU, or
+  // 16 of those with few activations (or one row that soon is operands); of more than four waves, one
+  // workgroup or two.  14336 x 4096 in bfloat16, 16 rows: 12.4 us with 8 waves, 16.4 with 16; one row 9.7 and 11.6, in
+  // binary16 11.1 and 10.0, four rows 11.2 and 12.2; 128 experts of 1536 x 2048, 32 rows: 16.0 with 32, 14.8
+  // with 16.  A few workgroups too many cost as much as all: 33 rows of 4217 x 2944 17.5 us with 264 workgroups of six
+  // waves, 13.9 with 176; by expert, where some end early, 128 experts of 2048 x 768 with 488 rows 26.0 with 1500 of
+  // three, 21.5 with 1380 (and 22.5 with 1250).
+  const bool few = nv * sx < 4 || (XT == kF16 && a.m == 1);
+  const int64_t places = p.ks <= 4 ? (few ? 4096 : 2048) / p.ks : few ? 512 : 256;
+  int64_t per = (rt_n * busy + places - 1) / places;
+  while (!a.offsets && per < rt_n && (rt_n + per - 1) / per * busy > places) ++per;
+  if (per > rt_n) per = rt_n;
+  p.per = (int)((rt_n + (rt_n + per - 1) / per - 1) / ((rt_n + per - 1) / per));  // (evenly)
   // joins: every four row tiles (a multiple of those that a wave loads ahead), or, where each would load X again,
   // as many as the CU's LDS holds (57 rows of 6097 x 8768, six row tiles each: 49.5 us with two joins, 40.9 with one)
   const int room = (160 * 1024 / 8 - g4_x_lds(XT, 1, 6, G)) / 1024;
