@@ -162,13 +162,12 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // (Rows both read and written bound it: 3256 tokens of 2048, eight rows of 16 bits each, 47 us, 4.8 TB/s.)
-// A workgroup of WAVES per token: a lane takes every WAVES * 64th piece of the row, its part of dO
-// from memory once and the rows of eight slots at once; the slots' dots are summed over the
-// lanes in a fixed order.
-template <int TD, int TR, int WAVES, bool STREAM>
-__global__ void __launch_bounds__(WAVES * 64) combine_grad_kernel(SlotArgs a, uint32_t pieces) {
+// A workgroup per token: a lane takes every blockDim-th piece of the row, its part of dO from memory once and
+// the rows of eight slots at once; the slots' dots are summed over the lanes in a fixed order.
+template <int TD, int TR, bool STREAM>
+__global__ void __launch_bounds__(1024) combine_grad_kernel(SlotArgs a, uint32_t pieces) {
   constexpr int P = kPiece<TD, TR>;
-  __shared__ float part[WAVES][16];
+  __shared__ float part[16][16];
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const TokenSlots s(a, t);
@@ -177,7 +176,7 @@ __global__ void __launch_bounds__(WAVES * 64) combine_grad_kernel(SlotArgs a, ui
     float dot[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) dot[j] = 0.f;
-    for (uint32_t q = threadIdx.x; q < pieces; q += WAVES * 64) {
+    for (uint32_t q = threadIdx.x; q < pieces; q += blockDim.x) {
       const Piece c = piece_of<P>(q, a.hidden);
       float d[P], v[8][P];
       load_piece<TD, P>(dout, c.at, c.left, d);
@@ -223,16 +222,10 @@ __global__ void __launch_bounds__(WAVES * 64) combine_grad_kernel(SlotArgs a, ui
     }
   }
   if (!a.dw) return;
-  if constexpr (WAVES > 1) __syncthreads();
-  else {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  }
+  __syncthreads();
   if ((int)threadIdx.x < a.top_k) {
     float s = part[0][threadIdx.x];
-#pragma unroll
-    for (int v = 1; v < WAVES; ++v) s = s + part[v][threadIdx.x];
+    for (int v = 1; v < (int)(blockDim.x >> 6); ++v) s = s + part[v][threadIdx.x];
     a.dw[t * a.top_k + threadIdx.x] = s;
   }
 }
@@ -353,18 +346,6 @@ int launch_combine_rows(const SlotArgs& a, int rows_type, int out_type, hipStrea
   });
 }
 
-template <int WAVES, bool STREAM>
-static int launch_grad_waves(const SlotArgs& a, int dout_type, int rows_type, uint32_t pieces, hipStream_t s) {
-  return by_tokens(a, ((int64_t)1 << 31) / (64 * WAVES), dout_type, rows_type, false, [&](const SlotArgs& b) {
-    const dim3 grid((unsigned)b.n_tok);
-#define IQ4_CALL(T1, T2) \
-  hipLaunchKernelGGL((combine_grad_kernel<T1, T2, WAVES, STREAM>), grid, dim3(64 * WAVES), 0, s, b, pieces)
-    IQ4_TYPES(dout_type, rows_type, IQ4_CALL)
-#undef IQ4_CALL
-    return check_launch("combine_grad_kernel");
-  });
-}
-
 int launch_combine_grad(const SlotArgs& a, int dout_type, int rows_type, hipStream_t s) {
   const uint32_t pieces = pieces_of(a.hidden, dout_type, rows_type);
   if (pieces <= 16)
@@ -375,13 +356,22 @@ int launch_combine_grad(const SlotArgs& a, int dout_type, int rows_type, hipStre
 #undef IQ4_CALL
       return check_launch("combine_grad_kernel");
     });
-  // waves a token: one a 64 pieces, up to four; sixteen where the tokens alone would not fill the device
-  // (four tokens of 8192: 7.9 us)
-  if (pieces <= 64) return launch_grad_waves<1, false>(a, dout_type, rows_type, pieces, s);
-  if (pieces > 256 && a.n_tok <= 256) return launch_grad_waves<16, false>(a, dout_type, rows_type, pieces, s);
-  if (pieces <= 128) return launch_grad_waves<2, false>(a, dout_type, rows_type, pieces, s);
-  return streams(a, rows_type) ? launch_grad_waves<4, true>(a, dout_type, rows_type, pieces, s)
-            : launch_grad_waves<4, false>(a, dout_type, rows_type, pieces, s);
+  // waves a token: a wave per 64 pieces up to four, in rounds of four or of three, whichever fill the last one better
+  // (5147 tokens of 2290 numbers of 16 bits, 287 pieces: 35 us with three, 40 with four; 3256 of 2048 59 and 47); up to
+  // sixteen where the tokens alone would not fill the device (four tokens of 8192: 6.2 us, 12.9 with four)
+  int waves = (int)((pieces + 63) / 64);
+  if (pieces > 256 && a.n_tok <= 256) waves = waves < 16 ? waves : 16;
+  else if (waves > 2) waves = (pieces + 191) / 192 * 192 < (pieces + 255) / 256 * 256 ? 3 : 4;
+  const bool st = streams(a, rows_type);
+  return by_tokens(a, ((int64_t)1 << 31) / (64 * waves), dout_type, rows_type, false, [&](const SlotArgs& b) {
+    const dim3 grid((unsigned)b.n_tok);
+#define IQ4_CALL(T1, T2)                                                                                         \
+  if (st) hipLaunchKernelGGL((combine_grad_kernel<T1, T2, true>), grid, dim3(64 * waves), 0, s, b, pieces);      \
+  else hipLaunchKernelGGL((combine_grad_kernel<T1, T2, false>), grid, dim3(64 * waves), 0, s, b, pieces)
+    IQ4_TYPES(dout_type, rows_type, IQ4_CALL)
+#undef IQ4_CALL
+    return check_launch("combine_grad_kernel");
+  });
 }
 
 }  // namespace iq4
