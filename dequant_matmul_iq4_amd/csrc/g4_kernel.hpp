@@ -570,10 +570,11 @@ static int launch_g4_group(const G4Args& a, hipStream_t s) {
   // three, 21.5 with 1380 (and 22.5 with 1250).
   const bool few = nv * sx < 4 || (XT == kF16 && a.m == 1);
   const int64_t places = p.ks <= 4 ? (few ? 4096 : 2048) / p.ks : few ? 512 : 256;
-  int64_t per = (rt_n * busy + places - 1) / places;
-  while (!a.offsets && per < rt_n && (rt_n + per - 1) / per * busy > places) ++per;
-  if (per > rt_n) per = rt_n;
-  p.per = (int)((rt_n + (rt_n + per - 1) / per - 1) / ((rt_n + per - 1) / per));  // (evenly)
+  // workgroups along the row tiles, which share them evenly
+  const int64_t share = (rt_n * busy + places - 1) / places;
+  int64_t along = a.offsets ? (rt_n + share - 1) / share : busy < places ? places / busy : 1;
+  if (along > rt_n) along = rt_n;
+  p.per = (int)((rt_n + along - 1) / along);
   // joins: every four row tiles (a multiple of those that a wave loads ahead), or, where each would load X again,
   // as many as the CU's LDS holds (57 rows of 6097 x 8768, six row tiles each: 49.5 us with two joins, 40.9 with one)
   const int room = (160 * 1024 / 8 - g4_x_lds(XT, 1, 6, G)) / 1024;
