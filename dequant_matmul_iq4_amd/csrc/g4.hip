@@ -8,7 +8,8 @@ namespace iq4 {
 // A wave makes a code tile: word b of lane 16 g + c has elements 8g .. 8g+7 of block b (of 32) of
 // row 16 rt + c, elements 0, 2, 4, 6 in the low half's nibbles and 1, 3, 5, 7 in the high half's.
 // Scales and zero points keep their order inside a tile's row.  What lies past n or k is zero.  Run
-// once per matrix; the source is read byte by byte, which spares it any alignment.
+// once per matrix; the source is read byte by byte, which spares it any alignment and bounds it (14336 x
+// 4096 25 us, 2.5 TB/s).
 __global__ void __launch_bounds__(256) g4_pack_kernel(G4Pack a) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int lane = (int)(i & 63), g = lane >> 4, c = lane & 15;

@@ -57,7 +57,7 @@ struct G4Args {
   int top_k;
 };
 int launch_g4_qmv(const G4Args& a, hipStream_t s);
-// by group; nv: operands of 16 rows of X (8 of binary32) that a workgroup multiplies at once, 1 or 2
+// by group
 int launch_g4_32(const G4Args& a, hipStream_t s);
 int launch_g4_64(const G4Args& a, hipStream_t s);
 int launch_g4_128(const G4Args& a, hipStream_t s);
