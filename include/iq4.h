@@ -565,6 +565,7 @@ int iq4_g4_pack_weights(const void* codes, int64_t ldq, const void* scales, int6
  *   x bfloat16   a group's sum is made as sum (16 + q) X - (16 + z) sum X: it rounds as sums of terms of up to
  *                31 |s X| do.
  * An infinity or a NaN of X makes what it makes in the formula, in its own row's results alone.
+ * Deterministic: the order of the sums depends on the sizes alone.
  *   packed  iq4_g4_pack_weights, 256-byte aligned.   scale_dtype: IQ4_F16 or IQ4_BF16.
  *   zeros   != 0 if packed with zero points.
  *   x       [m][ldx], y [m][ldy] of their dtypes (IQ4_F32, IQ4_F16, IQ4_BF16), element aligned,
@@ -638,7 +639,8 @@ int iq4_moe_combine_grad(const void* dout, int32_t dout_dtype, int64_t ldd, cons
  *   y       [m][ldy] of y_dtype, h rounded once, element aligned; or NULL.
  *   codes, scales  h (the float32 values) quantised as by iq4_quantize_rows, or codes NULL (fmt, ldq,
  *           scales, lds are then ignored); k % 32 == 0 with codes.  y or codes must be given.
- *   m >= 0 (0: no-op), m <= 2^21, k <= 2^20, m * k <= 2^34.  No output may overlap another buffer.
+ *   m >= 0 (0: no-op), m <= 2^21, k <= 2^20, m * k <= 2^34.  No output may overlap another buffer
+ *   (rows of one stride may lie between each other's).
  * Errors: IQ4_E_ARG, IQ4_E_ALIGN, IQ4_E_UNSUPPORTED.
  */
 int iq4_swiglu(const void* g, int64_t ldg, const void* u, int64_t ldu, int32_t dtype, int64_t m, int64_t k, void* y,
