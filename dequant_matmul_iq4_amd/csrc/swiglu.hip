@@ -7,8 +7,12 @@
 
 namespace iq4 {
 
-// e^-g in binary32: 2^-(g log2 e) with the product's rounding error carried along (its relative weight in
-// the result grows with |g|); beyond +-88 the power leaves binary32.
+// Below this e^-g comes near the end of binary32, while g e^g u may be a normal number (-91.8 for u = 1, -180 for
+// the largest): such elements are made again in 64 bits, behind a branch that a lane without one skips.
+constexpr float kDeep = -80.f;
+
+// e^-g in binary32 for g >= kDeep: 2^-(g log2 e) with the product's rounding error carried along (its relative
+// weight in the result grows with |g|); above 88 the power leaves binary32.
 __device__ __forceinline__ float power(float g) {
   const float x = fminf(fmaxf(-g, -88.f), 88.f);
   const float hi = x * 1.44269502f;
@@ -16,24 +20,30 @@ __device__ __forceinline__ float power(float g) {
   const float e = __builtin_amdgcn_exp2f(hi);
   return fmaf(e, lo * 0.693147182f, e);
 }
-// 1 / (1 + e^-g) in binary32.
-__device__ __forceinline__ float sigmoid(float g) {
-  const float s = __builtin_amdgcn_rcpf(1.0f + power(g));
-  return g < -88.f ? 0.f : s;
+// e^g for g < kDeep, where it is the sigmoid too (1 + e^g rounds to 1): a binary32 fraction of the same way, and the
+// power of two that only 64 bits hold.
+__device__ __forceinline__ double deep_power(float g) {
+  const float x = fmaxf(g, -1000.f);  // (2^-1443: zero)
+  const float hi = x * 1.44269502f;
+  const float lo = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -hi));
+  const float n = rintf(hi), e = __builtin_amdgcn_exp2f(hi - n);
+  return __builtin_amdgcn_ldexp((double)fmaf(e, lo * 0.693147182f, e), (int)n);
 }
-// g / (1 + e^-g) * u, all roundings but the last and the power's carried along: a row that is quantised
-// next makes a whole step of every error next to a border.  Its errors' root mean square is 0.42 of a last
+// 1 / (1 + e^-g) in binary32 for g >= kDeep.
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + power(g)); }
+// g / (1 + e^-g) * u for g >= kDeep, all roundings but the last and the power's carried along: a row that is
+// quantised next makes a whole step of every error next to a border.  Its errors' root mean square is 0.42 of a last
 // place; with the sum, the reciprocal and both products rounded it was 0.68, and of the formula's operations
 // one by one, each rounded right, it is 0.57.
 __device__ __forceinline__ float gated(float g, float u) {
   const float e = power(g);
-  float r = __builtin_amdgcn_rcpf(1.0f + e);
-  if (g < -88.f) r = 0.f;
+  const float r = __builtin_amdgcn_rcpf(1.0f + e);
   const float t = fmaf(-e, r, 1.0f - r);  // what r misses, relative to it
   const float a = g * r, h = a * u;
   const float rest = fmaf(fmaf(a, t, fmaf(g, r, -a)), u, fmaf(a, u, -h));
   return fabsf(h) < __builtin_inff() ? h + rest : h;
 }
+__device__ __forceinline__ float deep_gated(float g, float u) { return (float)(deep_power(g) * g * u); }
 
 // Eight elements a lane, whatever row they belong to.  Memory bounds it: 26048 rows of 768 in binary16
 // 23 us with y alone (5.2 TB/s), 3 of the few rows of a step.  Past the caches it is no faster.
@@ -51,8 +61,14 @@ __global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a, Pieces octs) 
     float g[8], u[8];
     load_piece<T, 8>(static_cast<const char*>(a.g) + r * a.ldg * (T == kF32 ? 4 : 2), c.at, c.left, g);
     load_piece<T, 8>(static_cast<const char*>(a.u) + r * a.ldu * (T == kF32 ? 4 : 2), c.at, c.left, u);
+    bool deep = false;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = gated(g[e], u[e]);
+    for (int e = 0; e < 8; ++e) v[e] = gated(g[e], u[e]), deep |= g[e] < kDeep;
+    if (__builtin_expect(deep, 0)) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (g[e] < kDeep) v[e] = deep_gated(g[e], u[e]);
+    }
     if (a.y) {
       char* y = static_cast<char*>(a.y) + r * a.ldy * (a.y_type == kF32 ? 4 : 2);
       if (a.y_type == kF32) store_piece<kF32, 8>(y, c.at, c.left, v);
@@ -97,6 +113,7 @@ __global__ void __launch_bounds__(256) swiglu_grad_kernel(SwigluGradArgs a, Piec
   if (r >= a.m) return;
   const Piece c = piece_of<P>(i - r * pieces.n, a.k);  // (what two pieces have is written twice, the same)
   float d[P], g[P], u[P], x[P], z[P];
+  bool deep = false;
   load_piece<TD, P, STREAM>(static_cast<const char*>(a.dh) + r * a.lddh * (TD == kF32 ? 4 : 2), c.at, c.left, d);
   load_piece<T, P, STREAM>(static_cast<const char*>(a.g) + r * a.ldg * kSize, c.at, c.left, g);
   load_piece<T, P, STREAM>(static_cast<const char*>(a.u) + r * a.ldu * kSize, c.at, c.left, u);
@@ -105,6 +122,15 @@ __global__ void __launch_bounds__(256) swiglu_grad_kernel(SwigluGradArgs a, Piec
     const float s = sigmoid(g[e]);
     z[e] = d[e] * (g[e] * s);
     x[e] = (d[e] * u[e]) * (s * fmaf(g[e], 1.0f - s, 1.0f));
+    deep |= g[e] < kDeep;
+  }
+  if (__builtin_expect(deep, 0)) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      if (!(g[e] < kDeep)) continue;
+      const double s = deep_power(g[e]) * d[e];
+      z[e] = (float)(s * g[e]), x[e] = (float)(s * (1.0 + g[e]) * u[e]);
+    }
   }
   store_piece<T, P, STREAM>(static_cast<char*>(a.dg) + r * a.lddg * kSize, c.at, c.left, x);
   store_piece<T, P, STREAM>(static_cast<char*>(a.du) + r * a.lddu * kSize, c.at, c.left, z);

@@ -634,7 +634,8 @@ int iq4_moe_combine_grad(const void* dout, int32_t dout_dtype, int64_t ldd, cons
 
 /*
  * SwiGLU between a layer's two products, h = g / (1 + e^-g) * u in binary32, and the quantisation of
- * its rows for the second product in the same pass.
+ * its rows for the second product in the same pass.  h is within 2^-20 of itself down to the smallest normal number,
+ * wherever e^-g may be (a closed gate's u may be large).
  *   g, u    [m][ldg], [m][ldu] of dtype (side by side in one buffer, or apart), element aligned.
  *   y       [m][ldy] of y_dtype, h rounded once, element aligned; or NULL.
  *   codes, scales  h (the float32 values) quantised as by iq4_quantize_rows, or codes NULL (fmt, ldq,

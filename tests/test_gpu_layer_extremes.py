@@ -1,0 +1,78 @@
+"""The group-scaled products, the experts' rows and SwiGLU where values lie at the ends of their types, or
+past them."""
+import numpy as np
+import pytest
+import torch
+
+import dequant_matmul_iq4_amd as iq4
+import oracle
+from gpu_util import dev, host, note
+from rows_util import FMT, HALF_STEP, TYPES, floats, row_buffers, rounder, same_rows
+
+pytestmark = pytest.mark.gpu
+F = np.float32
+
+
+# ---- SwiGLU -------------------------------------------------------------------------------
+
+
+def deep(seed, m, k, t):
+    """Gates from -75 to -180 (and some beyond), and values and gradients of any size the type has."""
+    rng = np.random.default_rng(seed)
+    top = 14 if t == "f16" else 126
+    g = rounder(t)(-rng.uniform(75, 180, (m, k)))
+    g.reshape(-1)[:: 7] = rounder(t)(rng.choice([-80.0, -88.0, -88.72, -91.8, -1000.0, -60000.0, 3.0], g.reshape(-1)[:: 7].shape))
+    wide = lambda: rounder(t)(rng.choice([1, -1], (m, k)) * 2.0 ** rng.uniform(-14, top, (m, k)))  # noqa: E731
+    return g, wide(), wide()
+
+
+def _step(t):
+    """Half a step of the type's subnormal numbers."""
+    f = torch.finfo(TYPES[t][1])
+    return float(f.smallest_normal) * float(f.eps) / 2
+
+
+@pytest.mark.parametrize("t,y_t", [("f32", "f32"), ("bf16", "f32"), ("f16", "f32"), ("bf16", "bf16"), ("f32", "bf16"), ("f16", "f16")])
+def test_swiglu_of_deeply_closed_gates(t, y_t):
+    """silu(g) falls to 2^-126 at -91.8 and is a part of h below: 2^-20 of h, as everywhere, and a rounding (2^-150 more
+    for the binary32 value behind one of 16 bits)."""
+    note(f"extremes: SwiGLU of closed gates, {t} -> {y_t}")
+    m, k = 9, 133
+    g, u, _ = deep(1, m, k, t)
+    y = torch.full((m, k), -7.0, dtype=TYPES[y_t][1], device="cuda")
+    iq4.iq4_swiglu(floats(g, t), k, floats(u, t), k, TYPES[t][0], m, k, y, TYPES[y_t][0], k)
+    got, want = host(y.double()), oracle.swiglu(g, u)
+    assert y_t == "f16" or (np.abs(want[g < -88]) > float(torch.finfo(TYPES[y_t][1]).smallest_normal)).sum() > 50
+    assert np.all(abs(want) < float(torch.finfo(TYPES[y_t][1]).max))
+    assert np.all(abs(got - want) <= (2.0**-20 + HALF_STEP[y_t]) * abs(want) + _step(y_t) + 2.0**-150)
+
+
+@pytest.mark.parametrize("dt,t", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")])
+def test_swiglu_gradient_of_deeply_closed_gates(dt, t):
+    """The same of the gradients, where 1 + g (1 - s) is 1 + g (or, at three, off by 2^-20 of 1 + |g|)."""
+    note(f"extremes: SwiGLU's gradient of closed gates, {dt}, {t}")
+    m, k = 9, 133
+    g, u, _ = deep(2, m, k, t)
+    dh = deep(3, m, k, dt)[2]
+    dh *= np.where(abs(dh * u) > 2.0**120, 2.0**-126, 1)  # (dh u is a binary32 number)
+    dh = rounder(dt)(dh)
+    dg, du = (torch.full((m, k), -7.0, dtype=TYPES[t][1], device="cuda") for _ in range(2))
+    iq4.iq4_swiglu_grad(floats(dh, dt), TYPES[dt][0], k, floats(g, t), k, floats(u, t), k, TYPES[t][0], m, k, dg, k, du, k)
+    wg, wu = oracle.swiglu_grad(dh, g, u)
+    small = _step(t) + 2.0**-149  # (and of one product on the way where the gate is open)
+    assert np.all(abs(host(du.double()) - wu) <= (2.0**-20 + HALF_STEP[t]) * abs(wu) + small)
+    assert np.all(abs(host(dg.double()) - wg) <= (2.0**-18 + HALF_STEP[t]) * abs(wg) + small)
+    assert ((g < -88) & (abs(wg) > 2.0**-126)).sum() > 50 and ((g < -88) & (abs(wu) > 2.0**-126)).sum() > 50
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_quantised_rows_of_deeply_closed_gates(fmt):
+    note(f"extremes: SwiGLU of closed gates -> {fmt}")
+    m, k = 5, 160
+    g, u, _ = deep(4, m, k, "bf16")
+    q, d, ldq, lds = row_buffers(fmt, m, k)
+    y = torch.zeros(m, k, device="cuda")
+    iq4.iq4_swiglu(floats(g, "bf16"), k, floats(u, "bf16"), k, iq4.IQ4_BF16, m, k, y, iq4.IQ4_F32, k, FMT[fmt], q, ldq, d, lds)
+    same_rows(fmt, k, q, d, oracle.quantize_rows(host(y), fmt))
+    want = oracle.swiglu(g, u)
+    assert np.all(abs(host(y) - want) <= 2.0**-19 * abs(want) + 2.0**-149)
