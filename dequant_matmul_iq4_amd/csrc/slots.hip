@@ -201,9 +201,14 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(SlotArgs a, uint32_t
         }
       }
       if (a.dw) {
-        if (c.twice) {  // and counted once
+        if (c.twice) {  // and counted once (both are zero: a zero times an infinity would not be)
 #pragma unroll
-          for (int e = 0; e < P; ++e) d[e] = e < c.twice ? 0.f : d[e];
+          for (int e = 0; e < P; ++e) {
+            if (e >= c.twice) continue;
+            d[e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j][e] = 0.f;
+          }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -239,12 +244,10 @@ __global__ void __launch_bounds__(256) combine_grad_short_kernel(SlotArgs a, uin
   const uint32_t q = threadIdx.x & 15;
   const bool live = t < a.n_tok && q < pieces;  // (the others take part in the sums)
   const Piece c = piece_of<P>(live ? q : 0, a.hidden);
-  float d[P], once[P];
+  float d[P];
 #pragma unroll
   for (int e = 0; e < P; ++e) d[e] = 0.f;
   if (live) load_piece<TD, P>(row_of<TD>(a.tok, t, a.ldt), c.at, c.left, d);
-#pragma unroll
-  for (int e = 0; e < P; ++e) once[e] = e < c.twice ? 0.f : d[e];
   for (int j0 = 0; j0 < a.top_k; j0 += 4) {
     Slots<4> s = slots_of<4>(a, t < a.n_tok ? t : 0, j0);
     float v[4][P];
@@ -261,9 +264,9 @@ __global__ void __launch_bounds__(256) combine_grad_short_kernel(SlotArgs a, uin
           for (int e = 0; e < P; ++e) o[e] = scaled(s.w[j], d[e]);
           store_piece<TR, P>(row_of<TR>(a.out, s.r[j], a.ldo), c.at, c.left, o);
         }
-        if (a.dw) {
+        if (a.dw) {  // (what two pieces have is counted once)
 #pragma unroll
-          for (int e = 0; e < P; ++e) dot = fmaf(once[e], v[j][e], dot);
+          for (int e = 0; e < P; ++e) dot = e < c.twice ? dot : fmaf(d[e], v[j][e], dot);
         }
       }
       dot += moved<0xB1>(dot);

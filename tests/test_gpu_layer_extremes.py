@@ -76,3 +76,37 @@ def test_quantised_rows_of_deeply_closed_gates(fmt):
     same_rows(fmt, k, q, d, oracle.quantize_rows(host(y), fmt))
     want = oracle.swiglu(g, u)
     assert np.all(abs(host(y) - want) <= 2.0**-19 * abs(want) + 2.0**-149)
+
+
+# ---- experts' rows ------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("top", [1, 9])
+@pytest.mark.parametrize("hidden", [3, 9, 37, 70, 131, 261, 1093])
+def test_an_infinity_at_every_place_of_a_row(hidden, top, t):
+    """dw of a row (or of a gradient) with an infinity anywhere is that infinity, where the kernel reads a place twice too."""
+    note(f"extremes: gradient of combine, an infinity in rows of {hidden}, top {top}, {t}")
+    rng = np.random.default_rng(hidden)
+    tokens = -(-hidden // top)
+    n = tokens * top
+    slot = rng.permutation(n).astype(np.int32).reshape(tokens, top)
+    x, do = (rounder(t)(rng.choice([1, -1], s) * rng.uniform(0.5, 2, s)) for s in ((n, hidden), (tokens, hidden)))
+    at = np.arange(n) % hidden
+    rows = x.copy()
+    rows[slot.reshape(-1), at] = np.inf
+
+    def dw_of(d, r):
+        dw = torch.full((tokens, top), -7.0, device="cuda")
+        iq4.iq4_moe_combine_grad(floats(d, t), TYPES[t][0], hidden, floats(r, t), TYPES[t][0], hidden, n, dev(slot), None, tokens, top, hidden, None,
+                                 0, dw)
+        return host(dw)
+
+    assert np.array_equal(dw_of(do, rows), (np.repeat(do, top, 0)[np.arange(n), at] * np.inf).reshape(tokens, top))
+    for i in range(0, hidden, 1 + hidden // 40):
+        d = do.copy()
+        d[:, i] = -np.inf
+        assert np.array_equal(dw_of(d, x), -np.inf * x[slot][:, :, i])
+        r = x.copy()
+        r[:, i] = np.nan
+        assert np.isnan(dw_of(do, r)).all()
