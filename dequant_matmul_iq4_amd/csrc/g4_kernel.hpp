@@ -12,7 +12,7 @@
 //               the group's sums of X, made once for all rows of W, are multiplied by -(16 + z) and begin
 //               d: 8 operations.  The sums are then some five times those of q - z, and so
 //               are their roundings, 2^-24 of them each.  An infinity leaves a NaN (infinity
-//               minus infinity): a result that is not finite is made again, one by one, without this.
+//               minus infinity): a result that is not finite is made again without this, in 64 bits, by a wave.
 //   binary32 X  two binary16 numbers, the value rounded to eleven bits and what is left, rounded
 //               likewise; a wave has a slice of k, and there a row's values are multiplied by the power
 //               of two that brings the largest to 2^14 .. 2^15, and its sums divided by it.  Within 2^-23
@@ -91,30 +91,54 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// One result by itself, from the definition.
+// Whether a row of X holds a NaN (all lanes of a wave, four loads of each under way).
 template <int XT>
-__device__ float g4_single(const G4Args& a, const uint8_t* W, int64_t x_row, int64_t r) {
-  const int64_t rt = r >> 4, kt_n = g4_k_tiles(a.k);
-  const int c = (int)(r & 15), sets = 128 / a.group;
-  const uint16_t* ss = reinterpret_cast<const uint16_t*>(W + g4_code_plane(a.n, a.k));
-  const uint8_t* zs = W + g4_code_plane(a.n, a.k) + g4_scale_plane(a.n, a.k, a.group);
-  float acc = 0.f;
+__device__ bool g4_nan(const G4Args& a, int64_t x_row) {
+  const int lane = threadIdx.x & 63, K = (int)a.k;
+  const char* row = static_cast<const char*>(a.x) + x_row * a.ldx * (XT == kF32 ? 4 : 2);
+  bool found = false;
 #pragma nounroll
-  for (int64_t k0 = 0; k0 < a.k; k0 += a.group) {
-    const int64_t tile = rt * kt_n + (k0 >> 7), at = (tile * 16 + c) * sets + (k0 & 127) / a.group;
-    const float s = a.scale_type == kF16 ? h2f(ss[at]) : __uint_as_float((uint32_t)ss[at] << 16);
-    const int z = a.zeros ? zs[at] : 8;
-    float d = 0.f;
-#pragma nounroll
-    for (int64_t k = k0; k < min(k0 + a.group, a.k); ++k) {
-      const int b = (int)(k >> 5 & 3), g = (int)(k >> 3 & 3), e = (int)(k & 7);
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(W + tile * kG4TileBytes + (16 * g + c) * 16 + 4 * b);
-      const uint16_t h = static_cast<const uint16_t*>(a.x)[x_row * a.ldx + k];
-      d = fmaf((float)((int)(w >> (16 * (e & 1) + 4 * (e >> 1)) & 15u) - z), __uint_as_float((uint32_t)h << 16), d);
-    }
-    acc = fmaf(s, d, acc);
+  for (int k0 = 8 * lane; k0 < K; k0 += 4 * 512) {
+    float x[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_piece<XT, 8>(row, min(k0 + 512 * i, K - 8), 8, x[i]);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) found |= x[i / 8][i % 8] != x[i / 8][i % 8];
   }
-  return acc;
+  return __ballot(found) != 0;
+}
+// The results of one row of X in a row tile, from the definition: in 64 bits, in a fixed order, column c in the lanes
+// (g, c).
+template <int XT, int G>
+__device__ float g4_again(const G4Args& a, const uint8_t* W, int64_t x_row, int64_t rt) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, K = (int)a.k;
+  constexpr int kSets = 128 / G;
+  const int64_t kt_n = g4_k_tiles(a.k);
+  const uint8_t* ss = W + g4_code_plane(a.n, a.k);
+  const uint8_t* zs = ss + g4_scale_plane(a.n, a.k, G);
+  const char* row = static_cast<const char*>(a.x) + x_row * a.ldx * (XT == kF32 ? 4 : 2);
+  double sum = 0.0;
+#pragma unroll 2
+  for (int kt = 0; kt < (int)kt_n; ++kt) {
+    const int64_t tile = rt * kt_n + kt;
+    const u32x4 w = *reinterpret_cast<const u32x4*>(W + tile * kG4TileBytes + 16 * lane);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int k = 128 * kt + 32 * b + 8 * g;
+      const int64_t at = (tile * 16 + c) * kSets + 32 * b / G;
+      const uint16_t h = reinterpret_cast<const uint16_t*>(ss)[at];
+      const double s = a.scale_type == kF16 ? h2f(h) : __uint_as_float((uint32_t)h << 16);
+      const int z = a.zeros ? zs[at] : 8;
+      float x[8];
+      load_piece<XT, 8>(row, min(k, K - 8), 8, x);
+      double d = 0.0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d = fma((double)((int)(w[b] >> (16 * (e & 1) + 4 * (e >> 1)) & 15u) - z), (double)x[e], d);
+      sum = k < K ? fma(s, d, sum) : sum;
+    }
+  }
+  sum += __shfl_xor(sum, 16);
+  return (float)(sum + __shfl_xor(sum, 32));
 }
 
 // How a call's work is dealt out (set by the launcher).
@@ -424,11 +448,10 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
       *to = s;
     }
   };
+  bool odd = false;  // a result of this lane is not finite
   auto store = [&](int t, int64_t at, float v) {  // row t of the tile, column `at`
     if (t >= rows || at >= a.n) return;
-    if constexpr (XT == kBF16) {
-      if (__builtin_expect(!(fabsf(v) < __builtin_inff()), 0)) v = g4_single<XT>(a, W, x_row(t), at);
-    }
+    if constexpr (XT == kBF16) odd |= !(fabsf(v) < __builtin_inff());
     const int64_t o = (int64_t)(row0 + t) * a.ldy + at;
     if (a.y_type == kF32) static_cast<float*>(a.y)[o] = v;
     else static_cast<uint16_t*>(a.y)[o] = (uint16_t)(a.y_type == kF16 ? pack2<kF16>(v, 0.f) : pack2<kBF16>(v, 0.f));
@@ -506,6 +529,39 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
       }
     }
     if (b + plan.rb < last) lds_barrier();  // the sums are read before the next ones are written
+  }
+  if constexpr (XT == kBF16) {
+    // Results that are not finite are made again (here, where the operands' registers are free), each from where the
+    // lane stored it; those of a row that holds a NaN (a batch's padding may be full of them) are right, and the
+    // first of them that a wave looks at says so for all.  (Eight of 16 rows of 4096 x 4096 with an infinity 147 us, with
+    // a NaN 15, with neither 7.)
+    if (__builtin_expect(__ballot(odd) == 0, 1)) return;
+    uint32_t nan_rows = 0;
+    for (int b = first; b < last; b += plan.rb)
+      for (int q = slice; q < min(plan.rb, last - b) * NV; q += KS) {
+        const int64_t rt = b + q / NV;
+#pragma nounroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = 16 * (q % NV) + 4 * g + e;
+          bool again = false;
+          if (t < rows && rt * 16 + c < a.n && !(nan_rows >> t & 1)) {
+            const int64_t o = (int64_t)(row0 + t) * a.ldy + rt * 16 + c;
+            if (a.y_type == kF32) again = !(fabsf(static_cast<const float*>(a.y)[o]) < __builtin_inff());
+            else again = (~static_cast<const uint16_t*>(a.y)[o] & (a.y_type == kF16 ? 0x7C00 : 0x7F80)) == 0;
+          }
+#pragma nounroll
+          for (int u = 0; u < 4; ++u) {  // the four rows of this e
+            if ((__ballot(again) >> (16 * u) & 0xFFFF) == 0) continue;
+            const int at = 16 * (q % NV) + 4 * u + e;
+            if (g4_nan<XT>(a, x_row(at))) {
+              nan_rows |= 1u << at;
+            } else {
+              const float v = g4_again<XT, G>(a, W, x_row(at), rt);
+              if (again && g == u) store(t, rt * 16 + c, v);
+            }
+          }
+        }
+      }
   }
 }
 

@@ -8,6 +8,7 @@ import dequant_matmul_iq4_amd as iq4
 import oracle
 from gpu_util import dev, host, note
 from rows_util import FMT, HALF_STEP, TYPES, floats, row_buffers, rounder, same_rows
+from test_gpu_g4 import pack, weights
 
 pytestmark = pytest.mark.gpu
 F = np.float32
@@ -110,3 +111,82 @@ def test_an_infinity_at_every_place_of_a_row(hidden, top, t):
         r = x.copy()
         r[:, i] = np.nan
         assert np.isnan(dw_of(do, r)).all()
+
+
+# ---- group-scaled products ----------------------------------------------------------------
+
+
+def _product(p, n, k, group, z, x, t, y_t="f32"):
+    y = torch.full((len(x), n), -7.0, dtype=TYPES[y_t][1], device="cuda")
+    iq4.iq4_g4_qmv(p, n, k, group, iq4.IQ4_F16, z is not None, floats(x, t), TYPES[t][0], k, len(x), y, TYPES[y_t][0], n)
+    return host(y.double())
+
+
+# one operand of rows and two; short rows, long ones, ones in slices; a last group, row tile and code tile that are not full
+ODD = [(33, 544, 32, 3), (33, 544, 32, 20), (2100, 4096, 64, 33), (4100, 160, 128, 21), (600, 8768, 32, 17), (70, 6240, 128, 5), (2105, 2048, 32, 70)]
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("n,k,group,m", ODD)
+def test_infinities_and_nan_in_every_form_of_the_product(n, k, group, m, t):
+    """Rows with an infinity, with two of either sign, with a NaN, with the largest numbers: each result what the formula says, the
+    other rows' whole numbers exact."""
+    note(f"extremes: infinities and NaN, {m} x {n} x {k} by {group}, {t}")
+    codes, s, z = weights(n + k, n, k, group, True, "f16", True)
+    p, w = pack(codes, s, z, group, "f16"), oracle.g4_weights(codes, s, z, group)
+    rng = np.random.default_rng(m)
+    x = rng.integers(-4, 5, (m, k)).astype(np.float64)
+    for y_t in ("f32", t):
+        inf, both, nan = rng.permutation(m)[:3]
+        v = x.copy()
+        i, j, l = rng.integers(0, k, 3)
+        v[inf, i], v[both, j], v[both, (j + k // 2) % k], v[nan, l] = -np.inf, np.inf, -np.inf, np.nan
+        got = _product(p, n, k, group, z, v, t, y_t)
+        rest = np.delete(np.arange(m), [inf, both, nan])
+        assert np.array_equal(got[rest], rounder(y_t)(oracle.g4_product(w, v[rest])))
+        assert np.isnan(got[nan]).all()
+        with np.errstate(invalid="ignore"):
+            assert np.array_equal(got[inf], -np.inf * w[:, i], equal_nan=True)
+            assert np.array_equal(got[both], np.inf * w[:, j] - np.inf * w[:, (j + k // 2) % k], equal_nan=True)
+
+
+def test_large_bfloat16_sums_that_cancel():
+    """The terms that 16 + q makes pass binary32's largest number where those of q - z do not."""
+    note("extremes: bfloat16 values near the largest")
+    n, k, group, m = 50, 1024, 64, 18
+    codes, s, z = weights(3, n, k, group, True, "f16", True)
+    p, w = pack(codes, s, z, group, "f16"), oracle.g4_weights(codes, s, z, group)
+    x = np.random.default_rng(4).integers(-4, 5, (m, k)).astype(np.float64)
+    x[::3] *= 2.0**113  # |y| <= 1024 * 30 * 4 * 2^113 < 2^128
+    assert np.array_equal(_product(p, n, k, group, z, x, "bf16"), rounder("f32")(oracle.g4_product(w, x)))
+    x[1::3] *= 2.0**124
+    got, want = _product(p, n, k, group, z, x, "bf16"), oracle.g4_product(w, x)
+    with np.errstate(over="ignore"):
+        assert np.array_equal(got, want.astype(F))
+    assert np.isinf(got[1::3]).any() and np.isfinite(got[1::3]).any()
+
+
+@pytest.mark.parametrize("what", [np.nan, np.inf])
+@pytest.mark.parametrize("t", list(TYPES))
+def test_rows_that_are_not_finite_cost_no_more_than_many_rows(t, what):
+    """A batch whose padding holds NaN: a few times the call without (each such result once took a lane through all of k)."""
+    note(f"extremes: time of rows that are {what}, {t}")
+    n, k, group, m = 4096, 4096, 64, 16
+    codes, s, z = weights(5, n, k, group, True, "f16", True)
+    p = pack(codes, s, z, group, "f16")
+    x = floats(np.ones((m, k)), t)
+    bad = x.clone()
+    bad[1:9, 77] = what
+    y = torch.zeros(m, n, dtype=TYPES[t][1], device="cuda")
+    times = []
+    for v in (x, bad, x, bad):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        for i in range(6):
+            if i == 1:
+                a.record()
+            iq4.iq4_g4_qmv(p, n, k, group, iq4.IQ4_F16, 1, v, TYPES[t][0], k, m, y, TYPES[t][0], n)
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) / 5 * 1e3)
+    note(f"  {times[2]:.1f} us, {times[3]:.1f} with them")
+    assert times[3] <= (20 if np.isnan(what) else 100) * times[2]
