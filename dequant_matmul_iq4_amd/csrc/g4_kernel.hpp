@@ -18,6 +18,8 @@
 //               of two that brings the largest to 2^14 .. 2^15, and its sums divided by it.  Within 2^-23
 //               of the value (a tie of what is left), or 2^-39 of the slice's largest (half a step of the
 //               smallest).  Each of the two is a row of the operand; their sums are joined before they are divided.
+//               An infinity's rest is a NaN, and scales near the largest number may take the multiplied sums past
+//               it: again a result that is not finite is made again.
 //
 // Operands of v_mfma_f32_16x16x32 (lane l = 16 g + c): the activations are the first one, rows by c;
 // the weights the second, 16 rows of W by c, so that a lane's scale is that of the row whose codes
@@ -91,39 +93,33 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Whether a row of X holds a NaN (all lanes of a wave, four loads of each under way).
+// The largest magnitude, by its bits, of eight elements from k on of a row of X: an infinity is above all numbers, and a
+// NaN above that.
 template <int XT>
-__device__ bool g4_nan(const G4Args& a, int64_t x_row) {
-  const int lane = threadIdx.x & 63, K = (int)a.k;
-  const char* row = static_cast<const char*>(a.x) + x_row * a.ldx * (XT == kF32 ? 4 : 2);
-  bool found = false;
-#pragma nounroll
-  for (int k0 = 8 * lane; k0 < K; k0 += 4 * 512) {
-    float x[4][8];
+__device__ __forceinline__ uint32_t g4_top(const char* row, int k, int K) {
+  float v[8];
+  load_piece<XT, 8>(row, min(k, K - 8), 8, v);
+  uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_piece<XT, 8>(row, min(k0 + 512 * i, K - 8), 8, x[i]);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) found |= x[i / 8][i % 8] != x[i / 8][i % 8];
-  }
-  return __ballot(found) != 0;
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+  return k < K ? top : 0u;
 }
 // The results of one row of X in a row tile, from the definition: in 64 bits, in a fixed order, column c in the lanes
-// (g, c).
+// (g, c).  infinite: the row holds an infinity, so that only the code tiles where it has one count.
 template <int XT, int G>
-__device__ float g4_again(const G4Args& a, const uint8_t* W, int64_t x_row, int64_t rt) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, K = (int)a.k;
+__device__ float g4_again(const G4Args& a, const uint8_t* W, int64_t x_row, int64_t rt, bool infinite, int lane) {
+  const int g = lane >> 4, c = lane & 15, K = (int)a.k;
   constexpr int kSets = 128 / G;
-  const int64_t kt_n = g4_k_tiles(a.k);
+  const int kt_n = g4_k_tiles(a.k);
   const uint8_t* ss = W + g4_code_plane(a.n, a.k);
   const uint8_t* zs = ss + g4_scale_plane(a.n, a.k, G);
   const char* row = static_cast<const char*>(a.x) + x_row * a.ldx * (XT == kF32 ? 4 : 2);
   double sum = 0.0;
-#pragma unroll 2
-  for (int kt = 0; kt < (int)kt_n; ++kt) {
+  auto add = [&](int kt) {
     const int64_t tile = rt * kt_n + kt;
-    const u32x4 w = *reinterpret_cast<const u32x4*>(W + tile * kG4TileBytes + 16 * lane);
-#pragma unroll
+#pragma unroll 2
     for (int b = 0; b < 4; ++b) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(W + tile * kG4TileBytes + 16 * lane + 4 * b);
       const int k = 128 * kt + 32 * b + 8 * g;
       const int64_t at = (tile * 16 + c) * kSets + 32 * b / G;
       const uint16_t h = reinterpret_cast<const uint16_t*>(ss)[at];
@@ -133,9 +129,17 @@ __device__ float g4_again(const G4Args& a, const uint8_t* W, int64_t x_row, int6
       load_piece<XT, 8>(row, min(k, K - 8), 8, x);
       double d = 0.0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d = fma((double)((int)(w[b] >> (16 * (e & 1) + 4 * (e >> 1)) & 15u) - z), (double)x[e], d);
+      for (int e = 0; e < 8; ++e) d = fma((double)((int)(w >> (16 * (e & 1) + 4 * (e >> 1)) & 15u) - z), (double)x[e], d);
       sum = k < K ? fma(s, d, sum) : sum;
     }
+  };
+#pragma nounroll
+  for (int kt = 0; kt < kt_n; kt += 4) {
+    // (16 lanes have a code tile's elements)
+    const uint64_t who = infinite ? __ballot(g4_top<XT>(row, 128 * kt + 8 * lane, K) >= 0x7F800000u) : ~0ull;
+#pragma nounroll
+    for (int h = 0; h < 4; ++h)
+      if (kt + h < kt_n && (who >> (16 * h) & 0xFFFF)) add(kt + h);
   }
   sum += __shfl_xor(sum, 16);
   return (float)(sum + __shfl_xor(sum, 32));
@@ -358,13 +362,6 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
               rest[2 * i] = less_lo(x[2 * i], h[i]);
               rest[2 * i + 1] = less_hi(x[2 * i + 1], h[i]);
             }
-            if (__builtin_expect(__ballot(s == 0x1p-114f) != 0, 0)) {  // a row holds an infinity: it has no rest
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if (fabsf(x[i]) == __builtin_inff()) rest[i] = 0.f;
-                asm volatile("" : "+v"(rest[i]));  // (keeps this a branch: as selects it costs every call)
-              }
-            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) m[i] = pack2<kF16>(rest[2 * i], rest[2 * i + 1]);
             uint8_t* to = mine + (4 * p + g) * kG4StageRow + 16 * c;
@@ -448,10 +445,9 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
       *to = s;
     }
   };
-  bool odd = false;  // a result of this lane is not finite
+  uint64_t odd = 0;  // lanes that had a result that is not finite
   auto store = [&](int t, int64_t at, float v) {  // row t of the tile, column `at`
     if (t >= rows || at >= a.n) return;
-    if constexpr (XT == kBF16) odd |= !(fabsf(v) < __builtin_inff());
     const int64_t o = (int64_t)(row0 + t) * a.ldy + at;
     if (a.y_type == kF32) static_cast<float*>(a.y)[o] = v;
     else static_cast<uint16_t*>(a.y)[o] = (uint16_t)(a.y_type == kF16 ? pack2<kF16>(v, 0.f) : pack2<kBF16>(v, 0.f));
@@ -523,6 +519,10 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
       }
       const int v = q % NV;
       const int64_t at = (int64_t)(b + q / NV) * 16 + c;
+      if constexpr (XT != kF16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) odd |= __ballot(!(fabsf(s[e]) < __builtin_inff()) && (f32 ? 8 : 16) * v + 4 * g + e < rows);
+      }
       if (!f32 || g < 2) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) store((f32 ? 8 : 16) * v + 4 * g + e, at, s[e]);
@@ -530,35 +530,45 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
     }
     if (b + plan.rb < last) lds_barrier();  // the sums are read before the next ones are written
   }
-  if constexpr (XT == kBF16) {
+  if constexpr (XT != kF16) {
     // Results that are not finite are made again (here, where the operands' registers are free), each from where the
-    // lane stored it; those of a row that holds a NaN (a batch's padding may be full of them) are right, and the
-    // first of them that a wave looks at says so for all.  (Eight of 16 rows of 4096 x 4096 with an infinity 147 us, with
-    // a NaN 15, with neither 7.)
-    if (__builtin_expect(__ballot(odd) == 0, 1)) return;
-    uint32_t nan_rows = 0;
+    // lane stored it; those of a row that holds a NaN (a batch's padding may be full of them) are right.  What a row
+    // holds a wave looks up once.  (16 rows of 4096 x 4096, eight of them with an infinity 47 us, with a NaN 19, with
+    // neither 7 in bfloat16 and 9 in binary32.)
+    if (__builtin_expect(odd == 0, 1)) return;
+    constexpr int kRows = f32 ? 8 : 16;  // of an operand
+    // (counted anew: of the lane number above, what is made of it here would be made before, and kept)
+    const int lane = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+    const int g = lane >> 4, c = lane & 15;
+    uint32_t known = 0, nan = 0, inf = 0;
     for (int b = first; b < last; b += plan.rb)
       for (int q = slice; q < min(plan.rb, last - b) * NV; q += KS) {
         const int64_t rt = b + q / NV;
 #pragma nounroll
         for (int e = 0; e < 4; ++e) {
-          const int t = 16 * (q % NV) + 4 * g + e;
+          const int t = kRows * (q % NV) + 4 * g + e;
           bool again = false;
-          if (t < rows && rt * 16 + c < a.n && !(nan_rows >> t & 1)) {
+          if (4 * g < kRows && t < rows && rt * 16 + c < a.n && !(nan >> t & 1)) {
             const int64_t o = (int64_t)(row0 + t) * a.ldy + rt * 16 + c;
             if (a.y_type == kF32) again = !(fabsf(static_cast<const float*>(a.y)[o]) < __builtin_inff());
             else again = (~static_cast<const uint16_t*>(a.y)[o] & (a.y_type == kF16 ? 0x7C00 : 0x7F80)) == 0;
           }
 #pragma nounroll
-          for (int u = 0; u < 4; ++u) {  // the four rows of this e
+          for (int u = 0; u < kRows / 4; ++u) {  // the rows of this e
             if ((__ballot(again) >> (16 * u) & 0xFFFF) == 0) continue;
-            const int at = 16 * (q % NV) + 4 * u + e;
-            if (g4_nan<XT>(a, x_row(at))) {
-              nan_rows |= 1u << at;
-            } else {
-              const float v = g4_again<XT, G>(a, W, x_row(at), rt);
-              if (again && g == u) store(t, rt * 16 + c, v);
+            const int at = kRows * (q % NV) + 4 * u + e;
+            const int64_t xr = x_row(at);
+            if (!(known >> at & 1)) {
+              uint32_t top = 0;
+              const char* row = static_cast<const char*>(a.x) + xr * a.ldx * (f32 ? 4 : 2);
+              for (int k = 8 * lane; k < K; k += 512) top = max(top, g4_top<XT>(row, k, K));
+              known |= 1u << at;
+              if (__ballot(top > 0x7F800000u)) nan |= 1u << at;
+              else if (__ballot(top == 0x7F800000u)) inf |= 1u << at;
             }
+            if (nan >> at & 1) continue;
+            const float v = g4_again<XT, G>(a, W, xr, rt, inf >> at & 1, lane);
+            if (again && g == u) store(t, rt * 16 + c, v);
           }
         }
       }

@@ -564,9 +564,10 @@ int iq4_g4_pack_weights(const void* codes, int64_t ldq, const void* scales, int6
  *                itself or 2^-39 of the largest magnitude in the slice, whichever is more.
  *   x bfloat16   a group's sum is made as sum (16 + q) X - (16 + z) sum X: it rounds as sums of terms of up to
  *                31 |s X| do.
- * An infinity or a NaN of X makes what it makes in the formula, in its own row's results alone.  (x bfloat16: a
- * result that is not finite is made again from the formula, in 64 bits; eight of 16 rows of 4096 x 4096 with an
- * infinity each take 147 us in all for 7, with a NaN 15.)
+ * An infinity or a NaN of X makes what it makes in the formula, in its own row's results alone.  (x binary32 or
+ * bfloat16: a result that is not finite is made again from the formula, in 64 bits, so that sums that pass the largest
+ * number on the way do not count.  16 rows of 4096 x 4096, eight of them with an infinity each: 47 us for 7 to 9; with
+ * a NaN 19.)
  * Deterministic: the order of the sums depends on the sizes alone.
  *   packed  iq4_g4_pack_weights, 256-byte aligned.   scale_dtype: IQ4_F16 or IQ4_BF16.
  *   zeros   != 0 if packed with zero points.

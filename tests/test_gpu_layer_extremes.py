@@ -166,6 +166,22 @@ def test_large_bfloat16_sums_that_cancel():
     assert np.isinf(got[1::3]).any() and np.isfinite(got[1::3]).any()
 
 
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("n,k,group,m", ODD)
+def test_scales_near_the_largest_number(n, k, group, m, t):
+    """Scales of some 2^105 by values of some 2^-100, results of ordinary size: every product and sum is a binary32 number,
+    whatever power of two the values are held with on the way.  (The bfloat16 kernel holds them as they are.)"""
+    note(f"extremes: scales of 2^105, {m} x {n} x {k} by {group}, {t}")
+    codes, s, z = weights(n * k, n, k, group, True, "bf16", True)
+    p, w = pack(codes, s * 2.0**105, z, group, "bf16"), oracle.g4_weights(codes, s * 2.0**105, z, group)
+    x = np.random.default_rng(m).integers(-4, 5, (m, k)) * 2.0**-100
+    x[1::3] *= 2.0**90   # |y| < 2^(105 + 23 - 10)
+    x[2::3] *= 2.0**-27  # (2^-127 .. 2^-125: subnormal)
+    y = torch.full((m, n), -7.0, device="cuda")
+    iq4.iq4_g4_qmv(p, n, k, group, iq4.IQ4_BF16, 1, floats(x, t), TYPES[t][0], k, m, y, iq4.IQ4_F32, n)
+    assert np.array_equal(host(y), oracle.g4_product(w, x))
+
+
 @pytest.mark.parametrize("what", [np.nan, np.inf])
 @pytest.mark.parametrize("t", list(TYPES))
 def test_rows_that_are_not_finite_cost_no_more_than_many_rows(t, what):
