@@ -18,8 +18,10 @@ __device__ __forceinline__ int scan64(int v) {
 }
 
 // Tile t of `bm` rows, expert by expert (an expert's last tile may be partial): its expert, first
-// row and rows.  False: there are fewer tiles.  Offsets are clamped to ascending ones in [0, m]:
-// whatever they hold, no row outside is named.  128 experts at a time, their loads together.
+// row and rows.  False: there are fewer tiles.  128 experts at a time, their loads together.  Offsets are
+// clamped to [0, m], an expert's end to its start or more: whatever they hold, no row outside is named.  Ones that
+// do not ascend may name a row twice, or more tiles than there are columns for them: such rows are unspecified (a
+// look at their order here costs every call 0.06 us).
 __device__ __forceinline__ bool expert_tile(const int32_t* offsets, int n_expert, int m, int bm, int t, int& e, int& row0,
                                             int& rows) {
   const int lane = threadIdx.x & 63;

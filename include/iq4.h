@@ -584,7 +584,8 @@ int iq4_g4_qmv(const void* packed, int64_t n, int64_t k, int32_t group, int32_t 
 /*
  * The same product with one matrix per expert, output rows sorted by expert: Y[i] = W_e X[row(i)],
  * offsets[e] <= i < offsets[e + 1], row(i) = pairs[i] / top_k, or i if pairs is NULL (offsets and
- * pairs as for iq4_mx_grouped_gemm: iq4_moe_gather writes them; values out of range are clamped).
+ * pairs as for iq4_mx_grouped_gemm: iq4_moe_gather writes them).  Values out of range are clamped: ascending offsets to
+ * 0 .. n_pairs, row(i) to the rows of x.  Where offsets do not ascend, the rows of y are unspecified; nothing else is touched.
  *   packed  n_expert packed n x k matrices, expert e at e * iq4_g4_packed_bytes(n, k, group, zeros).
  *   x       n_rows rows.   y  [n_pairs][ldy]; rows from offsets[n_expert] on are left as they were.
  * Errors: as iq4_g4_qmv; IQ4_E_ARG too if x has too few rows for n_pairs.

@@ -8,7 +8,7 @@ import dequant_matmul_iq4_amd as iq4
 import oracle
 from gpu_util import dev, host, note
 from rows_util import FMT, HALF_STEP, TYPES, floats, row_buffers, rounder, same_rows
-from test_gpu_g4 import pack, weights
+from test_gpu_g4 import bank, pack, weights
 
 pytestmark = pytest.mark.gpu
 F = np.float32
@@ -206,3 +206,44 @@ def test_rows_that_are_not_finite_cost_no_more_than_many_rows(t, what):
         times.append(a.elapsed_time(b) / 5 * 1e3)
     note(f"  {times[2]:.1f} us, {times[3]:.1f} with them")
     assert times[3] <= (20 if np.isnan(what) else 100) * times[2]
+
+
+def _offset_lists(e, m):
+    rng = np.random.default_rng(e)
+    yield np.linspace(0, m, e + 1).astype(int)
+    yield np.concatenate([[-5], np.linspace(0, m, e).astype(int)])  # below the rows, and past them
+    yield np.linspace(3, m + 90, e + 1).astype(int)
+    yield np.sort(rng.choice([-(2**31), -1, 0, 9, m, m + 1, 2**31 - 1], e + 1))
+    for v in (2**31 - 1, -(2**31), m):
+        yield np.full(e + 1, v)
+    yield np.linspace(m, 0, e + 1).astype(int)  # from here on they fall, somewhere at least
+    for _ in range(3):
+        yield rng.integers(-m, 2 * m, e + 1)
+    yield rng.choice([2**31 - 1, -(2**31), 0, m], e + 1)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("e", [1, 4, 64, 130, 300])
+def test_offsets_and_pairs_of_any_kind(e, t):
+    """Offsets that ascend count within the rows, pair ids name a row of x whatever they are; rows without an expert are left
+    alone, and what lies around the rows always."""
+    n, k, group, m, top, around = 16, 32, 32, 61, 2, 40
+    p, ws = bank(7, e, n, k, group, True, "f16")
+    rng = np.random.default_rng(e)
+    x = rng.integers(-4, 5, (-(-m // top), k)).astype(np.float64)
+    for i, offsets in enumerate(_offset_lists(e, m)):
+        note(f"extremes: {e} experts, offsets of kind {i}, {t}")
+        pairs = rng.integers(0, m, m) if i % 2 else rng.choice([-1, 1000, 2**31 - 1, -(2**31), 7, -7], m)
+        big = torch.full((m + 2 * around, n + 3), -7.0, device="cuda")
+        y = big[around:]
+        iq4.iq4_g4_grouped_qmv(p, e, n, k, group, iq4.IQ4_F16, 1, floats(x, t), TYPES[t][0], k, len(x), dev(offsets.astype(np.int32)),
+                               dev(pairs.astype(np.int32)), top, m, y, iq4.IQ4_F32, n + 3)
+        got = host(big)
+        assert np.all(got[:around] == -7.0) and np.all(got[around + m:] == -7.0) and np.all(got[:, n:] == -7.0)
+        if np.all(offsets[1:] >= offsets[:-1]):
+            want = np.full((m, n), -7.0)
+            at = offsets.clip(0, m)
+            src = x[np.trunc(pairs / top).clip(0, len(x) - 1).astype(int)]
+            for j in range(e):
+                want[at[j]: at[j + 1]] = oracle.g4_product(ws[j], src[at[j]: at[j + 1]])
+            assert np.array_equal(got[around: around + m, :n], want), i
