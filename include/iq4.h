@@ -568,7 +568,9 @@ int iq4_g4_pack_weights(const void* codes, int64_t ldq, const void* scales, int6
  * bfloat16: a result that is not finite is made again from the formula, in 64 bits, so that sums that pass the largest
  * number on the way do not count.  16 rows of 4096 x 4096, eight of them with an infinity each: 47 us for 7 to 9; with
  * a NaN 19.)
- * Deterministic: the order of the sums depends on the sizes alone.
+ * Deterministic: the order of the sums depends on the sizes alone.  The number of rows is one of them: up to eight rows
+ * of binary32, or 16 of 16 bits, each row is bit for bit what it is by itself; with more, and by expert, a row's
+ * roundings may differ with the number of rows (pairs, experts) it comes with.
  *   packed  iq4_g4_pack_weights, 256-byte aligned.   scale_dtype: IQ4_F16 or IQ4_BF16.
  *   zeros   != 0 if packed with zero points.
  *   x       [m][ldx], y [m][ldy] of their dtypes (IQ4_F32, IQ4_F16, IQ4_BF16), element aligned,

@@ -133,3 +133,18 @@ def test_infinities_and_nan_by_expert(t):
             else:
                 want = oracle.g4_product(ws[j], x[r][None])[0]
             assert np.array_equal(got[i], want, equal_nan=True), (j, i)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("n,k,group", [(40, 96, 32), (520, 1024, 64), (70000, 512, 128), (4096, 4096, 128), (100, 5024, 64), (300, 7200, 32), (2560, 6144, 32)])
+def test_a_row_alone_is_the_row_among_few(n, k, group, t):
+    """Up to eight rows of binary32, or 16 of 16 bits, against one matrix: bit for bit what each is by itself."""
+    note(f"g4 plans: rows alone and together, {n} x {k} by {group}, {t}")
+    most = 8 if t == "f32" else 16
+    codes, s, z = weights(n, n, k, group, True, "f16", False)
+    p = pack(codes, s, z, group, "f16")
+    x = rounder(t)(np.random.default_rng(k).standard_normal((most, k)))
+    together = [product(p, n, k, group, z, "f16", x[:m], t, "f32") for m in (2, 4, 7, most)]
+    for r in range(0, most, 3 if n > 9999 else 1):
+        alone = product(p, n, k, group, z, "f16", x[r:r + 1], t, "f32")[0]
+        assert all(np.array_equal(y[r], alone) for y in together if r < len(y)), r
