@@ -576,17 +576,20 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
 }
 
 template <int XT, int NV, int SX, int G, bool CHUNKS = false>
-static int launch_g4_kernel(const G4Args& a, G4Plan p, hipStream_t s) {
+static int launch_g4_kernel(const G4Args& a, G4Plan p, int64_t places, hipStream_t s) {
   // (at most 4096 workgroups or one a tile of X, 2^21: far from a grid's 2^32 threads)
   p.kt_n = g4_k_tiles(a.k);
   p.rt_n = (int)g4_row_tiles(a.n);
   p.y = p.cols < 32768 ? p.cols : 32768;
   p.chunks = (p.kt_n + p.ks * SX - 1) / (p.ks * SX);
   // Workgroups go to the eight XCDs in turn: with a multiple of eight along the row tiles, those that have the same
-  // weights meet in one L2 (60 rows of 13000 x 4096 22.5 us for 23.8).  Not by expert, where that would leave some XCDs
+  // weights meet in one L2 (60 rows of 13000 x 4096 22.5 us for 23.8).  Only where the device holds those too: the ones
+  // without row tiles all fall to the same XCDs, and the others then get more of the rest than they hold (47 rows of
+  // 14336 x 6144, 264 for 246 of them, 56 us for 32).  Not by expert, where that would leave some XCDs
   // more workgroups than others (488 rows of 128 experts 35 us for 25).
   unsigned along = (unsigned)((p.rt_n + p.per - 1) / p.per);
-  if (!a.offsets && p.cols > 1 && along >= 32) along = (along + 7) / 8 * 8;
+  const unsigned even = (along + 7) / 8 * 8;
+  if (!a.offsets && p.cols > 1 && along >= 32 && (int64_t)even * p.cols <= places) along = even;
   const dim3 grid(along, (unsigned)p.y, (unsigned)((p.cols + p.y - 1) / p.y));
   const int lds = p.ks * (g4_x_lds(XT, NV, SX, G) + p.rb * NV * 1024);
   hipLaunchKernelGGL((g4_kernel<XT, NV, SX, G, CHUNKS>), grid, dim3(64 * p.ks), lds, s, a, p);
@@ -653,16 +656,16 @@ static int launch_g4_group(const G4Args& a, hipStream_t s) {
   const int room = (160 * 1024 / 8 - g4_x_lds(XT, 1, 6, G)) / 1024;
   const int rb = chunks ? room : 4;
   p.rb = p.per < rb ? p.per : rb;
-  if (chunks) return sx == 6 ? launch_g4_kernel<XT, 1, 6, G, true>(a, p, s) : launch_g4_kernel<XT, 1, 4, G, true>(a, p, s);
+  if (chunks) return sx == 6 ? launch_g4_kernel<XT, 1, 6, G, true>(a, p, places, s) : launch_g4_kernel<XT, 1, 4, G, true>(a, p, places, s);
   switch (10 * nv + sx) {
-    case 11: return launch_g4_kernel<XT, 1, 1, G>(a, p, s);
-    case 12: return launch_g4_kernel<XT, 1, 2, G>(a, p, s);
-    case 13: return launch_g4_kernel<XT, 1, 3, G>(a, p, s);
-    case 14: return launch_g4_kernel<XT, 1, 4, G>(a, p, s);
-    case 16: return launch_g4_kernel<XT, 1, 6, G>(a, p, s);
-    case 21: return launch_g4_kernel<XT, 2, 1, G>(a, p, s);
-    case 22: return launch_g4_kernel<XT, 2, 2, G>(a, p, s);
-    default: return launch_g4_kernel<XT, 2, 4, G>(a, p, s);
+    case 11: return launch_g4_kernel<XT, 1, 1, G>(a, p, places, s);
+    case 12: return launch_g4_kernel<XT, 1, 2, G>(a, p, places, s);
+    case 13: return launch_g4_kernel<XT, 1, 3, G>(a, p, places, s);
+    case 14: return launch_g4_kernel<XT, 1, 4, G>(a, p, places, s);
+    case 16: return launch_g4_kernel<XT, 1, 6, G>(a, p, places, s);
+    case 21: return launch_g4_kernel<XT, 2, 1, G>(a, p, places, s);
+    case 22: return launch_g4_kernel<XT, 2, 2, G>(a, p, places, s);
+    default: return launch_g4_kernel<XT, 2, 4, G>(a, p, places, s);
   }
 }
 

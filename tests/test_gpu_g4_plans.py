@@ -12,7 +12,7 @@ import torch
 import dequant_matmul_iq4_amd as iq4
 import oracle
 from gpu_util import note
-from rows_util import TYPES, rounder
+from rows_util import TYPES, floats, rounder
 from test_gpu_g4 import grouped, pack, product, weights
 
 pytestmark = pytest.mark.gpu
@@ -148,3 +148,27 @@ def test_a_row_alone_is_the_row_among_few(n, k, group, t):
     for r in range(0, most, 3 if n > 9999 else 1):
         alone = product(p, n, k, group, z, "f16", x[r:r + 1], t, "f32")[0]
         assert all(np.array_equal(y[r], alone) for y in together if r < len(y)), r
+
+
+@pytest.mark.parametrize("n,fewer,k,m", [(14336, 13978, 6144, 47), (9566, 9216, 6144, 66)])
+def test_no_second_round_of_workgroups(n, fewer, k, m):
+    """Sizes whose workgroups just fit the device take little longer than a few row tiles less (1.7 times as long, were some
+    XCDs given more of them than they hold)."""
+    note(f"g4 plans: time of {m} x {n} x {k}")
+    group = 64
+    codes, s, z = weights(1, n, k, group, True, "f16", True)
+    x = floats(np.ones((m, k)), "bf16")
+    y = torch.zeros(m, n, dtype=torch.bfloat16, device="cuda")
+    p = [(r, pack(codes[:r], s[:r], z[:r], group, "f16")) for r in (n, fewer)]
+    times = [[], []]
+    for _ in range(7):
+        for (rows, w), out in zip(p, times):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(10):
+                iq4.iq4_g4_qmv(w, rows, k, group, iq4.IQ4_F16, 1, x, iq4.IQ4_BF16, k, m, y, iq4.IQ4_BF16, rows)
+            b.record()
+            torch.cuda.synchronize()
+            out.append(a.elapsed_time(b) * 100)
+    note("  {:.1f} us, {:.1f} with fewer row tiles".format(*map(min, times)))
+    assert min(times[0]) <= 1.35 * min(times[1])
