@@ -15,9 +15,11 @@
 //               minus infinity): a result that is not finite is made again without this, in 64 bits, by a wave.
 //   binary32 X  two binary16 numbers, the value rounded to eleven bits and what is left, rounded
 //               likewise; a wave has a slice of k, and there a row's values are multiplied by the power
-//               of two that brings the largest to 2^14 .. 2^15, and its sums divided by it.  Within 2^-23
-//               of the value (a tie of what is left), or 2^-39 of the slice's largest (half a step of the
-//               smallest).  Each of the two is a row of the operand; their sums are joined before they are divided.
+//               of two that brings the largest to 2^14 .. 2^15 (what is left by 2^11 more), and its sums divided by it.
+//               Within 2^-23 of the value (a tie of what is left), or 2^-50 of the slice's largest (half a step of the
+//               smallest).  Each of the two is a row of the operand; their sums are divided and joined.  (Without the 2^11
+//               a value in 2^16 times another's shadow lost bits, 2^-39 of the largest, and 4 rows of 2560 x 6144 took 8.0 us
+//               for 8.2; three parts would leave nothing out, and five rows in an operand for eight.)
 //               An infinity's rest is a NaN, and scales near the largest number may take the multiplied sums past
 //               it: again a result that is not finite is made again.
 //
@@ -152,7 +154,8 @@ struct G4Plan {
   int ks;      // waves a workgroup
   int kt_n, rt_n;  // code tiles along k, row tiles
   int per;     // row tiles of W a workgroup
-  int rb;      // row tiles between two joins of the waves' sums: all, or a multiple of four
+  int rb;      // row tiles between two joins of the waves' sums: all, or a multiple of those that a wave loads ahead
+               // (four at most; one where k goes in slices)
   int chunks;  // slices of k one after another (the activations of one are in registers)
 };
 constexpr int kG4StageRow = 128 * 2 + 16;  // a row of 128 binary16 numbers; 16 bytes on, so that rows begin in different banks
@@ -168,9 +171,9 @@ constexpr int g4_x_lds(int xt, int nv, int sx, int group) {
 // memory straight into registers, a row tile ahead.  The waves' sums are joined through LDS in
 // the waves' order.
 // Measured, weights from memory: one binary16 row of 4096 x 4096 5.3 us (1.6 TB/s: the start and one pass of latency),
-// of 14336 x 4096 10.0 (3.0 TB/s); 47 bfloat16 rows of it 22 (X, 262 KB into each CU, then half of the vector
-// issue slots and 18 % of the matrix pipe); 32 binary32 rows of 28 experts of 1536 x 2048 16.5 (2.1 TB/s: offsets, pair ids
-// and rows come before the weights' products); 488 rows of 128 experts of 2048 x 768 24 (3.1 TB/s).
+// of 14336 x 4096 10.1 (3.0 TB/s); 47 bfloat16 rows of it 22 (X, 262 KB into each CU; vector operations for 9 of them, the
+// matrix pipe 18 %, waves wait 40 % of their time); 32 binary32 rows of 28 experts of 1536 x 2048 16.6 (2.1 TB/s: offsets, pair
+// ids and rows come before the weights' products); 488 rows of 128 experts of 2048 x 768 23 (3.3 TB/s; waves wait 56 %).
 template <int XT, int NV, int SX, int G, bool CHUNKS>
 __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
   // all arguments at once: loaded where they are used, one would wait for memory after the other
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
           // 2^(141 - E) for a largest value of exponent field E, at most 2^126
           const uint32_t f = min(268u - (row_max(__float_as_uint(top)) >> 23), 253u);
           scale[v][p] = f << 23;
-          if (c == 0) exps[16 * v + 4 * p + g] = 127 - (int)f;
+          if (c < 2) exps[16 * v + 8 * c + 4 * p + g] = 127 - 11 * c - (int)f;  // (of the rest, 11 less)
         }
 #pragma unroll
       for (int t = 0; t < SX; ++t)
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
               rest[2 * i + 1] = less_hi(x[2 * i + 1], h[i]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m[i] = pack2<kF16>(rest[2 * i], rest[2 * i + 1]);
+            for (int i = 0; i < 4; ++i) m[i] = pack2<kF16>(rest[2 * i] * 0x1p11f, rest[2 * i + 1] * 0x1p11f);
             uint8_t* to = mine + (4 * p + g) * kG4StageRow + 16 * c;
             *reinterpret_cast<u32x4*>(to) = h;
             *reinterpret_cast<u32x4*>(to + 8 * kG4StageRow) = m;
@@ -434,7 +437,10 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
       f32x4 s = acc[v];
       if constexpr (f32) {  // rows 8 .. 15 have what rows 0 .. 7 left
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = __builtin_amdgcn_ldexpf(s[e] + __shfl_xor(s[e], 32), exps[16 * v + 4 * (g & 1) + e]);
+        for (int e = 0; e < 4; ++e) {
+          s[e] = __builtin_amdgcn_ldexpf(s[e], exps[16 * v + 4 * g + e]);
+          s[e] += __shfl_xor(s[e], 32);
+        }
       }
       f32x4* to = part + (rb * NV + v) * 64 + lane;
       if (add) {

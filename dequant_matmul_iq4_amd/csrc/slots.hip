@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(256) dispatch_kernel(SlotArgs a, Pieces pieces
 }
 
 // The same way; the rows of four slots are under way at once.  The rows read bound it: 3256 tokens of
-// 2048, eight rows of 16 bits each, 26 us (4.6 TB/s), of 2047 29, of float32 44; four tokens 3.3.  (Eight, 16-bit rows: the prompt's 31.9 us
-// for 26.1; a workgroup per token, its slots in scalar registers: 28.2, and 52 for rows of 700.)
+// 2048, eight rows of 16 bits each, 24 us (5.0 TB/s), of 2047 29, of float32 44; four tokens 3.3.  (While this way took 26.1:
+// eight slots at once 31.9; a workgroup per token, its slots in scalar registers, 28.2, and 52 for rows of 700.)
 template <int TR, int TO, bool STREAM>
 __global__ void __launch_bounds__(256) combine_rows_kernel(SlotArgs a, Pieces pieces) {
   constexpr int P = kPiece<TR, TO>;
@@ -162,8 +162,8 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // (Rows both read and written bound it: 3256 tokens of 2048, eight rows of 16 bits each, 47 us, 4.8 TB/s.)
-// A workgroup per token: a lane takes every blockDim-th piece of the row, its part of dO from memory once and
-// the rows of eight slots at once; the slots' dots are summed over the lanes in a fixed order.
+// A workgroup per token: a lane takes every blockDim-th piece of the row, its part of dO and the rows of eight
+// slots at once (dO once for every eight slots: twice where top_k is above eight); the slots' dots are summed over the lanes in a fixed order.
 template <int TD, int TR, bool STREAM>
 __global__ void __launch_bounds__(1024) combine_grad_kernel(SlotArgs a, uint32_t pieces) {
   constexpr int P = kPiece<TD, TR>;

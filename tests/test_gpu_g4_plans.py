@@ -88,7 +88,7 @@ def test_by_expert(n, k, m, e):
 @pytest.mark.parametrize("n,k,group,m", [(2100, 4000, 64, 40), (600, 8768, 32, 17), (500, 6528, 128, 300), (1200, 2016, 32, 700)])
 def test_real_inputs(n, k, group, m, t):
     """Sums of k products and of the groups' scalings, each off by at most a step of the magnitudes' sum (of |s| (16 + q) and
-    |s| (16 + z) for bfloat16); a binary32 value by 2^-23 of itself or 2^-39 of its slice's largest."""
+    |s| (16 + z) for bfloat16); a binary32 value by 2^-23 of itself or 2^-50 of its slice's largest."""
     note(f"g4 plans: real {m} x {n} x {k} by {group}, {t}")
     codes, s, z = weights(k, n, k, group, True, "bf16", False)
     rng = np.random.default_rng(m)
@@ -96,7 +96,7 @@ def test_real_inputs(n, k, group, m, t):
     w = oracle.g4_weights(codes, s, z, group)
     want, mags = oracle.g4_product(w, x), oracle.g4_product(abs(w), abs(x))
     got = product(pack(codes, s, z, group, "bf16"), n, k, group, z, "bf16", x, t, "f32")
-    own = 2.0**-23 * mags + 2.0**-39 * abs(x).max(1, keepdims=True) * abs(w).sum(1) if t == "f32" else 0
+    own = 2.0**-23 * mags + 2.0**-50 * abs(x).max(1, keepdims=True) * abs(w).sum(1) if t == "f32" else 0
     if t == "bf16":
         q = np.stack((codes & 15, codes >> 4), 2).reshape(n, k)
         wide = lambda v: np.repeat(v, group, axis=1)[:, :k]  # noqa: E731

@@ -182,6 +182,23 @@ def test_scales_near_the_largest_number(n, k, group, m, t):
     assert np.array_equal(host(y), oracle.g4_product(w, x))
 
 
+@pytest.mark.parametrize("n,k,group,m", ODD)
+def test_a_large_activation_without_a_weight(n, k, group, m):
+    """A column of X 2^26 times the others, whose weights are all zero: the others keep their bits (2^-23 of each, or 2^-50 of
+    the largest, 2^-24 here).  The errors are of either sign, so their norm shows what a sum of bounds would hide."""
+    note(f"extremes: a large activation without a weight, {m} x {n} x {k} by {group}")
+    codes, s, z = weights(n + m, n, k, group, False, "f16", False)
+    rng = np.random.default_rng(k)
+    at = rng.permutation(k // 2)[: 1 + k // 500]  # bytes of two weights each
+    codes[:, at] = 0x88
+    x = rng.standard_normal((m, k)).astype(F).astype(np.float64)
+    x[:, 2 * at] = rng.choice([1, -1], (m, len(at))) * 2.0**26
+    y = torch.full((m, n), -7.0, device="cuda")
+    iq4.iq4_g4_qmv(pack(codes, s, None, group, "f16"), n, k, group, iq4.IQ4_F16, 0, floats(x, "f32"), iq4.IQ4_F32, k, m, y, iq4.IQ4_F32, n)
+    want = oracle.g4_product(oracle.g4_weights(codes, s, None, group), x)
+    assert np.linalg.norm(host(y) - want) <= 1e-6 * np.linalg.norm(want)
+
+
 @pytest.mark.parametrize("what", [np.nan, np.inf])
 @pytest.mark.parametrize("t", list(TYPES))
 def test_rows_that_are_not_finite_cost_no_more_than_many_rows(t, what):
