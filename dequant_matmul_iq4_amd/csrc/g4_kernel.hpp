@@ -526,8 +526,8 @@ __global__ void __launch_bounds__(512) g4_kernel(G4Args a, G4Plan plan) {
       const int v = q % NV;
       const int64_t at = (int64_t)(b + q / NV) * 16 + c;
       if constexpr (XT != kF16) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) odd |= __ballot(!(fabsf(s[e]) < __builtin_inff()) && (f32 ? 8 : 16) * v + 4 * g + e < rows);
+// (four rows without any hold what LDS held; a sum past the largest number only looks in vain)
+        odd |= __ballot((f32 ? 8 : 16) * v + 4 * g < rows && !(fabsf(s[0]) + fabsf(s[1]) + (fabsf(s[2]) + fabsf(s[3])) < __builtin_inff()));
       }
       if (!f32 || g < 2) {
 #pragma unroll
