@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(SlotArgs a, uint32_t
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const TokenSlots s(a, t);
+  const int twice = pieces > 1 ? (int)(pieces * P - a.hidden) : 0;  // what a row's last piece shares with the one before
   const char* dout = row_of<TD>(a.tok, t, a.ldt);
   for (int j0 = 0; j0 < a.top_k; j0 += 8) {
     float dot[8];
@@ -203,8 +204,8 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(SlotArgs a, uint32_t
       if (a.dw) {
         if (c.twice) {  // and counted once (both are zero: a zero times an infinity would not be)
 #pragma unroll
-          for (int e = 0; e < P; ++e) {
-            if (e >= c.twice) continue;
+          for (int e = 0; e < P - 1; ++e) {
+            if (e >= twice) break;
             d[e] = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j][e] = 0.f;
