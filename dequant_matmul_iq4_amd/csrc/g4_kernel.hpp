@@ -18,8 +18,8 @@
 //               of two that brings the largest to 2^14 .. 2^15 (what is left by 2^11 more), and its sums divided by it.
 //               Within 2^-23 of the value (a tie of what is left), or 2^-50 of the slice's largest (half a step of the
 //               smallest).  Each of the two is a row of the operand; their sums are divided and joined.  (Without the 2^11
-//               a value in 2^16 times another's shadow lost bits, 2^-39 of the largest, and 4 rows of 2560 x 6144 took 8.0 us
-//               for 8.2; three parts would leave nothing out, and five rows in an operand for eight.)
+//               a value below 2^-16 of the largest loses bits, 2^-39 of that one, and 4 rows of 2560 x 6144 take 8.0 us
+//               for 8.1; three parts lose nothing, but an operand then has five rows for eight.)
 //               An infinity's rest is a NaN, and scales near the largest number may take the multiplied sums past
 //               it: again a result that is not finite is made again.
 //
